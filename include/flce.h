@@ -266,6 +266,174 @@ FLCE_API size_t flce_jsd_workspace_size(int64_t BT, int64_t Hs, int64_t Ht, int6
  * once with nothing enqueued, device-side ones go to the status word. */
 FLCE_API int32_t flce_fused_linear_jsd(const flce_jsd_args* args, void* stream);
 
+/* ----------------------------------------------------------------------------------
+ * Operators around the head: the (tied) token embedding, the residual-adding RMS norm and
+ * 8-bit activation checkpoints. The pages have no counterpart of them: they are the parts
+ * of a training step that touch what flce_fwd_bwd reads and writes (X, W and the dW
+ * buffer) and what a step keeps between its forward and its backward.
+ *
+ * Common rules. Matrices are row-major with a row pitch `ld*` in ELEMENTS (>= the row's
+ * length) and any element alignment; rows whose base and pitch are multiples of 16 bytes
+ * take wide loads. Row counts may be 0. All calls only enqueue work on `stream` (no
+ * allocation, no synchronisation), return FLCE_ERR_INVALID_ARG / FLCE_ERR_UNSUPPORTED /
+ * FLCE_ERR_WORKSPACE before anything is enqueued, and give the same bits on every run.
+ * Sums, means and norms are held in fp32 (tensor-core accumulators included).
+ *
+ * 8-bit rows ("checkpoint rows"): e4m3 values q [N,H] with one fp32 scale per row and 128
+ * columns, scale [N, cdiv(H,128)] dense; the value is q * scale. flce_ckpt8_pack and the
+ * norm's h8 take scale = the smallest power of two >= 2^-117 with |x| <= 448 scale over the
+ * block's finite elements (1 for a block of zeros), so that the stored value times its
+ * scale is exact in bf16. Infinities and NaN are stored as NaN.
+ * ---------------------------------------------------------------------------------- */
+
+/* out_i = scale * E[tokens_i] (a zero row where tokens_i == ignore_index), and its gradient
+ * dE_v += scale * sum over { i : tokens_i == v } of dout_i, the tokens sorted (stable) and
+ * each row summed in fp32 in a fixed order, then added to dE with one rounding. dE may be
+ * the head's dW of flce_fwd_bwd (tied weights). A token outside [0,V) that is not
+ * ignore_index counts as ignored and sets FLCE_ERR_TARGET_RANGE in the status word. */
+typedef struct flce_embed_args {
+  int64_t N;                /* tokens, >= 0                                              */
+  int64_t H;                /* row length, >= 1                                          */
+  int64_t V;                /* rows of E / dE, >= 1                                      */
+  int32_t dtype;            /* flce_dtype of E, out and dout                             */
+  int32_t dE_dtype;         /* FLCE_F32, or dtype itself; others FLCE_ERR_UNSUPPORTED    */
+  const int64_t* tokens;    /* [N]                                                       */
+  int64_t ignore_index;
+  float scale;              /* finite                                                    */
+  uint32_t flags;           /* backward: FLCE_FLAG_DW_OVERWRITE writes all of dE (zero
+                               rows where no token points) instead of accumulating       */
+  const void* E;            /* [V,H], forward                                            */
+  int64_t ldE;
+  void* out;                /* [N,H], forward                                            */
+  int64_t ldout;
+  const void* dout;         /* [N,H], backward                                           */
+  int64_t lddout;
+  void* dE;                 /* [V,H], backward                                           */
+  int64_t lddE;
+  void* workspace;          /* backward: 256-byte aligned, flce_embed_workspace_size     */
+  size_t workspace_bytes;
+  int32_t* status;          /* device int, reset to 0 by the call, or NULL: not reported  */
+} flce_embed_args;
+
+FLCE_API int32_t flce_embed_fwd(const flce_embed_args* args, void* stream);
+FLCE_API int32_t flce_embed_bwd(const flce_embed_args* args, void* stream);
+/* Workspace bytes of flce_embed_bwd (0 on invalid sizes; N = 0 needs none but gives 256). */
+FLCE_API size_t flce_embed_workspace_size(int64_t N, int64_t H, int64_t V);
+
+/* h = x + residual (fp32; x alone when residual is NULL), rstd = 1 / sqrt(mean(h^2) + eps),
+ * y = h * rstd * (weight + weight_offset). Every output is optional:
+ *   h     rounded to dtype; may be x or residual itself (in place)
+ *   y     rounded to dtype
+ *   y8    e4m3 of u / s with u = h * (weight + weight_offset) and s the checkpoint scale of
+ *         u's block; y8_scale = s * rstd, so that y8 * y8_scale stands for y
+ *   h8    checkpoint row of h (the unrounded sum), for flce_rmsnorm_bwd                    */
+typedef struct flce_rmsnorm_args {
+  int64_t N;                /* rows, >= 0                                                */
+  int64_t H;                /* row length, >= 1                                          */
+  int32_t dtype;            /* flce_dtype of x, residual, weight, h and y                */
+  float eps;                /* > 0, finite                                               */
+  float weight_offset;      /* 0, or 1 for weights stored around zero                    */
+  uint32_t flags;           /* 0                                                         */
+  const void* x;            /* [N,H]                                                     */
+  int64_t ldx;
+  const void* residual;     /* [N,H] or NULL                                             */
+  int64_t ldres;
+  const void* weight;       /* [H]                                                       */
+  void* h;                  /* [N,H] or NULL                                             */
+  int64_t ldh;
+  void* y;                  /* [N,H] or NULL                                             */
+  int64_t ldy;
+  float* rstd;              /* [N] or NULL                                               */
+  void* y8;                 /* [N,H] e4m3 or NULL                                        */
+  int64_t ldy8;
+  float* y8_scale;          /* [N, cdiv(H,128)], with y8                                 */
+  void* h8;                 /* [N,H] e4m3 or NULL                                        */
+  int64_t ldh8;
+  float* h8_scale;          /* [N, cdiv(H,128)], with h8                                 */
+} flce_rmsnorm_args;
+
+/* Gradient: xhat = h * rstd with h either kept (h) or a checkpoint row (h8, h8_scale);
+ * g = dy * (weight + weight_offset);
+ *   dx = rstd * (g - xhat * mean(g * xhat)) + dh      (dh: the residual stream's own
+ *                                                      gradient, NULL for none)
+ *   dweight += sum over rows of dy * xhat
+ * dx is the gradient of x and of residual alike, and may be dy or dh itself. */
+typedef struct flce_rmsnorm_bwd_args {
+  int64_t N;
+  int64_t H;
+  int32_t dtype;            /* flce_dtype of dy, h, dh, weight and dx                    */
+  int32_t dweight_dtype;    /* FLCE_F32 or dtype                                         */
+  float weight_offset;
+  uint32_t flags;           /* FLCE_FLAG_DW_OVERWRITE: dweight is written, not accumulated */
+  const void* dy;           /* [N,H]                                                     */
+  int64_t lddy;
+  const void* h;            /* [N,H], or NULL with h8 given                              */
+  int64_t ldh;
+  const void* h8;           /* [N,H] e4m3, or NULL with h given                          */
+  int64_t ldh8;
+  const float* h8_scale;    /* [N, cdiv(H,128)]                                          */
+  const float* rstd;        /* [N], from the forward                                     */
+  const void* weight;       /* [H]                                                       */
+  const void* dh;           /* [N,H] or NULL                                             */
+  int64_t lddh;
+  void* dx;                 /* [N,H] or NULL: not wanted                                 */
+  int64_t lddx;
+  void* dweight;            /* [H] or NULL: not wanted                                   */
+  void* workspace;          /* with dweight: 256-byte aligned                            */
+  size_t workspace_bytes;   /* >= flce_rmsnorm_workspace_size(N, H)                      */
+} flce_rmsnorm_bwd_args;
+
+FLCE_API int32_t flce_rmsnorm_fwd(const flce_rmsnorm_args* args, void* stream);
+FLCE_API int32_t flce_rmsnorm_bwd(const flce_rmsnorm_bwd_args* args, void* stream);
+/* Workspace bytes of flce_rmsnorm_bwd with a dweight (0 on invalid sizes). */
+FLCE_API size_t flce_rmsnorm_workspace_size(int64_t N, int64_t H);
+
+/* Checkpoint rows of x [N,H]. */
+typedef struct flce_ckpt8_args {
+  int64_t N;
+  int64_t H;
+  int32_t dtype;            /* flce_dtype of x                                           */
+  uint32_t flags;           /* 0                                                         */
+  const void* x;            /* [N,H]                                                     */
+  int64_t ldx;
+  void* q;                  /* [N,H] e4m3                                                */
+  int64_t ldq;              /* a multiple of 16 lets flce_ckpt8_dw take tensor cores     */
+  float* scale;             /* [N, cdiv(H,128)]                                          */
+} flce_ckpt8_args;
+
+FLCE_API int32_t flce_ckpt8_pack(const flce_ckpt8_args* args, void* stream);
+
+/* Weight gradient of a projection y = x W^T from the 8-bit checkpoint of its input:
+ * dW[n,k] += sum_m dy[m,n] * q[m,k] * scale[m, k / 128], without expanding the checkpoint
+ * in memory. q * scale is rounded to dy's 16-bit dtype on the way into the tensor cores:
+ * exact for bf16 with power-of-two scales. For fp16, and for other scales, it is one more
+ * rounding of a value that has 4 significant bits (fp16: saturated at 65504). fp32 dy takes
+ * fp32 FMA kernels and no rounding. The sum is added to dW with one rounding. */
+typedef struct flce_ckpt8_dw_args {
+  int64_t M;                /* rows (tokens), >= 0                                       */
+  int64_t N;                /* output features: columns of dy, rows of dW                */
+  int64_t K;                /* input features: columns of q and dW                       */
+  int32_t dtype;            /* flce_dtype of dy                                          */
+  int32_t dW_dtype;         /* FLCE_F32, or dtype itself; others FLCE_ERR_UNSUPPORTED    */
+  uint32_t flags;           /* FLCE_FLAG_DW_OVERWRITE, FLCE_FLAG_FORCE_SIMT              */
+  uint32_t wait_timeout_ms; /* limit of every pipeline wait; 0 means 4000 ms             */
+  const void* dy;           /* [M,N]                                                     */
+  int64_t lddy;
+  const void* q;            /* [M,K] e4m3                                                */
+  int64_t ldq;
+  const float* scale;       /* [M, cdiv(K,128)]                                          */
+  void* dW;                 /* [N,K]                                                     */
+  int64_t lddW;
+  void* workspace;          /* 256-byte aligned, flce_ckpt8_dw_workspace_size            */
+  size_t workspace_bytes;
+  int32_t* status;          /* device int, reset to 0 by the call, or NULL: a word in the
+                               workspace is used                                         */
+} flce_ckpt8_dw_args;
+
+FLCE_API int32_t flce_ckpt8_dw(const flce_ckpt8_dw_args* args, void* stream);
+/* Workspace bytes of flce_ckpt8_dw (0 on invalid sizes or dtype). */
+FLCE_API size_t flce_ckpt8_dw_workspace_size(int64_t M, int64_t N, int64_t K, int32_t dtype);
+
 /* Size of the fixed device scratch used by flce_fwd_bwd_noalloc (128 MiB). */
 #define FLCE_NOALLOC_SCRATCH_BYTES ((size_t)128 << 20)
 

@@ -16,7 +16,7 @@
 #include <string>
 #include <vector>
 
-#include "flce_internal.cuh"
+#include "flce_ops.cuh"
 
 namespace flce {
 
@@ -153,6 +153,14 @@ static int32_t validate(const flce_args* x) {
 using namespace flce;
 
 static thread_local cudaError_t g_last_cuda_error = cudaSuccess;
+
+namespace flce {
+int32_t cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return FLCE_OK;
+  g_last_cuda_error = e;
+  return FLCE_ERR_CUDA;
+}
+}  // namespace flce
 
 extern "C" const char* flce_last_cuda_error(void) { return cudaGetErrorName(g_last_cuda_error); }
 

@@ -31,7 +31,11 @@ EXPORTED = ("flce_workspace_size", "flce_chunk_rows", "flce_fwd_bwd", "flce_fwd_
             "flce_profile_create", "flce_profile_reset", "flce_profile_destroy",
             "flce_profile_read", "flce_last_cuda_error", "flce_status_string", "flce_abi_version",
             "flce_jsd_workspace_size", "flce_fused_linear_jsd", "flce_scale_by",
-            "flce_plan_describe")
+            "flce_plan_describe",
+            "flce_embed_fwd", "flce_embed_bwd", "flce_embed_workspace_size",
+            "flce_rmsnorm_fwd", "flce_rmsnorm_bwd", "flce_rmsnorm_workspace_size",
+            "flce_ckpt8_pack", "flce_ckpt8_dw", "flce_ckpt8_dw_workspace_size")
+Q_BLOCK = 128  # columns of an 8-bit row that share a scale
 STAGES = ("prologue", "gather", "fwd", "finalize", "gpass", "dx", "dw", "reduce", "bwd")
 
 
@@ -68,6 +72,66 @@ class FlceJsdArgs(ctypes.Structure):
         ("dW", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
         ("status", ctypes.c_void_p), ("wait_timeout_ms", ctypes.c_uint32),
         ("profile", ctypes.c_void_p),
+    ]
+
+
+class FlceEmbedArgs(ctypes.Structure):
+    """Mirror of ``flce_embed_args``."""
+    _fields_ = [
+        ("N", ctypes.c_int64), ("H", ctypes.c_int64), ("V", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("dE_dtype", ctypes.c_int32),
+        ("tokens", ctypes.c_void_p), ("ignore_index", ctypes.c_int64),
+        ("scale", ctypes.c_float), ("flags", ctypes.c_uint32),
+        ("E", ctypes.c_void_p), ("ldE", ctypes.c_int64), ("out", ctypes.c_void_p), ("ldout", ctypes.c_int64),
+        ("dout", ctypes.c_void_p), ("lddout", ctypes.c_int64), ("dE", ctypes.c_void_p), ("lddE", ctypes.c_int64),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p),
+    ]
+
+
+class FlceRmsnormArgs(ctypes.Structure):
+    """Mirror of ``flce_rmsnorm_args``."""
+    _fields_ = [
+        ("N", ctypes.c_int64), ("H", ctypes.c_int64), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float), ("flags", ctypes.c_uint32),
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("residual", ctypes.c_void_p), ("ldres", ctypes.c_int64),
+        ("weight", ctypes.c_void_p), ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+        ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("rstd", ctypes.c_void_p),
+        ("y8", ctypes.c_void_p), ("ldy8", ctypes.c_int64), ("y8_scale", ctypes.c_void_p),
+        ("h8", ctypes.c_void_p), ("ldh8", ctypes.c_int64), ("h8_scale", ctypes.c_void_p),
+    ]
+
+
+class FlceRmsnormBwdArgs(ctypes.Structure):
+    """Mirror of ``flce_rmsnorm_bwd_args``."""
+    _fields_ = [
+        ("N", ctypes.c_int64), ("H", ctypes.c_int64), ("dtype", ctypes.c_int32), ("dweight_dtype", ctypes.c_int32),
+        ("weight_offset", ctypes.c_float), ("flags", ctypes.c_uint32),
+        ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+        ("h8", ctypes.c_void_p), ("ldh8", ctypes.c_int64), ("h8_scale", ctypes.c_void_p),
+        ("rstd", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+        ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dweight", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class FlceCkpt8Args(ctypes.Structure):
+    """Mirror of ``flce_ckpt8_args``."""
+    _fields_ = [
+        ("N", ctypes.c_int64), ("H", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+        ("scale", ctypes.c_void_p),
+    ]
+
+
+class FlceCkpt8DwArgs(ctypes.Structure):
+    """Mirror of ``flce_ckpt8_dw_args``."""
+    _fields_ = [
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("dW_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
+        ("wait_timeout_ms", ctypes.c_uint32),
+        ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+        ("scale", ctypes.c_void_p), ("dW", ctypes.c_void_p), ("lddW", ctypes.c_int64),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p),
     ]
 
 
@@ -108,6 +172,18 @@ def load(path: str | None = None):
     lib.flce_jsd_workspace_size.argtypes = [ctypes.c_int64] * 4 + [ctypes.c_int32, ctypes.c_size_t]
     lib.flce_fused_linear_jsd.restype = ctypes.c_int32
     lib.flce_fused_linear_jsd.argtypes = [ctypes.POINTER(FlceJsdArgs), ctypes.c_void_p]
+    for name, args in (("embed_fwd", FlceEmbedArgs), ("embed_bwd", FlceEmbedArgs),
+                       ("rmsnorm_fwd", FlceRmsnormArgs), ("rmsnorm_bwd", FlceRmsnormBwdArgs),
+                       ("ckpt8_pack", FlceCkpt8Args), ("ckpt8_dw", FlceCkpt8DwArgs)):
+        fn = getattr(lib, "flce_" + name)
+        fn.restype = ctypes.c_int32
+        fn.argtypes = [ctypes.POINTER(args), ctypes.c_void_p]
+    lib.flce_embed_workspace_size.restype = ctypes.c_size_t
+    lib.flce_embed_workspace_size.argtypes = [ctypes.c_int64] * 3
+    lib.flce_rmsnorm_workspace_size.restype = ctypes.c_size_t
+    lib.flce_rmsnorm_workspace_size.argtypes = [ctypes.c_int64] * 2
+    lib.flce_ckpt8_dw_workspace_size.restype = ctypes.c_size_t
+    lib.flce_ckpt8_dw_workspace_size.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int32]
     lib.flce_profile_create.restype = ctypes.c_void_p
     lib.flce_profile_create.argtypes = []
     lib.flce_profile_reset.restype = None
@@ -355,3 +431,316 @@ def scale_by(x, g, stream=None):
 def raw_call(args: FlceArgs, stream_handle: int) -> int:
     """Call flce_fwd_bwd with a prepared FlceArgs (for callers that manage every buffer)."""
     return int(load().flce_fwd_bwd(ctypes.byref(args), ctypes.c_void_p(stream_handle)))
+
+
+# ---------------------------------------------------------------------------------------
+# Operators around the head: embedding, residual RMS norm, 8-bit checkpoints
+# ---------------------------------------------------------------------------------------
+
+def _matrix(name, t, rows, cols, dtype, dev):
+    """Checks a [rows, cols] CUDA matrix of unit column stride; returns (pointer, row pitch)."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (rows, cols) or t.device != dev:
+        raise ValueError(f"{name} must be [{rows}, {cols}] on {dev}, got {tuple(t.shape)} on {t.device}")
+    ld, inner = t.stride()
+    if rows <= 1:
+        ld = cols if rows == 0 else max(ld, cols)
+    if (inner != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap, got strides {t.stride()}")
+    return t.data_ptr(), ld
+
+
+def _vector(name, t, n, dtype, dev):
+    if t.dtype != dtype or t.shape != (n,) or t.device != dev or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a dense {dtype} vector of {n} on {dev}, got {t.dtype} {tuple(t.shape)} "
+                         f"strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def _dense(name, t, rows, cols, dev):
+    """Checks a dense fp32 [rows, cols] (block scales)."""
+    if t.dtype != torch.float32 or t.shape != (rows, cols) or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be dense fp32 [{rows}, {cols}] on {dev}")
+    return t.data_ptr()
+
+
+def _cuda_2d(name, t):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
+    if t.dtype not in DTYPES:
+        raise ValueError(f"{name} must be fp32, bf16 or fp16, got {t.dtype}")
+    return t.device
+
+
+def empty_rows8(N, H, device):
+    """An [N, H] e4m3 tensor whose rows start at multiples of 16 bytes."""
+    p = (H + 15) & ~15
+    t = torch.empty(N, p, dtype=torch.float8_e4m3fn, device=device)
+    return t if p == H else t[:, :H]
+
+
+def _scales(N, H, device):
+    return torch.empty(N, (H + Q_BLOCK - 1) // Q_BLOCK, dtype=torch.float32, device=device)
+
+
+def _launch(fn, where, args, dev, stream, used):
+    """Enqueue on `stream` (None: the current one). Tensors used on a stream other than the
+    current one are recorded on it, so that the allocator does not hand their memory out
+    before the kernels are done."""
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        handle = stream.cuda_stream
+        for t in used:
+            if t is not None:
+                t.record_stream(stream)
+    if dev.index == torch.cuda.current_device():
+        rc = fn(args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(args, handle)
+    if rc != FLCE_OK:
+        raise FlceError(rc, where)
+    return handle
+
+
+def _finish(o, lib, check, handle):
+    if check:
+        o["status_code"] = int(lib.flce_get_status(o["status"].data_ptr(), None, handle))
+    return o
+
+
+def embed_fwd(tokens, E, *, scale=1.0, ignore_index=-100, out=None, status=None, check=True, stream=None):
+    """out[i] = scale * E[tokens[i]], a zero row where tokens[i] == ignore_index.
+
+    tokens int64 [N], E [V, H] (fp32, bf16 or fp16; unit column stride). Returns a dict with
+    out and, when ``check`` is set (which synchronises the stream), status_code: a token
+    outside [0, V) gives a zero row and FLCE_ERR_TARGET_RANGE. ``status`` (int32 [1]) receives
+    the device status word without a check.
+    """
+    lib = load()
+    dev = _cuda_2d("E", E)
+    V, H = E.shape
+    N = tokens.shape[0]
+    if out is None:
+        out = torch.empty(N, H, dtype=E.dtype, device=dev)
+    o = {"out": out}
+    if status is None and check:
+        status = torch.empty(1, dtype=torch.int32, device=dev)
+    if status is not None:
+        o["status"] = status
+    pE, ldE = _matrix("E", E, V, H, E.dtype, dev)
+    po, ldo = _matrix("out", out, N, H, E.dtype, dev)
+    a = FlceEmbedArgs(N, H, V, DTYPES[E.dtype], 0, _vector("tokens", tokens, N, torch.int64, dev), ignore_index,
+                      scale, 0, pE, ldE, po, ldo, None, 0, None, 0, None, 0,
+                      None if status is None else _vector("status", status, 1, torch.int32, dev))
+    h = _launch(lib.flce_embed_fwd, "flce_embed_fwd", a, dev, stream, (tokens, E, out, status))
+    return _finish(o, lib, check, h)
+
+
+def embed_bwd(tokens, dout, *, V=None, dE=None, scale=1.0, ignore_index=-100, workspace=None, flags=0, status=None,
+              check=True, stream=None):
+    """dE[v] += scale * sum of the rows of dout whose token is v, in fp32 and in a fixed order.
+
+    dout [N, H]; dE [V, H] in fp32 or dout's dtype, accumulated into (FLAG_DW_OVERWRITE: all of
+    it is written), for instance the head's own dW of a tied embedding. Without dE a new fp32
+    one of ``V`` rows is written. Returns a dict with dE (and status_code when ``check``).
+    """
+    lib = load()
+    dev = _cuda_2d("dout", dout)
+    N, H = dout.shape
+    if dE is None:
+        if V is None:
+            raise ValueError("embed_bwd needs V or dE")
+        dE = torch.empty(V, H, dtype=torch.float32, device=dev)
+        flags |= FLAG_DW_OVERWRITE
+    V = dE.shape[0]
+    if dE.dtype not in DTYPES:
+        raise ValueError(f"dE must be fp32, bf16 or fp16, got {dE.dtype}")
+    nbytes = int(lib.flce_embed_workspace_size(N, H, V))
+    workspace = _workspace(workspace, nbytes, dev, stream)
+    o = {"dE": dE, "workspace": workspace}
+    if status is None and check:
+        status = torch.empty(1, dtype=torch.int32, device=dev)
+    if status is not None:
+        o["status"] = status
+    pd, ldd = _matrix("dout", dout, N, H, dout.dtype, dev)
+    pE, ldE = _matrix("dE", dE, V, H, dE.dtype, dev)
+    a = FlceEmbedArgs(N, H, V, DTYPES[dout.dtype], DTYPES[dE.dtype], _vector("tokens", tokens, N, torch.int64, dev),
+                      ignore_index, scale, flags, None, 0, None, 0, pd, ldd, pE, ldE,
+                      workspace.data_ptr(), workspace.numel(),
+                      None if status is None else _vector("status", status, 1, torch.int32, dev))
+    h = _launch(lib.flce_embed_bwd, "flce_embed_bwd", a, dev, stream, (tokens, dout, dE, workspace, status))
+    return _finish(o, lib, check, h)
+
+
+def _workspace(ws, nbytes, dev, stream):
+    """The caller's byte workspace, or a new one owned by the stream that uses it."""
+    if ws is not None:
+        if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev:
+            raise ValueError(f"workspace must be a dense uint8 tensor on {dev}")
+        return ws
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
+def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, weight_offset=0.0, want_y=True, want_h=None, want_y8=False,
+                want_h8=False, outputs=None, stream=None):
+    """h = x + residual, y = h * rstd * (weight + weight_offset), rstd = 1/sqrt(mean(h^2) + eps).
+
+    x and residual [N, H], weight [H], one dtype (fp32, bf16 or fp16). Returns a dict with rstd
+    and, as wanted: y; h (default: when a residual is given); y8, y8_scale (the 8-bit output);
+    h8, h8_scale (8-bit checkpoint of h for ``rmsnorm_bwd``). ``outputs`` may carry preallocated
+    tensors under the same keys; h may be x or residual itself.
+    """
+    lib = load()
+    dev = _cuda_2d("x", x)
+    N, H = x.shape
+    dt = x.dtype
+    o = dict(outputs) if outputs else {}
+    if want_h is None:
+        want_h = residual is not None
+    pr, ldr = (None, 0) if residual is None else _matrix("residual", residual, N, H, dt, dev)
+    px, ldx = _matrix("x", x, N, H, dt, dev)
+    y = h = y8 = h8 = None
+    py = ph = py8 = ph8 = psy = psh = None
+    ldy = ldh = ldy8 = ldh8 = 0
+    if o.get("rstd") is None:
+        o["rstd"] = torch.empty(N, dtype=torch.float32, device=dev)
+    if want_y:
+        y = o.get("y")
+        if y is None:
+            y = o["y"] = torch.empty(N, H, dtype=dt, device=dev)
+        py, ldy = _matrix("y", y, N, H, dt, dev)
+    if want_h:
+        h = o.get("h")
+        if h is None:
+            h = o["h"] = torch.empty(N, H, dtype=dt, device=dev)
+        ph, ldh = _matrix("h", h, N, H, dt, dev)
+    if want_y8:
+        y8, psy = _rows8(o, "y8", N, H, dev)
+        py8, ldy8 = _matrix("y8", y8, N, H, torch.float8_e4m3fn, dev)
+    if want_h8:
+        h8, psh = _rows8(o, "h8", N, H, dev)
+        ph8, ldh8 = _matrix("h8", h8, N, H, torch.float8_e4m3fn, dev)
+    a = FlceRmsnormArgs(N, H, DTYPES[dt], eps, weight_offset, 0, px, ldx, pr, ldr, _vector("weight", weight, H, dt, dev),
+                        ph, ldh, py, ldy, _vector("rstd", o["rstd"], N, torch.float32, dev), py8, ldy8, psy, ph8, ldh8,
+                        psh)
+    _launch(lib.flce_rmsnorm_fwd, "flce_rmsnorm_fwd", a, dev, stream,
+            (x, residual, weight, y, h, y8, h8, o["rstd"], o.get("y8_scale"), o.get("h8_scale")))
+    return o
+
+
+def _rows8(o, key, N, H, dev):
+    """The 8-bit rows o[key] and the pointer of their scales o[key + "_scale"], made if absent."""
+    if o.get(key) is None:
+        o[key] = empty_rows8(N, H, dev)
+    sk = "scale" if key == "q" else key + "_scale"
+    if o.get(sk) is None:
+        o[sk] = _scales(N, H, dev)
+    return o[key], _dense(sk, o[sk], N, (H + Q_BLOCK - 1) // Q_BLOCK, dev)
+
+
+def rmsnorm_bwd(dy, weight, rstd, h=None, *, h8=None, h8_scale=None, dh=None, weight_offset=0.0, want_dx=True,
+                want_dweight=True, dweight=None, workspace=None, outputs=None, flags=0, stream=None):
+    """Gradient of ``rmsnorm_fwd``: dx (of x and residual alike; with ``dh``, the residual
+    stream's own gradient, added) and dweight, accumulated into when given (fp32 or dy's dtype;
+    FLAG_DW_OVERWRITE: written), else a new fp32 vector. The norm's input is ``h`` or its 8-bit
+    checkpoint ``h8, h8_scale``. Returns a dict with dx and dweight."""
+    lib = load()
+    dev = _cuda_2d("dy", dy)
+    N, H = dy.shape
+    dt = dy.dtype
+    if (h is None) == (h8 is None) or (h8 is not None and h8_scale is None):
+        raise ValueError("rmsnorm_bwd takes h, or h8 with h8_scale")
+    o = dict(outputs) if outputs else {}
+    pdx, lddx = None, 0
+    if want_dx:
+        if o.get("dx") is None:
+            o["dx"] = torch.empty(N, H, dtype=dt, device=dev)
+        pdx, lddx = _matrix("dx", o["dx"], N, H, dt, dev)
+    pw = pws = None
+    wbytes, wdt = 0, 0
+    if want_dweight:
+        if dweight is None:
+            dweight = torch.empty(H, dtype=torch.float32, device=dev)
+            flags |= FLAG_DW_OVERWRITE
+        if dweight.dtype not in DTYPES:
+            raise ValueError(f"dweight must be fp32, bf16 or fp16, got {dweight.dtype}")
+        pw, wdt = _vector("dweight", dweight, H, dweight.dtype, dev), DTYPES[dweight.dtype]
+        workspace = _workspace(workspace, int(lib.flce_rmsnorm_workspace_size(N, H)), dev, stream)
+        pws, wbytes = workspace.data_ptr(), workspace.numel()
+        o["dweight"], o["workspace"] = dweight, workspace
+    else:
+        workspace = None
+    ph, ldh = (None, 0) if h is None else _matrix("h", h, N, H, dt, dev)
+    p8 = ps8 = None
+    ld8 = 0
+    if h8 is not None:
+        p8, ld8 = _matrix("h8", h8, N, H, torch.float8_e4m3fn, dev)
+        ps8 = _dense("h8_scale", h8_scale, N, (H + Q_BLOCK - 1) // Q_BLOCK, dev)
+    pdh, lddh = (None, 0) if dh is None else _matrix("dh", dh, N, H, dt, dev)
+    pdy, lddy = _matrix("dy", dy, N, H, dt, dev)
+    a = FlceRmsnormBwdArgs(N, H, DTYPES[dt], wdt, weight_offset, flags, pdy, lddy, ph, ldh, p8, ld8, ps8,
+                           _vector("rstd", rstd, N, torch.float32, dev), _vector("weight", weight, H, dt, dev),
+                           pdh, lddh, pdx, lddx, pw, pws, wbytes)
+    _launch(lib.flce_rmsnorm_bwd, "flce_rmsnorm_bwd", a, dev, stream,
+            (dy, weight, rstd, h, h8, h8_scale, dh, dweight, workspace, o.get("dx")))
+    return o
+
+
+def ckpt8_pack(x, *, outputs=None, stream=None):
+    """8-bit checkpoint of x [N, H]: a dict with q (e4m3 [N, H], rows at multiples of 16 bytes)
+    and scale (fp32 [N, ceil(H/128)], powers of two); the value kept is q * scale."""
+    lib = load()
+    dev = _cuda_2d("x", x)
+    N, H = x.shape
+    o = dict(outputs) if outputs else {}
+    q, ps = _rows8(o, "q", N, H, dev)
+    px, ldx = _matrix("x", x, N, H, x.dtype, dev)
+    pq, ldq = _matrix("q", q, N, H, torch.float8_e4m3fn, dev)
+    _launch(lib.flce_ckpt8_pack, "flce_ckpt8_pack", FlceCkpt8Args(N, H, DTYPES[x.dtype], 0, px, ldx, pq, ldq, ps), dev,
+            stream, (x, q, o["scale"]))
+    return o
+
+
+def ckpt8_dw(dy, q, scale, *, dW=None, workspace=None, flags=0, wait_timeout_ms=0, status=None, check=True,
+             stream=None):
+    """Weight gradient of y = x W^T from the 8-bit checkpoint of x: dW += dy^T (q * scale).
+
+    dy [M, N] (fp32, bf16 or fp16), q e4m3 [M, K], scale fp32 [M, ceil(K/128)]; dW [N, K] in
+    fp32 or dy's dtype, accumulated into (FLAG_DW_OVERWRITE: written), else a new fp32 one.
+    Returns a dict with dW (and status_code when ``check``, which synchronises the stream).
+    """
+    lib = load()
+    dev = _cuda_2d("dy", dy)
+    M, N = dy.shape
+    if q.dim() != 2:
+        raise ValueError(f"q must be 2-D, got {tuple(q.shape)}")
+    K = q.shape[1]
+    if dW is None:
+        dW = torch.empty(N, K, dtype=torch.float32, device=dev)
+        flags |= FLAG_DW_OVERWRITE
+    if dW.dtype not in DTYPES:
+        raise ValueError(f"dW must be fp32, bf16 or fp16, got {dW.dtype}")
+    dt = DTYPES[dy.dtype]
+    workspace = _workspace(workspace, int(lib.flce_ckpt8_dw_workspace_size(M, N, K, dt)), dev, stream)
+    o = {"dW": dW, "workspace": workspace}
+    if status is None and check:
+        status = torch.empty(1, dtype=torch.int32, device=dev)
+    if status is not None:
+        o["status"] = status
+    pdy, lddy = _matrix("dy", dy, M, N, dy.dtype, dev)
+    pq, ldq = _matrix("q", q, M, K, torch.float8_e4m3fn, dev)
+    pW, ldW = _matrix("dW", dW, N, K, dW.dtype, dev)
+    a = FlceCkpt8DwArgs(M, N, K, dt, DTYPES[dW.dtype], flags, wait_timeout_ms, pdy, lddy, pq, ldq,
+                        _dense("scale", scale, M, (K + Q_BLOCK - 1) // Q_BLOCK, dev), pW, ldW,
+                        workspace.data_ptr(), workspace.numel(),
+                        None if status is None else _vector("status", status, 1, torch.int32, dev))
+    h = _launch(lib.flce_ckpt8_dw, "flce_ckpt8_dw", a, dev, stream, (dy, q, scale, dW, workspace, status))
+    return _finish(o, lib, check, h)

@@ -1,0 +1,197 @@
+"""GPU tests of 8-bit checkpoint rows and of the weight gradient that reads them.
+
+Packing is compared bit for bit with the float64 oracle. Bounds of the product over M rows:
+fp32 FMA kernels add M products, each sum rounded to 2^-24 relative; the tensor cores may
+truncate (2^-23) each addition of 16 products: M * 2^-23 * sum|dy x| covers both. An expanded
+value that is not exact in dy's 16-bit type adds a half ulp of it per product. Over all elements
+the relative error (2-norm) of an fp32 result is held to 1e-5, as for the other fp32 results of
+this package."""
+
+import numpy as np
+import pytest
+import torch
+
+from linear_cross_entropy_logits_gb300 import build as B
+from linear_cross_entropy_logits_gb300 import flce
+from oracle import ops_oracle as oo
+from ops_util import DT, FLOOR, ULP, close, np64, odd_rows, strided
+from parity_util import rel_fro
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    B.build()
+    flce.load()
+
+
+def _rows(N, H, dt, seed, spread=3.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(N, H, generator=g) * torch.exp(spread * torch.randn(N, 1, generator=g))
+    x[:, ::29] *= 20
+    return x.to(DT[dt])
+
+
+@pytest.mark.parametrize("N,H,dt,extra,offset", [
+    (1, 1, "f32", 0, 0), (1, 128, "bf16", 0, 0), (3, 129, "f16", 0, 0), (50, 4096, "bf16", 0, 0), (7, 1336, "f16", 0, 0),
+    (9, 1000, "f32", 0, 0), (5, 20001, "bf16", 0, 0), (33, 200, "bf16", 3, 1), (33, 200, "f32", 4, 4), (1000, 77, "bf16", 0, 0),
+    (16, 136, "f16", 8, 8)])
+def test_pack(N, H, dt, extra, offset):
+    x = _rows(N, H, dt, N + H)
+    o = {"q": odd_rows(N, H, torch.float8_e4m3fn, extra, offset)} if extra else None
+    o = flce.ckpt8_pack(strided(x.cuda(), extra, offset), outputs=o)
+    q, s = oo.pack(np64(x))
+    assert np.array_equal(np64(o["q"]), q) and np.array_equal(np64(o["scale"]), s)
+
+
+def test_pack_extremes():
+    """Blocks of zeros, of the type's largest and smallest values, and with non-finite values."""
+    fi = torch.finfo(torch.float32)
+    x = torch.randn(8, 256)
+    x[0] = 0
+    x[1] = fi.max
+    x[2] = -fi.tiny / 8
+    x[3, 5] = float("inf")
+    x[4, 130:] = float("nan")
+    x[5] *= 1e-30
+    x[6, :128] = 448.0
+    x[6, 128:] = 449.0
+    x[7, :] = float("-inf")
+    o = flce.ckpt8_pack(x.cuda())
+    q, s = oo.pack(np64(x))
+    assert np.array_equal(np64(o["q"]), q, equal_nan=True) and np.array_equal(np64(o["scale"]), s)
+    assert np64(o["scale"])[6].tolist() == [1.0, 2.0] and np64(o["scale"])[7].tolist() == [1.0, 1.0]
+
+
+def test_pack_nothing():
+    o = flce.ckpt8_pack(torch.empty(0, 40, device="cuda"))
+    assert o["q"].shape == (0, 40) and o["scale"].shape == (0, 1)
+
+
+def _dw_bound(dy, x, M, dt, wdt, total, base, inexact):
+    mag = np.abs(dy).T @ np.abs(x)
+    b = M * 2.0 ** -23 * mag + 2 * ULP[wdt] * np.abs(total) + 2.0 ** -23 * np.abs(base) + FLOOR[wdt]
+    return b + (ULP[dt] * mag if inexact else 0.0)
+
+
+DW = [(1, 1, 1, "f32", "f32"), (1, 8, 16, "bf16", "f32"), (1, 300, 520, "bf16", "bf16"), (63, 64, 128, "f16", "f32"),
+      (64, 256, 256, "bf16", "f32"), (65, 264, 272, "bf16", "f32"), (200, 257, 133, "bf16", "f32"),
+      (130, 520, 1336, "f16", "f16"), (1000, 136, 400, "f32", "f32"), (777, 72, 2000, "bf16", "bf16"),
+      (2049, 512, 640, "bf16", "f32"), (5000, 256, 384, "bf16", "f32"), (4100, 264, 300, "f16", "f32"),
+      (300, 1030, 90, "f32", "f32"), (129, 2000, 31, "f16", "f32")]
+
+
+@pytest.mark.parametrize("M,N,K,dt,wdt", DW)
+@pytest.mark.parametrize("accumulate", [True, False])
+@pytest.mark.parametrize("simt", [False, True])
+def test_dw(M, N, K, dt, wdt, accumulate, simt):
+    g = torch.Generator().manual_seed(M + N + K)
+    dy = (torch.randn(M, N, generator=g) * 0.3).to(DT[dt])
+    p = flce.ckpt8_pack(_rows(M, K, dt, M + K, 1.0).cuda())
+    x = np64(p["q"]) * oo.spread(np64(p["scale"]), K)
+    init = torch.randn(N, K, generator=g).to(DT[wdt]) if accumulate else torch.full((N, K), float("nan"), dtype=DT[wdt])
+    dW = init.clone().cuda()
+    o = flce.ckpt8_dw(dy.cuda(), p["q"], p["scale"], dW=dW, flags=(0 if accumulate else flce.FLAG_DW_OVERWRITE)
+                      | (flce.FLAG_FORCE_SIMT if simt else 0))
+    assert o["status_code"] == flce.FLCE_OK
+    base = np64(init) if accumulate else np.zeros((N, K))
+    want = np64(dy).T @ x
+    total = want + base
+    close(dW, total, _dw_bound(np64(dy), x, M, dt, wdt, total, base, dt == "f16" and not simt))
+    if wdt == "f32" and dt != "f16":
+        assert rel_fro(np64(dW), total) <= 1e-5
+
+
+def test_dw_long_sum_keeps_fp32():
+    """16384 rows of one sign: the sum's error grows with the rows summed without a rounding
+    to nearest, which the kernel bounds."""
+    g = torch.Generator().manual_seed(1)
+    M, N, K = 16384, 256, 256
+    dy = (1 + 0.1 * torch.rand(M, N, generator=g)).bfloat16().cuda()
+    p = flce.ckpt8_pack((1 + torch.rand(M, K, generator=g)).bfloat16().cuda())
+    want = dy.double().t() @ (p["q"].double() * p["scale"].double().repeat_interleave(128, dim=1))
+    got = flce.ckpt8_dw(dy, p["q"], p["scale"])["dW"]
+    assert rel_fro(np64(got), np64(want)) <= 1e-5
+
+
+@pytest.mark.parametrize("extra,offset", [(8, 8), (3, 1), (16, 0)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_dw_strides(dt, extra, offset):
+    M, N, K = 300, 136, 272
+    g = torch.Generator().manual_seed(2)
+    dy = torch.randn(M, N, generator=g).to(DT[dt]).cuda()
+    p = flce.ckpt8_pack(_rows(M, K, dt, 3, 1.0).cuda())
+    want = flce.ckpt8_dw(dy, p["q"], p["scale"])["dW"]
+    dW = strided(torch.zeros(N, K, device="cuda"), extra, offset)
+    flce.ckpt8_dw(strided(dy, extra, offset), strided(p["q"], extra, offset), p["scale"], dW=dW)
+    x = np64(p["q"]) * oo.spread(np64(p["scale"]), K)
+    ref = np64(dy).T @ x
+    close(dW, ref, _dw_bound(np64(dy), x, M, dt, "f32", ref, 0 * ref, False))
+    close(want, ref, _dw_bound(np64(dy), x, M, dt, "f32", ref, 0 * ref, False))
+
+
+def test_dw_scales_that_are_no_powers_of_two():
+    """The norm's 8-bit output as the projection's input."""
+    M, N, K = 500, 128, 384
+    x = _rows(M, K, "bf16", 6, 0.5).cuda()
+    w = (1 + 0.2 * torch.randn(K, generator=torch.Generator().manual_seed(3))).bfloat16().cuda()
+    o = flce.rmsnorm_fwd(x, w, want_y8=True)
+    dy = torch.randn(M, N, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    got = flce.ckpt8_dw(dy, o["y8"], o["y8_scale"])["dW"]
+    xs = np64(o["y8"]) * oo.spread(np64(o["y8_scale"]), K)
+    want = np64(dy).T @ xs
+    close(got, want, _dw_bound(np64(dy), xs, M, "bf16", "f32", want, 0 * want, True))
+
+
+def test_dw_non_finite_rows_stay_in_their_columns():
+    M, N, K = 70, 64, 256
+    x = torch.randn(M, K)
+    x[3, 17] = float("inf")
+    x[60, 200] = float("nan")
+    dy = torch.randn(M, N)
+    dy[5, 9] = float("nan")
+    p = flce.ckpt8_pack(x.bfloat16().cuda())
+    dW = flce.ckpt8_dw(dy.bfloat16().cuda(), p["q"], p["scale"])["dW"].cpu()
+    bad = torch.zeros(N, K, dtype=torch.bool)
+    bad[:, 17] = bad[:, 200] = True
+    bad[9] = True
+    assert torch.equal(torch.isnan(dW), bad)
+
+
+def test_dw_no_rows():
+    dy, q, s = torch.empty(0, 8, device="cuda"), torch.empty(0, 16, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(0, 1, device="cuda")
+    dW = torch.ones(8, 16, device="cuda")
+    flce.ckpt8_dw(dy, q, s, dW=dW)
+    assert torch.all(dW == 1)
+    assert torch.all(flce.ckpt8_dw(dy, q, s)["dW"] == 0)
+
+
+def test_dw_is_the_derivative_of_the_projection():
+    """Central differences of L(W) = sum(c * x W^T), linear in W, over a step of 1."""
+    M, N, K = 90, 6, 40
+    g = torch.Generator().manual_seed(7)
+    p = flce.ckpt8_pack(torch.randn(M, K, generator=g).cuda())
+    x = np64(p["q"]) * oo.spread(np64(p["scale"]), K)
+    c, W = np.asarray(torch.randn(M, N, generator=g).double()), np.asarray(torch.randn(N, K, generator=g).double())
+    dW = np64(flce.ckpt8_dw(torch.from_numpy(c).float().cuda(), p["q"], p["scale"])["dW"])
+    for n, k in [(0, 0), (5, 39), (2, 20)]:
+        Wp, Wm = W.copy(), W.copy()
+        Wp[n, k] += 1
+        Wm[n, k] -= 1
+        diff = ((c * (x @ Wp.T)).sum() - (c * (x @ Wm.T)).sum()) / 2
+        assert abs(diff - dW[n, k]) <= 1e-4
+
+
+def test_dw_same_bits_and_side_stream():
+    g = torch.Generator().manual_seed(8)
+    p = flce.ckpt8_pack(torch.randn(3000, 520, generator=g).bfloat16().cuda())
+    dy = torch.randn(3000, 264, generator=g).bfloat16().cuda()
+    a = flce.ckpt8_dw(dy, p["q"], p["scale"])["dW"]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    b = flce.ckpt8_dw(dy, p["q"], p["scale"], stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert b["status_code"] == flce.FLCE_OK and torch.equal(a, b["dW"])

@@ -1,0 +1,224 @@
+"""Host-side checks of the embedding, RMS norm and 8-bit checkpoint operators: their structs
+match the header, their refusals come before any CUDA call, the binding's argument checks, and
+the oracles they are tested against (the oracle's gradients against differences)."""
+
+import ctypes
+import os
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+from linear_cross_entropy_logits_gb300 import build as B
+from linear_cross_entropy_logits_gb300 import flce
+from oracle import ops_oracle as oo
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+BAD, UNS, WS = flce.FLCE_ERR_INVALID_ARG, flce.FLCE_ERR_UNSUPPORTED, flce.FLCE_ERR_WORKSPACE
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return flce.load()
+
+
+STRUCTS = [(flce.FlceEmbedArgs, "flce_embed_args"), (flce.FlceRmsnormArgs, "flce_rmsnorm_args"),
+           (flce.FlceRmsnormBwdArgs, "flce_rmsnorm_bwd_args"), (flce.FlceCkpt8Args, "flce_ckpt8_args"),
+           (flce.FlceCkpt8DwArgs, "flce_ckpt8_dw_args")]
+
+
+def test_struct_layouts_match_c(lib, tmp_path):
+    src = ["#include <stdio.h>", "#include <stddef.h>", f'#include "{ROOT}/include/flce.h"', "int main(void){"]
+    for cls, cname in STRUCTS:
+        src.append(f'printf("%zu\\n", sizeof({cname}));')
+        src += [f'printf("%zu\\n", offsetof({cname}, {f}));' for f, _ in cls._fields_]
+    c, exe = tmp_path / "layout.c", tmp_path / "layout"
+    c.write_text("\n".join(src + ["return 0;}"]))
+    subprocess.run(["gcc", "-std=c99", "-o", str(exe), str(c)], check=True)
+    vals = iter(int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split())
+    for cls, _ in STRUCTS:
+        assert next(vals) == ctypes.sizeof(cls)
+        for f, _ in cls._fields_:
+            assert getattr(cls, f).offset == next(vals), f
+
+
+def _set(a, kw):
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def _embed(**kw):
+    return _set(flce.FlceEmbedArgs(4, 16, 10, 1, 0, 0x1000, -100, 1.0, 0, 0x2000, 16, 0x3000, 16, 0x4000, 16, 0x5000, 16,
+                                   0x10000, 1 << 20, None), kw)
+
+
+@pytest.mark.parametrize("kw", [dict(N=-1), dict(H=0), dict(V=0), dict(V=1 << 31), dict(dtype=3), dict(scale=NAN),
+                                dict(scale=INF), dict(tokens=None), dict(tokens=0x1004), dict(E=None), dict(out=None),
+                                dict(ldE=15), dict(ldout=15), dict(E=0x2001), dict(out=0x3001), dict(flags=1),
+                                dict(status=0x6001)])
+def test_embed_fwd_refusals(lib, kw):
+    assert lib.flce_embed_fwd(_embed(**kw), None) == BAD
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(N=-1), BAD), (dict(dtype=9), BAD), (dict(dE_dtype=2), UNS), (dict(dout=None), BAD), (dict(dE=None), BAD),
+    (dict(lddout=8), BAD), (dict(lddE=8), BAD), (dict(dE=0x5002), BAD), (dict(workspace=None), BAD),
+    (dict(workspace=0x10010), BAD), (dict(workspace_bytes=64), WS), (dict(flags=1), BAD), (dict(tokens=None), BAD)])
+def test_embed_bwd_refusals(lib, kw, code):
+    assert lib.flce_embed_bwd(_embed(**kw), None) == code
+
+
+def _norm(**kw):
+    return _set(flce.FlceRmsnormArgs(4, 16, 1, 1e-5, 0.0, 0, 0x1000, 16, None, 0, 0x2000, None, 0, 0x3000, 16, 0x4000,
+                                     None, 0, None, None, 0, None), kw)
+
+
+@pytest.mark.parametrize("kw", [dict(N=-1), dict(H=0), dict(dtype=5), dict(eps=0.0), dict(eps=-1.0), dict(eps=NAN),
+                                dict(eps=INF), dict(weight_offset=NAN), dict(flags=4), dict(x=None), dict(x=0x1001),
+                                dict(ldx=15), dict(weight=None), dict(residual=0x5000), dict(h=0x5000), dict(ldy=3),
+                                dict(y=0x3001), dict(rstd=0x4002), dict(y8=0x5000, ldy8=16), dict(y8=0x5000, y8_scale=0x6000),
+                                dict(h8=0x5000, ldh8=16), dict(h8=0x5000, h8_scale=0x6000, ldh8=15)])
+def test_rmsnorm_fwd_refusals(lib, kw):
+    assert lib.flce_rmsnorm_fwd(_norm(**kw), None) == BAD
+
+
+def _norm_bwd(**kw):
+    return _set(flce.FlceRmsnormBwdArgs(4, 16, 1, 0, 0.0, 0, 0x1000, 16, 0x2000, 16, None, 0, None, 0x3000, 0x4000, None, 0,
+                                        0x5000, 16, 0x6000, 0x10000, 1 << 30), kw)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(N=-1), BAD), (dict(dtype=5), BAD), (dict(dweight_dtype=2), UNS), (dict(dy=None), BAD), (dict(lddy=1), BAD),
+    (dict(h=None), BAD), (dict(h8=0x7000, ldh8=16, h8_scale=0x8000), BAD), (dict(h=None, h8=0x7000, ldh8=16), BAD),
+    (dict(rstd=None), BAD), (dict(weight=None), BAD), (dict(dh=0x7001, lddh=16), BAD), (dict(lddx=2), BAD),
+    (dict(workspace=None), BAD), (dict(workspace=0x10004), BAD), (dict(workspace_bytes=100), WS), (dict(flags=1), BAD),
+    (dict(weight_offset=INF), BAD)])
+def test_rmsnorm_bwd_refusals(lib, kw, code):
+    assert lib.flce_rmsnorm_bwd(_norm_bwd(**kw), None) == code
+
+
+@pytest.mark.parametrize("kw", [dict(N=-1), dict(H=0), dict(dtype=4), dict(flags=1), dict(x=None), dict(q=None),
+                                dict(scale=None), dict(ldx=8), dict(ldq=8), dict(x=0x1001), dict(scale=0x3002)])
+def test_pack_refusals(lib, kw):
+    assert lib.flce_ckpt8_pack(_set(flce.FlceCkpt8Args(4, 16, 1, 0, 0x1000, 16, 0x2000, 16, 0x3000), kw), None) == BAD
+
+
+def _dw(**kw):
+    return _set(flce.FlceCkpt8DwArgs(4, 8, 16, 1, 0, 0, 0, 0x1000, 8, 0x2000, 16, 0x3000, 0x4000, 16, 0x10000, 1 << 30, None), kw)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), BAD), (dict(N=0), BAD), (dict(K=0), BAD), (dict(dtype=8), BAD), (dict(dW_dtype=2), UNS),
+    (dict(dtype=0, dW_dtype=1), UNS), (dict(dy=None), BAD), (dict(q=None), BAD), (dict(scale=None), BAD),
+    (dict(dW=None), BAD), (dict(lddy=7), BAD), (dict(ldq=15), BAD), (dict(lddW=15), BAD), (dict(dW=0x4002), BAD),
+    (dict(workspace=None), BAD), (dict(workspace=0x10020), BAD), (dict(workspace_bytes=8), WS), (dict(flags=2), BAD)])
+def test_dw_refusals(lib, kw, code):
+    assert lib.flce_ckpt8_dw(_dw(**kw), None) == code
+
+
+def test_null_argument_structs(lib):
+    for name in ("embed_fwd", "embed_bwd", "rmsnorm_fwd", "rmsnorm_bwd", "ckpt8_pack", "ckpt8_dw"):
+        assert getattr(lib, "flce_" + name)(None, None) == BAD
+
+
+def test_no_rows_need_no_pointers(lib):
+    """N = 0 with nothing to overwrite returns at once (an empty tensor's pointer is null)."""
+    assert lib.flce_embed_fwd(_embed(N=0, tokens=None, E=None, out=None), None) == flce.FLCE_OK
+    assert lib.flce_embed_bwd(_embed(N=0, tokens=None, dout=None, workspace=None, workspace_bytes=0), None) == flce.FLCE_OK
+    assert lib.flce_rmsnorm_fwd(_norm(N=0, x=None, y=None, rstd=None), None) == flce.FLCE_OK
+    assert lib.flce_rmsnorm_bwd(_norm_bwd(N=0, dy=None, h=None, rstd=None, dx=None), None) == flce.FLCE_OK
+    assert lib.flce_ckpt8_pack(flce.FlceCkpt8Args(0, 16, 1, 0, None, 16, None, 16, None), None) == flce.FLCE_OK
+    assert lib.flce_ckpt8_dw(_dw(M=0, dy=None, q=None, scale=None), None) == flce.FLCE_OK
+
+
+def test_workspace_sizes(lib):
+    assert lib.flce_embed_workspace_size(-1, 4, 4) == 0 and lib.flce_embed_workspace_size(4, 0, 4) == 0
+    assert lib.flce_embed_workspace_size(0, 4, 4) > 0
+    assert lib.flce_rmsnorm_workspace_size(4, 0) == 0 and lib.flce_rmsnorm_workspace_size(0, 8) > 0
+    assert lib.flce_ckpt8_dw_workspace_size(4, 4, 0, 1) == 0 and lib.flce_ckpt8_dw_workspace_size(4, 4, 4, 7) == 0
+    assert lib.flce_ckpt8_dw_workspace_size(0, 4, 4, 1) > 0
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
+    x, w = torch.randn(4, 8), torch.randn(8)
+    for f in (lambda: flce.rmsnorm_fwd(x, w), lambda: flce.ckpt8_pack(x),
+              lambda: flce.embed_fwd(torch.zeros(3, dtype=torch.int64), x),
+              lambda: flce.embed_bwd(torch.zeros(4, dtype=torch.int64), x, V=3),
+              lambda: flce.ckpt8_dw(x, x, x)):
+        with pytest.raises(ValueError, match="CUDA"):
+            f()
+
+
+def test_matrix_check():
+    """The binding's check of a matrix operand, which needs no GPU."""
+    cpu = torch.device("cpu")
+    x = torch.randn(6, 8)
+    assert flce._matrix("x", x, 6, 8, torch.float32, cpu) == (x.data_ptr(), 8)
+    assert flce._matrix("x", x[:, 2:5], 6, 3, torch.float32, cpu) == (x.data_ptr() + 8, 8)
+    for bad in (x.t(), x[:, ::2], x.half(), x[:1].expand(6, 8), x[:5]):
+        with pytest.raises(ValueError):
+            flce._matrix("x", bad, 6, bad.shape[1], torch.float32, cpu)
+    with pytest.raises(ValueError):
+        flce._vector("v", x[:, 0], 6, torch.float32, cpu)
+    with pytest.raises(ValueError):
+        flce._dense("s", x[:, :4], 6, 4, cpu)
+
+
+# ---- the oracles
+
+def test_e4m3_rounding_against_torch():
+    """Every quotient near every e4m3 value rounds as torch's conversion does."""
+    codes = torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    mids = (codes[1:] + codes[:-1]) / 2
+    x = torch.cat([codes, mids, mids * (1 + 2.0 ** -20), mids * (1 - 2.0 ** -20), torch.rand(5000).double() * 448])
+    x = torch.cat([x, -x]).float()
+    assert np.array_equal(oo.round_e4m3(x.double().numpy()), x.to(torch.float8_e4m3fn).double().numpy())
+
+
+def test_block_scales_are_the_smallest_that_fit():
+    x = np.random.default_rng(0).standard_normal((50, 300)) * np.exp(np.random.default_rng(1).standard_normal((50, 1)) * 8)
+    x[0, :128] = 0
+    x[1, :128] = 448.0
+    x[2, :128] = np.nextafter(448.0, 1e9)
+    e = oo.block_exponent(x)
+    assert e[0, 0] == 0 and e[1, 0] == 0 and e[2, 0] == 1
+    for b in range(3):
+        m = np.abs(x[:, b * 128:(b + 1) * 128]).max(axis=1)
+        live = m > 0
+        assert np.all(m[live] <= 448 * np.exp2(e[live, b])) and np.all(m[live] > 448 * np.exp2(e[live, b] - 1))
+
+
+def test_rmsnorm_oracle_gradient_against_differences():
+    rng = np.random.default_rng(2)
+    h, w, c = rng.standard_normal((4, 9)), rng.standard_normal(9), rng.standard_normal((4, 9))
+    _, rstd = oo.rmsnorm_fwd(h, w, 1e-3, 0.5)
+    dx, dw, _, _ = oo.rmsnorm_bwd(c, h, rstd, w, 0.5)
+    L = lambda hh, ww: (c * oo.rmsnorm_fwd(hh, ww, 1e-3, 0.5)[0]).sum()  # noqa: E731
+    st = 1e-6
+    for i in range(4):
+        for j in range(9):
+            d = np.zeros_like(h)
+            d[i, j] = st
+            assert abs((L(h + d, w) - L(h - d, w)) / (2 * st) - dx[i, j]) < 1e-7
+    for j in range(9):
+        d = np.zeros_like(w)
+        d[j] = st
+        assert abs((L(h, w + d) - L(h, w - d)) / (2 * st) - dw[j]) < 1e-7
+
+
+def test_embed_oracle_gradient_against_differences():
+    rng = np.random.default_rng(3)
+    t = np.array([0, 2, 2, -100, 1, 2])
+    E, c = rng.standard_normal((4, 5)), rng.standard_normal((6, 5))
+    dE, _, n = oo.embed_bwd(t, c, 4, 1.3, -100)
+    assert n.tolist() == [1, 1, 3, 0]
+    L = lambda e: (c * oo.embed_fwd(t, e, 1.3, -100)).sum()  # noqa: E731
+    for v in range(4):
+        for j in range(5):
+            d = np.zeros_like(E)
+            d[v, j] = 1.0
+            assert abs((L(E + d) - L(E - d)) / 2 - dE[v, j]) < 1e-12
