@@ -7,7 +7,7 @@
 // Packing is bound by HBM: 2 bytes read and 1.03 written per 16-bit element.
 #include <math.h>
 
-#include "flce_ops.cuh"
+#include "flce_ckpt8.cuh"
 
 namespace flce {
 namespace {
@@ -47,20 +47,8 @@ cudaError_t pack(const flce_ckpt8_args& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// fp32 FMA product: a block makes a 64 x 64 tile of dW, 256 threads with 4 x 4 sums each,
+// The product in fp32 FMAs (FLCE_FLAG_FORCE_SIMT): a block makes a 64 x 64 tile of dW, 256 threads with 4 x 4 sums each,
 // 16 rows of dy and of the expanded checkpoint at a time in shared memory.
-struct DwArgs {
-  int64_t M, N, K, nblk;
-  const void* dy;
-  int64_t lddy;
-  const uint8_t* q;
-  int64_t ldq;
-  const float* scale;
-  void* dW;
-  int64_t lddW;
-  int ovw;
-};
-
 template <typename T, typename D>
 __global__ void __launch_bounds__(256) k_dw_simt(const __grid_constant__ DwArgs a) {
   __shared__ __align__(16) float as[16][64], bs[16][64];
@@ -107,7 +95,7 @@ cudaError_t dw_simt(const DwArgs& a, bool f32, cudaStream_t s) {
 }
 
 bool sizes_ok(int64_t M, int64_t N, int64_t K) {
-  return M >= 0 && N >= 1 && K >= 1 && M <= 0x7fffffffLL && N <= 65535LL * 64 && K <= (1LL << 30);
+  return M >= 0 && N >= 1 && K >= 1 && M <= (1LL << 29) && N <= 65535LL * 64 && K <= 65535LL * 64;
 }
 
 }  // namespace
@@ -133,7 +121,7 @@ extern "C" int32_t flce_ckpt8_pack(const flce_ckpt8_args* x, void* stream) {
 
 extern "C" size_t flce_ckpt8_dw_workspace_size(int64_t M, int64_t N, int64_t K, int32_t dtype) {
   if (!sizes_ok(M, N, K) || !valid_dtype(dtype)) return 0;
-  return 256;
+  return dw_tc_workspace(M, N, K, dtype);
 }
 
 extern "C" int32_t flce_ckpt8_dw(const flce_ckpt8_dw_args* x, void* stream) {
@@ -151,14 +139,23 @@ extern "C" int32_t flce_ckpt8_dw(const flce_ckpt8_dw_args* x, void* stream) {
     if (x->workspace_bytes < flce_ckpt8_dw_workspace_size(x->M, x->N, x->K, x->dtype)) return FLCE_ERR_WORKSPACE;
   }
   const bool ovw = (x->flags & FLCE_FLAG_DW_OVERWRITE) != 0;
+  const bool simt = (x->flags & FLCE_FLAG_FORCE_SIMT) != 0;
+  if (x->M > 0 && !simt && !dw_tc_supported()) return FLCE_ERR_UNSUPPORTED;  // no tensor-map encoder in the driver
   cudaStream_t s = (cudaStream_t)stream;
+  // without a status word of the caller's: the one flce_get_status reads in a workspace
+  int* status = x->status ? (int*)x->status : x->M > 0 ? &((Ctrl*)x->workspace)->status : nullptr;
   cudaError_t e = cudaSuccess;
-  if (x->status) e = cudaMemsetAsync(x->status, 0, sizeof(int), s);
+  if (status) e = cudaMemsetAsync(status, 0, sizeof(int), s);
   if (e == cudaSuccess && x->M == 0 && ovw)
     e = cudaMemset2DAsync(x->dW, (size_t)x->lddW * wsz, 0, (size_t)x->K * wsz, (size_t)x->N, s);
   if (e != cudaSuccess || x->M == 0) return cuda_status(e);
-  DwArgs a = {x->M, x->N, x->K, cdiv64(x->K, Q_BLOCK), x->dy, x->lddy, (const uint8_t*)x->q, x->ldq,
-              x->scale, x->dW, x->lddW, ovw};
+  const DwArgs a = {x->M, x->N, x->K, cdiv64(x->K, Q_BLOCK), x->dy, x->lddy, (const uint8_t*)x->q, x->ldq,
+                    x->scale, x->dW, x->lddW, ovw};
+  if (!simt) {
+    const uint32_t ms = x->wait_timeout_ms ? x->wait_timeout_ms : DEFAULT_TIMEOUT_MS;
+    return cuda_status(
+        launch_dw_tc8(a, x->dtype, x->dW_dtype, x->workspace, status, (uint64_t)ms * 1000000ull, s));
+  }
   const bool f32 = x->dW_dtype == FLCE_F32;
   switch (x->dtype) {
     case FLCE_F32: return cuda_status(dw_simt<float>(a, f32, s));
