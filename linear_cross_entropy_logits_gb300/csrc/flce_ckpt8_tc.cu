@@ -11,9 +11,13 @@
 // rows m per step. Each CTA stages its 128 columns of dy (TMA, 16 KB) and its 128 columns of
 // q (TMA, 8 KB: one scale block), expands q into 16 KB of bf16 / fp16 in the swizzled MN-major
 // layout that the tensor cores read, and holds a 128 x 256 fp32 accumulator in its TMEM (two,
-// used in turn). 512 threads:
-//   warp 0        TMA producer                    warps 4..7    expand q
-//   warp 1        MMA issuer (leader CTA)         warps 8..15   sums and output
+// used in turn). The copies run up to seven steps ahead, the expansion up to three.
+// 640 threads:
+//   warp 0   TMA producer               warps 4..11   expand q
+//   warp 1   MMA issuer (leader CTA)    warps 12..19  sums and output
+//   warp 2   the steps' scales (cp.async)
+// A step's MMAs take 512 cycles; expanding 8192 values takes about 230 instructions of each of
+// the eight warps (two per scheduler).
 // The tensor cores truncate when they add to an accumulator; over M rows that adds up to an
 // error of about M * 1.1e-9 relative (9e-6 at 8192 rows). So the accumulator is read out after
 // every SEGMENT of rows and added, rounded to nearest, to fp32 sums in the registers of the
@@ -42,11 +46,17 @@ constexpr int TILE = 256;                 // pair tile, both ways
 constexpr int A_BYTES = 128 * BK * 2;     // dy: 128 columns
 constexpr int B_BYTES = 128 * BK * 2;     // expanded q
 constexpr int Q_BYTES = 128 * BK;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES + Q_BYTES;  // 40 KB
-constexpr int STAGES = 5;
+constexpr int S_BYTES = BK * 4;           // the rows' scales
+constexpr int STAGES = 7;                 // of dy, q and scales
+constexpr int STAGE_BYTES = A_BYTES + Q_BYTES;
+constexpr int SLOTS = 3;                  // of expanded q
+constexpr int OFF_B = STAGES * STAGE_BYTES;
+constexpr int OFF_S = OFF_B + SLOTS * B_BYTES;
+constexpr int OFF_BARS = OFF_S + STAGES * S_BYTES;
 constexpr int BOX = 64 * 64 * 2;          // one 64 x 64 MN-major box
-constexpr int THREADS = 512;
-constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + 512;
+constexpr int THREADS = 640;
+constexpr int CONV_WARPS = 8;
+constexpr int SMEM = OFF_BARS + 512 + 1024;
 static_assert(SMEM <= 232448, "shared memory per CTA");
 constexpr int SEG16 = 32;                 // steps per accumulator for 16-bit dy (2048 rows)
 constexpr int SEG32 = 8;                  // for fp32 dy: its results are held to fp32 accuracy
@@ -96,28 +106,35 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return r;
 }
 
-// dW columns col .. col + 3 of a row (p: the row) (+)= v.
+// 16 columns of a row of dW, from p on, of which `left` exist, (+)= v; the loads go out
+// together.
 template <typename D>
-__device__ __forceinline__ void put4(D* p, int64_t col, int64_t K, const float* v, int vec, int ovw) {
-  if (vec && col + 4 <= K) {
-    if constexpr (std::is_same<D, float>::value) {
-      float4* q = (float4*)(p + col);
-      float4 o = ovw ? make_float4(0.f, 0.f, 0.f, 0.f) : *q;
-      *q = make_float4(o.x + v[0], o.y + v[1], o.z + v[2], o.w + v[3]);
-    } else {
-      uint2* q = (uint2*)(p + col);
-      uint2 u = ovw ? make_uint2(0u, 0u) : *q;
-      const D* h = (const D*)&u;
-      D r[4];
+__device__ __forceinline__ void put16(D* p, int64_t left, const float* v, int vec, int ovw) {
+  if (vec && left >= 16) {
+    constexpr int E = 16 / sizeof(D), NQ = 16 / E;  // elements per 16 bytes, and their number
+    uint4 u[NQ];
+    if (!ovw) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = from_f<D>(ovw ? v[i] : to_f<D>(h[i]) + v[i]);
-      *q = *(const uint2*)r;
+      for (int i = 0; i < NQ; ++i) u[i] = ((const uint4*)p)[i];
+    }
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      float o[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = v[i * E + e];
+      if (!ovw) {
+        float old[E];
+        Vec<D, E>::unpack(u[i], old);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += old[e];
+      }
+      Vec<D, E>::store(p + i * E, o);
     }
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (col + i < K) p[col + i] = from_f<D>(ovw ? v[i] : to_f<D>(p[col + i]) + v[i]);
+  for (int i = 0; i < 16; ++i)
+    if (i < left) p[i] = from_f<D>(ovw ? v[i] : to_f<D>(p[i]) + v[i]);
 }
 
 template <typename T, typename D>
@@ -126,16 +143,20 @@ __global__ void __launch_bounds__(THREADS, 1)
              const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint64_t* bars = (uint64_t*)(smem + STAGES * STAGE_BYTES);
+  uint64_t* bars = (uint64_t*)(smem + OFF_BARS);
   const uint32_t bar0 = smem_u32(bars);
   auto full_a = [&](int s) { return bar0 + 8u * s; };                  // both CTAs' dy (leader)
   auto full_q = [&](int s) { return bar0 + 8u * (STAGES + s); };       // this CTA's q
-  auto conv = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };     // q expanded, both CTAs (leader)
-  auto empty = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };    // MMAs done with the stage
-  auto tfull = [&](int s) { return bar0 + 8u * (4 * STAGES + s); };    // accumulator filled
-  auto tempty = [&](int s) { return bar0 + 8u * (4 * STAGES + 2 + s); };  // and read out (leader)
-  const uint32_t drain = bar0 + 8u * (4 * STAGES + 4);
-  uint32_t* tmem_slot = (uint32_t*)(bars + 4 * STAGES + 5);
+  auto full_s = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };   // and its scales
+  auto empty_a = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };  // MMAs done with the stage
+  auto conv = [&](int s) { return bar0 + 8u * (4 * STAGES + s); };     // q expanded, both CTAs (leader)
+  auto empty_b = [&](int s) { return bar0 + 8u * (4 * STAGES + SLOTS + s); };      // MMAs done with the slot
+  auto tfull = [&](int s) { return bar0 + 8u * (4 * STAGES + 2 * SLOTS + s); };    // accumulator filled
+  auto tempty = [&](int s) { return bar0 + 8u * (4 * STAGES + 2 * SLOTS + 2 + s); };  // and read out (leader)
+  const uint32_t drain = bar0 + 8u * (4 * STAGES + 2 * SLOTS + 4);
+  constexpr int NBARS = 4 * STAGES + 2 * SLOTS + 5;
+  static_assert(NBARS * 8 + 8 + STAGES * 4 <= 512, "barrier block");
+  uint32_t* tmem_slot = (uint32_t*)(bars + NBARS);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   int* copies = (int*)(tmem_slot + 2);  // per stage: phases this CTA's producer filled
 
@@ -149,9 +170,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int s = 0; s < STAGES; ++s) {
       bar_init(full_a(s), 1);
       bar_init(full_q(s), 1);
-      bar_init(conv(s), 8);   // four warps of each CTA
-      bar_init(empty(s), 1);
+      bar_init(full_s(s), 32);
+      bar_init(empty_a(s), 1);
       copies[s] = 0;
+    }
+    for (int s = 0; s < SLOTS; ++s) {
+      bar_init(conv(s), 2 * CONV_WARPS);
+      bar_init(empty_b(s), 1);
     }
     for (int s = 0; s < 2; ++s) {
       bar_init(tfull(s), 1);
@@ -174,9 +199,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Registers: 128 a thread at launch (4 warpgroups: 512 in all) = 40 + 88 + 192 + 192.
+  // Registers: 96 a thread at launch (5 warpgroups: 480 in all) = 32 + 2 * 56 + 2 * 168.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp == 0 && lane == 0) {
       // ---------------- TMA producer, both CTAs
       int s = 0;
@@ -186,7 +211,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int i = pair; ok && get_item(p, i, it); i += npairs) {
         const int n0 = it.tile / p.tk * TILE + (int)rank * 128, k0 = it.tile % p.tk * TILE + (int)rank * 128;
         for (int st = it.s0; st < it.s1; ++st) {
-          if (!bar_wait(empty(s), ph ^ 1u, ab, true)) {
+          if (!bar_wait(empty_a(s), ph ^ 1u, ab, true)) {
             ok = false;
             break;
           }
@@ -194,7 +219,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (leader) bar_expect(full_a(s), 2 * A_BYTES);
           bar_expect(full_q(s), Q_BYTES);
           const uint32_t a = smem_u32(smem + s * STAGE_BYTES);
-          tma_load(a + A_BYTES + B_BYTES, &tm_q, full_q(s), k0, st % p.mstep * BK);
+          tma_load(a + A_BYTES, &tm_q, full_q(s), k0, st % p.mstep * BK);
           tma_load_pair(a, &tm_dy, fa, n0, st * BK);
           tma_load_pair(a + BOX, &tm_dy, fa, n0 + 64, st * BK);
           copies[s] += 1;
@@ -210,8 +235,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       // kind::f16, fp32 accumulator, both operands MN-major, N = 256, M = 256
       constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 15) | (1u << 16) |
                                  ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
-      int s = 0, g = 0;
-      uint32_t ph = 0;
+      int s = 0, b = 0, g = 0;
+      uint32_t ph = 0, bph = 0;
       bool ok = true;
       Item it;
       for (int i = pair; ok && get_item(p, i, it); i += npairs) {
@@ -224,20 +249,25 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc_after();
           const int end = min(st + p.seg, it.s1);
           for (bool first = true; st < end; ++st, first = false) {
-            if (!bar_wait(full_a(s), ph, ab, true) || !bar_wait(conv(s), ph, ab, true)) {
+            if (!bar_wait(full_a(s), ph, ab, true) || !bar_wait(conv(b), bph, ab, true)) {
               ok = false;
               break;
             }
             tc_after();
-            const uint32_t a = smem_u32(smem + s * STAGE_BYTES), b = a + A_BYTES;
+            const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = smem_u32(smem + OFF_B + b * B_BYTES);
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k)
-              mma_pair(tmem + (uint32_t)(as * TILE), desc_mn(a + k * 2048, BOX), desc_mn(b + k * 2048, BOX), idesc,
+              mma_pair(tmem + (uint32_t)(as * TILE), desc_mn(sa + k * 2048, BOX), desc_mn(sb + k * 2048, BOX), idesc,
                        !first || k != 0);
-            mma_commit_pair(empty(s));
+            mma_commit_pair(empty_a(s));
+            mma_commit_pair(empty_b(b));
             if (++s == STAGES) {
               s = 0;
               ph ^= 1u;
+            }
+            if (++b == SLOTS) {
+              b = 0;
+              bph ^= 1u;
             }
           }
           if (ok) mma_commit_pair(tfull(as));
@@ -246,64 +276,85 @@ __global__ void __launch_bounds__(THREADS, 1)
       // every MMA issued completes before TMEM is freed or shared memory released
       mma_commit_local(drain);
       bar_wait(drain, 0u, ab, false);
+    } else if (warp == 2) {
+      // ---------------- scales of a step's 64 rows, that of row 16 j + r at 4 r + j
+      const uint32_t dst = smem_u32(smem + OFF_S) + (uint32_t)((lane & 15) * 4 + (lane >> 4)) * 4;
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      Item it;
+      for (int i = pair; ok && get_item(p, i, it); i += npairs) {
+        const int blk = it.tile % p.tk * 2 + (int)rank;  // this CTA's 128 columns: one scale block
+        const float* sp = p.d.scale + (blk < p.d.nblk ? blk : 0);
+        int row = it.s0 % p.mstep;  // step within a term of dy
+        for (int st = it.s0; st < it.s1; ++st) {
+          ok = __all_sync(0xffffffffu, bar_wait(empty_a(s), ph ^ 1u, ab, true));
+          if (!ok) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int64_t m = (int64_t)row * BK + h * 32 + lane;
+            const bool in = blk < p.d.nblk && m < p.d.M;
+            cp_async4(dst + (uint32_t)(s * S_BYTES + h * 8), sp + (in ? m * p.d.nblk : 0), in);
+          }
+          bar_arrive_cp_async(full_s(s));
+          if (++row == p.mstep) row = 0;
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      cp_async_wait_all();
     }
-  } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    // ---------------- expand q: thread (r8, c) takes bytes 8c .. 8c + 7 of rows r8 + 8 i
+  } else if (warp < 4 + CONV_WARPS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // ---------------- expand q: thread (r, c) takes bytes 8c .. 8c + 7 of rows r + 16 j
     const int t = threadIdx.x - 128;
-    const int c = t & 15, r8 = t >> 4;
-    const uint32_t out_col = (uint32_t)(c >> 3) * BOX + (uint32_t)r8 * 128 + (uint32_t)(((c & 7) ^ r8) << 4);
-    int s = 0;
-    uint32_t ph = 0;
+    const int c = t & 15, r = t >> 4;
+    const uint32_t out = (uint32_t)(c >> 3) * BOX + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+    int s = 0, b = 0;
+    uint32_t ph = 0, bph = 0;
     bool ok = true;
     Item it;
     for (int i = pair; ok && get_item(p, i, it); i += npairs) {
-      const int blk = it.tile % p.tk * 2 + (int)rank;  // this CTA's 128 columns: one scale block
-      const bool live = blk < p.d.nblk;
-      const float* sp = p.d.scale + blk;
-      float sc[8];
-      auto scales = [&](int st) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int64_t m = (int64_t)(st % p.mstep) * BK + j * 8 + r8;
-          sc[j] = live && m < p.d.M ? sp[m * p.d.nblk] : 0.0f;
-        }
-      };
-      scales(it.s0);
       for (int st = it.s0; st < it.s1; ++st) {
-        ok = __all_sync(0xffffffffu, bar_wait(full_q(s), ph, ab, true));
+        ok = bar_wait(full_q(s), ph, ab, true) && bar_wait(full_s(s), ph, ab, true) &&
+             bar_wait(empty_b(b), bph ^ 1u, ab, true);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint8_t* q = smem + s * STAGE_BYTES + A_BYTES + B_BYTES;
-        uint8_t* b = smem + s * STAGE_BYTES + A_BYTES + out_col;
-        uint2 u[8];
+        const uint8_t* q = smem + s * STAGE_BYTES + A_BYTES + r * 128 + c * 8;
+        uint8_t* o = smem + OFF_B + b * B_BYTES + out;
+        const float4 sc4 = *(const float4*)(smem + OFF_S + s * S_BYTES + r * 16);
+        const float sc[4] = {sc4.x, sc4.y, sc4.z, sc4.w};
+        uint2 u[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = *(const uint2*)(q + (j * 8 + r8) * 128 + c * 8);
-        float now[8];
+        for (int j = 0; j < 4; ++j) u[j] = *(const uint2*)(q + j * 2048);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) now[j] = sc[j];
-        if (st + 1 < it.s1) scales(st + 1);  // in flight while this step is expanded
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const float2 x0 = q_unpack2(u[j].x), x1 = q_unpack2(u[j].x >> 16);
           const float2 x2 = q_unpack2(u[j].y), x3 = q_unpack2(u[j].y >> 16);
-          *(uint4*)(b + j * 1024) =
-              make_uint4(pack16<T>(x0.x * now[j], x0.y * now[j]), pack16<T>(x1.x * now[j], x1.y * now[j]),
-                         pack16<T>(x2.x * now[j], x2.y * now[j]), pack16<T>(x3.x * now[j], x3.y * now[j]));
+          *(uint4*)(o + j * 2048) =
+              make_uint4(pack16<T>(x0.x * sc[j], x0.y * sc[j]), pack16<T>(x1.x * sc[j], x1.y * sc[j]),
+                         pack16<T>(x2.x * sc[j], x2.y * sc[j]), pack16<T>(x3.x * sc[j], x3.y * sc[j]));
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) bar_arrive(mapa(conv(s), 0));
+        if (lane == 0) bar_arrive(mapa(conv(b), 0));
         if (++s == STAGES) {
           s = 0;
           ph ^= 1u;
         }
+        if (++b == SLOTS) {
+          b = 0;
+          bph ^= 1u;
+        }
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     // ---------------- sums and output: warp w has rows 32 (w % 4) .. of this CTA's 128 and
     // columns 128 h .. of the tile's 256
-    const int w = warp - 8, quad = warp & 3, h = w >> 2;
+    const int w = warp - 4 - CONV_WARPS, quad = warp & 3, h = w >> 2;
     const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(h * 128);
     int g = 0;
     bool ok = true;
@@ -359,8 +410,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (n < p.d.N) {
         D* row = (D*)p.d.dW + n * p.d.lddW;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (k0 + 4 * j < p.d.K) put4<D>(row, k0 + 4 * j, p.d.K, &acc[4 * j], p.vec, p.d.ovw);
+        for (int j = 0; j < 8; ++j)
+          if (k0 + 16 * j < p.d.K) put16<D>(row + k0 + 16 * j, p.d.K - k0 - 16 * j, &acc[16 * j], p.vec, p.d.ovw);
       }
     }
   }
