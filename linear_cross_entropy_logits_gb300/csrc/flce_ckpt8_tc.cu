@@ -11,7 +11,7 @@
 // rows m per step. Each CTA stages its 128 columns of dy (TMA, 16 KB) and its 128 columns of
 // q (TMA, 8 KB: one scale block), expands q into 16 KB of bf16 / fp16 in the swizzled MN-major
 // layout that the tensor cores read, and holds a 128 x 256 fp32 accumulator in its TMEM (two,
-// used in turn). The copies run up to seven steps ahead, the expansion up to three.
+// used in turn). The copies run up to six steps ahead, the expansion up to four.
 // 640 threads:
 //   warp 0   TMA producer               warps 4..11   expand q
 //   warp 1   MMA issuer (leader CTA)    warps 12..19  sums and output
@@ -47,9 +47,9 @@ constexpr int A_BYTES = 128 * BK * 2;     // dy: 128 columns
 constexpr int B_BYTES = 128 * BK * 2;     // expanded q
 constexpr int Q_BYTES = 128 * BK;
 constexpr int S_BYTES = BK * 4;           // the rows' scales
-constexpr int STAGES = 7;                 // of dy, q and scales
+constexpr int STAGES = 6;                 // of dy, q and scales
 constexpr int STAGE_BYTES = A_BYTES + Q_BYTES;
-constexpr int SLOTS = 3;                  // of expanded q
+constexpr int SLOTS = 4;                  // of expanded q
 constexpr int OFF_B = STAGES * STAGE_BYTES;
 constexpr int OFF_S = OFF_B + SLOTS * B_BYTES;
 constexpr int OFF_BARS = OFF_S + STAGES * S_BYTES;
@@ -58,6 +58,7 @@ constexpr int THREADS = 640;
 constexpr int CONV_WARPS = 8;
 constexpr int SMEM = OFF_BARS + 512 + 1024;
 static_assert(SMEM <= 232448, "shared memory per CTA");
+static_assert(STAGES > SLOTS, "the expanding warps watch a stage's barrier for their slot");
 constexpr int SEG16 = 32;                 // steps per accumulator for 16-bit dy (2048 rows)
 constexpr int SEG32 = 8;                  // for fp32 dy: its results are held to fp32 accuracy
 constexpr int MAX_SPLIT = 16;
@@ -148,13 +149,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto full_a = [&](int s) { return bar0 + 8u * s; };                  // both CTAs' dy (leader)
   auto full_q = [&](int s) { return bar0 + 8u * (STAGES + s); };       // this CTA's q
   auto full_s = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };   // and its scales
-  auto empty_a = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };  // MMAs done with the stage
+  auto empty_a = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };  // MMAs done with the stage (and its slot)
   auto conv = [&](int s) { return bar0 + 8u * (4 * STAGES + s); };     // q expanded, both CTAs (leader)
-  auto empty_b = [&](int s) { return bar0 + 8u * (4 * STAGES + SLOTS + s); };      // MMAs done with the slot
-  auto tfull = [&](int s) { return bar0 + 8u * (4 * STAGES + 2 * SLOTS + s); };    // accumulator filled
-  auto tempty = [&](int s) { return bar0 + 8u * (4 * STAGES + 2 * SLOTS + 2 + s); };  // and read out (leader)
-  const uint32_t drain = bar0 + 8u * (4 * STAGES + 2 * SLOTS + 4);
-  constexpr int NBARS = 4 * STAGES + 2 * SLOTS + 5;
+  auto tfull = [&](int s) { return bar0 + 8u * (4 * STAGES + SLOTS + s); };       // accumulator filled
+  auto tempty = [&](int s) { return bar0 + 8u * (4 * STAGES + SLOTS + 2 + s); };  // and read out (leader)
+  const uint32_t drain = bar0 + 8u * (4 * STAGES + SLOTS + 4);
+  constexpr int NBARS = 4 * STAGES + SLOTS + 5;
   static_assert(NBARS * 8 + 8 + STAGES * 4 <= 512, "barrier block");
   uint32_t* tmem_slot = (uint32_t*)(bars + NBARS);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
@@ -174,10 +174,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       bar_init(empty_a(s), 1);
       copies[s] = 0;
     }
-    for (int s = 0; s < SLOTS; ++s) {
-      bar_init(conv(s), 2 * CONV_WARPS);
-      bar_init(empty_b(s), 1);
-    }
+    for (int s = 0; s < SLOTS; ++s) bar_init(conv(s), 8);  // four warps of each CTA
     for (int s = 0; s < 2; ++s) {
       bar_init(tfull(s), 1);
       bar_init(tempty(s), 16);  // eight warps of each CTA
@@ -260,7 +257,6 @@ __global__ void __launch_bounds__(THREADS, 1)
               mma_pair(tmem + (uint32_t)(as * TILE), desc_mn(sa + k * 2048, BOX), desc_mn(sb + k * 2048, BOX), idesc,
                        !first || k != 0);
             mma_commit_pair(empty_a(s));
-            mma_commit_pair(empty_b(b));
             if (++s == STAGES) {
               s = 0;
               ph ^= 1u;
@@ -277,8 +273,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mma_commit_local(drain);
       bar_wait(drain, 0u, ab, false);
     } else if (warp == 2) {
-      // ---------------- scales of a step's 64 rows, that of row 16 j + r at 4 r + j
-      const uint32_t dst = smem_u32(smem + OFF_S) + (uint32_t)((lane & 15) * 4 + (lane >> 4)) * 4;
+      // ---------------- scales of a step's 64 rows, that of row 8 j + r at 8 r + j
+      const uint32_t dst = smem_u32(smem + OFF_S) + (uint32_t)((lane & 7) * 8 + (lane >> 3)) * 4;
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -294,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int h = 0; h < 2; ++h) {
             const int64_t m = (int64_t)row * BK + h * 32 + lane;
             const bool in = blk < p.d.nblk && m < p.d.M;
-            cp_async4(dst + (uint32_t)(s * S_BYTES + h * 8), sp + (in ? m * p.d.nblk : 0), in);
+            cp_async4(dst + (uint32_t)(s * S_BYTES + h * 16), sp + (in ? m * p.d.nblk : 0), in);
           }
           bar_arrive_cp_async(full_s(s));
           if (++row == p.mstep) row = 0;
@@ -308,46 +304,56 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp < 4 + CONV_WARPS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    // ---------------- expand q: thread (r, c) takes bytes 8c .. 8c + 7 of rows r + 16 j
-    const int t = threadIdx.x - 128;
+    // ---------------- expand q: two groups of four warps take the steps in turn, so a step's
+    // expansion may last two steps; thread (r, c) takes bytes 8c .. 8c + 7 of rows r + 8 j
+    const int group = (warp - 4) >> 2;
+    const int t = threadIdx.x & 127;
     const int c = t & 15, r = t >> 4;
-    const uint32_t out = (uint32_t)(c >> 3) * BOX + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
-    int s = 0, b = 0;
-    uint32_t ph = 0, bph = 0;
+    const uint32_t out = (uint32_t)(c >> 3) * BOX + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ r) << 4);
+    int s = 0, b = 0, turn = 0;
+    uint32_t ph = 0;
     bool ok = true;
     Item it;
     for (int i = pair; ok && get_item(p, i, it); i += npairs) {
-      for (int st = it.s0; st < it.s1; ++st) {
-        ok = bar_wait(full_q(s), ph, ab, true) && bar_wait(full_s(s), ph, ab, true) &&
-             bar_wait(empty_b(b), bph ^ 1u, ab, true);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint8_t* q = smem + s * STAGE_BYTES + A_BYTES + r * 128 + c * 8;
-        uint8_t* o = smem + OFF_B + b * B_BYTES + out;
-        const float4 sc4 = *(const float4*)(smem + OFF_S + s * S_BYTES + r * 16);
-        const float sc[4] = {sc4.x, sc4.y, sc4.z, sc4.w};
-        uint2 u[4];
+      for (int st = it.s0; st < it.s1; ++st, ++turn) {
+        if ((turn & 1) == group) {
+          ok = bar_wait(full_q(s), ph, ab, true) && bar_wait(full_s(s), ph, ab, true);
+          if (ok && turn >= SLOTS) {
+            // the slot's last user, SLOTS steps back, was in stage s - SLOTS (this round's or,
+            // below 0, the round before's)
+            const int u = s - SLOTS;
+            ok = bar_wait(empty_a(u < 0 ? u + STAGES : u), u < 0 ? ph ^ 1u : ph, ab, true);
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint8_t* q = smem + s * STAGE_BYTES + A_BYTES + r * 128 + c * 8;
+          uint8_t* o = smem + OFF_B + b * B_BYTES + out;
+          const float4* sc4 = (const float4*)(smem + OFF_S + s * S_BYTES + r * 32);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = *(const uint2*)(q + j * 2048);
+          for (int h = 0; h < 2; ++h) {
+            const float4 f = sc4[h];
+            const float sc[4] = {f.x, f.y, f.z, f.w};
+            uint2 u[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 x0 = q_unpack2(u[j].x), x1 = q_unpack2(u[j].x >> 16);
-          const float2 x2 = q_unpack2(u[j].y), x3 = q_unpack2(u[j].y >> 16);
-          *(uint4*)(o + j * 2048) =
-              make_uint4(pack16<T>(x0.x * sc[j], x0.y * sc[j]), pack16<T>(x1.x * sc[j], x1.y * sc[j]),
-                         pack16<T>(x2.x * sc[j], x2.y * sc[j]), pack16<T>(x3.x * sc[j], x3.y * sc[j]));
+            for (int j = 0; j < 4; ++j) u[j] = *(const uint2*)(q + (4 * h + j) * 1024);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 x0 = q_unpack2(u[j].x), x1 = q_unpack2(u[j].x >> 16);
+              const float2 x2 = q_unpack2(u[j].y), x3 = q_unpack2(u[j].y >> 16);
+              *(uint4*)(o + (4 * h + j) * 1024) =
+                  make_uint4(pack16<T>(x0.x * sc[j], x0.y * sc[j]), pack16<T>(x1.x * sc[j], x1.y * sc[j]),
+                             pack16<T>(x2.x * sc[j], x2.y * sc[j]), pack16<T>(x3.x * sc[j], x3.y * sc[j]));
+            }
+          }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) bar_arrive(mapa(conv(b), 0));
         }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) bar_arrive(mapa(conv(b), 0));
         if (++s == STAGES) {
           s = 0;
           ph ^= 1u;
         }
-        if (++b == SLOTS) {
-          b = 0;
-          bph ^= 1u;
-        }
+        if (++b == SLOTS) b = 0;
       }
     }
   } else {
