@@ -107,6 +107,23 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return r;
 }
 
+// Four e4m3 values times a scale, as two pairs of 16-bit values (packed fp32 products).
+template <typename T>
+__device__ __forceinline__ uint2 expand4(uint32_t u, uint64_t sc2) {
+  uint32_t o[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 x = q_unpack2(i ? u >> 16 : u);
+    uint64_t a;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(x.x), "f"(x.y));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(sc2));
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a));
+    o[i] = pack16<T>(lo, hi);
+  }
+  return make_uint2(o[0], o[1]);
+}
+
 // 16 columns of a row of dW, from p on, of which `left` exist, (+)= v; the loads go out
 // together.
 template <typename D>
@@ -232,6 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // kind::f16, fp32 accumulator, both operands MN-major, N = 256, M = 256
       constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 15) | (1u << 16) |
                                  ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
+      const uint64_t desc0 = desc_mn(smem_u32(smem), BOX);  // the address counts 16 bytes from bit 0
       int s = 0, b = 0, g = 0;
       uint32_t ph = 0, bph = 0;
       bool ok = true;
@@ -251,11 +269,12 @@ __global__ void __launch_bounds__(THREADS, 1)
               break;
             }
             tc_after();
-            const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = smem_u32(smem + OFF_B + b * B_BYTES);
+            const uint64_t da = desc0 + (uint32_t)(s * (STAGE_BYTES >> 4));
+            const uint64_t db = desc0 + (uint32_t)((OFF_B + b * B_BYTES) >> 4);
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k)
-              mma_pair(tmem + (uint32_t)(as * TILE), desc_mn(sa + k * 2048, BOX), desc_mn(sb + k * 2048, BOX), idesc,
-                       !first || k != 0);
+              mma_pair(tmem + (uint32_t)(as * TILE), da + (uint64_t)(k * (2048 >> 4)), db + (uint64_t)(k * (2048 >> 4)),
+                       idesc, !first || k != 0);
             mma_commit_pair(empty_a(s));
             if (++s == STAGES) {
               s = 0;
@@ -338,11 +357,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int j = 0; j < 4; ++j) u[j] = *(const uint2*)(q + (4 * h + j) * 1024);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float2 x0 = q_unpack2(u[j].x), x1 = q_unpack2(u[j].x >> 16);
-              const float2 x2 = q_unpack2(u[j].y), x3 = q_unpack2(u[j].y >> 16);
-              *(uint4*)(o + (4 * h + j) * 1024) =
-                  make_uint4(pack16<T>(x0.x * sc[j], x0.y * sc[j]), pack16<T>(x1.x * sc[j], x1.y * sc[j]),
-                             pack16<T>(x2.x * sc[j], x2.y * sc[j]), pack16<T>(x3.x * sc[j], x3.y * sc[j]));
+              uint64_t sc2;
+              asm("mov.b64 %0, {%1, %1};" : "=l"(sc2) : "f"(sc[j]));
+              const uint2 x = expand4<T>(u[j].x, sc2), y = expand4<T>(u[j].y, sc2);
+              *(uint4*)(o + (4 * h + j) * 1024) = make_uint4(x.x, x.y, y.x, y.y);
             }
           }
           fence_async();
