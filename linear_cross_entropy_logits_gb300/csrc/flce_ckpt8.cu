@@ -42,7 +42,12 @@ void launch_pack(const flce_ckpt8_args& a, cudaStream_t s) {
 template <typename T>
 cudaError_t pack(const flce_ckpt8_args& a, cudaStream_t s) {
   constexpr int W = 16 / sizeof(T);
-  if (a.H % W == 0 && rows16(a.x, a.ldx, sizeof(T)) && aligned_to(a.q, W) && a.ldq % W == 0) launch_pack<T, W, 2>(a, s);
+  auto fits = [&](int bytes) {
+    const int e = bytes / (int)sizeof(T);
+    return a.H % e == 0 && rows_by(a.x, a.ldx, sizeof(T), bytes) && rows_by(a.q, a.ldq, 1, e);
+  };
+  if (fits(32)) launch_pack<T, 2 * W, 2>(a, s);
+  else if (fits(16)) launch_pack<T, W, 2>(a, s);
   else launch_pack<T, 1, 4>(a, s);
   return cudaGetLastError();
 }

@@ -130,10 +130,10 @@ template <typename D>
 __device__ __forceinline__ void put16(D* p, int64_t left, const float* v, int vec, int ovw) {
   if (vec && left >= 16) {
     constexpr int E = 16 / sizeof(D), NQ = 16 / E;  // elements per 16 bytes, and their number
-    uint4 u[NQ];
+    Raw<D, E> u[NQ];
     if (!ovw) {
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) u[i] = ((const uint4*)p)[i];
+      for (int i = 0; i < NQ; ++i) u[i].load(p + i * E);
     }
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
@@ -142,7 +142,7 @@ __device__ __forceinline__ void put16(D* p, int64_t left, const float* v, int ve
       for (int e = 0; e < E; ++e) o[e] = v[i * E + e];
       if (!ovw) {
         float old[E];
-        Vec<D, E>::unpack(u[i], old);
+        u[i].unpack(old);
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] += old[e];
       }

@@ -62,34 +62,31 @@ template <typename T, int EPV, int NV>
 __global__ void __launch_bounds__(512) k_rms_fwd(const __grid_constant__ FwdArgs a, int wpr) {
   __shared__ float red[MAX_WARPS];
   const int lane = threadIdx.x & 31, wb = threadIdx.x >> 5;
-  const int group = wb / wpr, w = wb % wpr;
+  const int group = wb / wpr, w = wb - group * wpr;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / 32 / wpr) + group;
   const bool live = row < a.N;
   float v[NV][EPV];
-  float ss = 0.0f;
+  Raw<T, EPV> x[NV], r[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) v[j][e] = 0.0f;
-    if (live && c < a.H) Vec<T, EPV>::load((const T*)a.x + row * a.ldx + c, v[j]);
-  }
-  if (a.res != nullptr) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
-      if (live && c < a.H) {
-        float r[EPV];
-        Vec<T, EPV>::load((const T*)a.res + row * a.ldres + c, r);
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) v[j][e] += r[e];
-      }
+    x[j].zero();
+    r[j].zero();
+    if (live && c < a.H) {
+      x[j].load((const T*)a.x + row * a.ldx + c);
+      if (a.res != nullptr) r[j].load((const T*)a.res + row * a.ldres + c);
     }
   }
+  float ss = 0.0f;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
 #pragma unroll
-    for (int e = 0; e < EPV; ++e) ss = fmaf(v[j][e], v[j][e], ss);
+    for (int e = 0; e < EPV; ++e) {
+      v[j][e] = x[j].get(e);
+      if (a.res != nullptr) v[j][e] += r[j].get(e);
+      ss = fmaf(v[j][e], v[j][e], ss);
+    }
+  }
   const float var = group_sum(ss, red, wpr, wb, group) * a.inv_h;
   const float rstd = 1.0f / sqrtf(var + a.eps);
   if (!live) return;
@@ -167,25 +164,27 @@ __global__ void __launch_bounds__(512) k_rms_fwd_long(const __grid_constant__ Fw
 }
 
 // Backward: a row group walks the rows group, group + groups, ...; its threads keep their
-// columns' dweight sums in registers and write them once, as one row of a.part.
+// columns' dweight sums in registers. All of a row is loaded before its sum is taken and kept as
+// it lies in memory (unpacked again after the sum), so that two blocks of 512 threads fit an SM
+// and enough loads are in flight. At the end the block's groups add their sums in group order
+// and write one row of a.part.
 template <typename T, int EPV, int NV, bool Q8>
-__global__ void __launch_bounds__(512) k_rms_bwd(const __grid_constant__ BwdArgs a, int wpr) {
+__global__ void __launch_bounds__(512, NV * EPV <= 16 ? 2 : 1) k_rms_bwd(const __grid_constant__ BwdArgs a, int wpr) {
   __shared__ float red[2][MAX_WARPS];
+  extern __shared__ float sums[];  // [H] where the block has several groups
   const int lane = threadIdx.x & 31, wb = threadIdx.x >> 5;
   const int rpb = blockDim.x / 32 / wpr;
-  const int group = wb / wpr, w = wb % wpr;
+  const int group = wb / wpr, w = wb - group * wpr;
   const int64_t g0 = (int64_t)blockIdx.x * rpb + group, step = (int64_t)gridDim.x * rpb;
-  float wt[NV][EPV], dw[NV][EPV];
+  Raw<T, EPV> wt[NV];
+  float dw[NV][EPV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
+    wt[j].zero();
+    if (c < a.H) wt[j].load((const T*)a.w + c);
 #pragma unroll
-    for (int e = 0; e < EPV; ++e) wt[j][e] = dw[j][e] = 0.0f;
-    if (c < a.H) {
-      Vec<T, EPV>::load((const T*)a.w + c, wt[j]);
-#pragma unroll
-      for (int e = 0; e < EPV; ++e) wt[j][e] += a.off;
-    }
+    for (int e = 0; e < EPV; ++e) dw[j][e] = 0.0f;
   }
   int buf = 0;
   // every group of the block takes the same number of turns (the sums hold barriers)
@@ -193,29 +192,40 @@ __global__ void __launch_bounds__(512) k_rms_bwd(const __grid_constant__ BwdArgs
   for (int64_t t = 0; t < turns; ++t, buf ^= 1) {
     const int64_t row = g0 + t * step;
     const bool live = row < a.N;
+    Raw<T, EPV> dy[NV], dh[NV];
+    typename std::conditional<Q8, RawQ<EPV>, Raw<T, EPV>>::type h[NV];
+    float f[NV];  // what h is multiplied by to give xhat
     const float rstd = live ? a.rstd[row] : 0.0f;
-    float dy[NV][EPV], xh[NV][EPV];
-    float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
+      f[j] = rstd;
+      dy[j].zero();
+      dh[j].zero();
 #pragma unroll
-      for (int e = 0; e < EPV; ++e) dy[j][e] = xh[j][e] = 0.0f;
+      for (int i = 0; i < h[j].W; ++i) h[j].w[i] = 0u;
       if (live && c < a.H) {
-        Vec<T, EPV>::load((const T*)a.dy + row * a.lddy + c, dy[j]);
-        float f = rstd;
+        dy[j].load((const T*)a.dy + row * a.lddy + c);
         if constexpr (Q8) {
-          q_load<EPV>(a.h8 + row * a.ldh8 + c, xh[j]);
-          f *= a.h8s[row * a.nblk + c / Q_BLOCK];
+          h[j].load(a.h8 + row * a.ldh8 + c);
+          f[j] = a.h8s[row * a.nblk + c / Q_BLOCK];
         } else {
-          Vec<T, EPV>::load((const T*)a.h + row * a.ldh + c, xh[j]);
+          h[j].load((const T*)a.h + row * a.ldh + c);
         }
+        if (a.dh != nullptr) dh[j].load((const T*)a.dh + row * a.lddh + c);
+      }
+    }
+    float dot = 0.0f;
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-          xh[j][e] *= f;
-          dot = fmaf(dy[j][e] * wt[j][e], xh[j][e], dot);
-          dw[j][e] = fmaf(dy[j][e], xh[j][e], dw[j][e]);
-        }
+    for (int j = 0; j < NV; ++j) {
+      if constexpr (Q8) f[j] *= rstd;
+      float xh[EPV];
+      h[j].unpack(xh);
+#pragma unroll
+      for (int e = 0; e < EPV; ++e) {
+        const float d = dy[j].get(e), x = xh[e] * f[j];
+        dot = fmaf(d * (wt[j].get(e) + a.off), x, dot);
+        dw[j][e] = fmaf(d, x, dw[j][e]);
       }
     }
     const float m = group_sum(dot, red[buf], wpr, wb, group) * a.inv_h;
@@ -224,28 +234,35 @@ __global__ void __launch_bounds__(512) k_rms_bwd(const __grid_constant__ BwdArgs
     for (int j = 0; j < NV; ++j) {
       const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
       if (c < a.H) {
-        float o[EPV];
+        float xh[EPV], o[EPV];
+        h[j].unpack(xh);
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) o[e] = rstd * (dy[j][e] * wt[j][e] - xh[j][e] * m);
-        if (a.dh != nullptr) {
-          float d[EPV];
-          Vec<T, EPV>::load((const T*)a.dh + row * a.lddh + c, d);
-#pragma unroll
-          for (int e = 0; e < EPV; ++e) o[e] += d[e];
+        for (int e = 0; e < EPV; ++e) {
+          o[e] = rstd * (dy[j].get(e) * (wt[j].get(e) + a.off) - xh[e] * f[j] * m);
+          if (a.dh != nullptr) o[e] += dh[j].get(e);
         }
         Vec<T, EPV>::store((T*)a.dx + row * a.lddx + c, o);
       }
     }
   }
-  if (a.part != nullptr) {
+  if (a.part == nullptr) return;
+  float* out = a.part + (int64_t)blockIdx.x * a.H;
+  for (int g = 0; g < rpb; ++g) {
+    if (group == g) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
-      if (c < a.H) {
+      for (int j = 0; j < NV; ++j) {
+        const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
+        if (c < a.H) {
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) a.part[g0 * a.H + c + e] = dw[j][e];
+          for (int e = 0; e < EPV; ++e) {
+            const float u = g == 0 ? dw[j][e] : sums[c + e] + dw[j][e];
+            if (g == rpb - 1) out[c + e] = u;
+            else sums[c + e] = u;
+          }
+        }
       }
     }
+    if (g < rpb - 1) __syncthreads();
   }
 }
 
@@ -287,22 +304,24 @@ __global__ void __launch_bounds__(256) k_rms_dw_long(const __grid_constant__ Bwd
   a.part[(int64_t)blockIdx.y * a.H + c] = s;
 }
 
-// dweight (+)= sum of the partial rows, in a fixed order: a block takes 32 columns, its
-// eight warps every eighth row, then the eight sums are added in warp order.
+// dweight (+)= sum of the partial rows, in a fixed order: a block takes 32 columns, its 32
+// warps every 32nd row, then the 32 sums are added in warp order.
 template <typename D>
-__global__ void __launch_bounds__(256) k_rms_dw_sum(const float* part, int64_t rows, int64_t H, D* dw, bool ovw) {
-  __shared__ float s[8][32];
+__global__ void __launch_bounds__(1024) k_rms_dw_sum(const float* part, int64_t rows, int64_t H, D* dw, bool ovw) {
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float t = 0.0f;
-  if (c < H)
-    for (int64_t r = w; r < rows; r += 8) t += part[r * H + c];
+  if (c < H) {
+#pragma unroll 4
+    for (int64_t r = w; r < rows; r += 32) t += part[r * H + c];
+  }
   s[w][lane] = t;
   __syncthreads();
   if (w == 0 && c < H) {
     float u = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u += s[i][lane];
+    for (int i = 0; i < 32; ++i) u += s[i][lane];
     dw[c] = from_f<D>(ovw ? u : to_f<D>(dw[c]) + u);
   }
 }
@@ -310,79 +329,82 @@ __global__ void __launch_bounds__(256) k_rms_dw_sum(const float* part, int64_t r
 constexpr int BWD_BLOCKS_PER_SM = 2;
 constexpr int LONG_DW_ROWS = 64;  // row groups of k_rms_dw_long
 
+// Rows that take 32-byte, 16-byte or single-element accesses.
+enum Width { W32, W16, W1 };
+
 // Warps per row and vectors per thread of a row of H elements in vectors of EPV: the fewest
-// warps that hold it; 0 when none does.
+// warps with 16 elements a thread (8 as single elements), else 16 warps with 32 (16) elements;
+// 0 when none holds it.
 struct Shape {
   int wpr, nv;
 };
 Shape row_shape(int64_t H, int epv) {
   const int64_t nvec = cdiv64(H, epv);
-  const int small = epv == 1 ? 8 : 2, large = epv == 1 ? 16 : 4;
-  for (int wpr = 1; wpr <= 16; wpr *= 2)
-    if ((int64_t)wpr * 32 * small >= nvec) return {wpr, small};
-  if ((int64_t)16 * 32 * large >= nvec) return {16, large};
+  const int small = epv == 1 ? 8 : 16 / epv, large = 2 * small;
+  if (cdiv64(nvec, 32 * small) <= 16) return {(int)cdiv64(nvec, 32 * small), small};
+  if (cdiv64(nvec, 32 * large) <= 16) return {16, large};
   return {0, 0};
 }
 
-// Rows in the dweight partials of a backward over N rows: at most one per row group of the
-// largest grid.
-int64_t partial_rows(int64_t N) {
-  const int64_t most = (int64_t)num_sms() * BWD_BLOCKS_PER_SM * 16;
-  const int64_t rows = N < most ? N + 16 : most;
-  return rows > LONG_DW_ROWS ? rows : LONG_DW_ROWS;
+// Rows of the dweight partials: at most one per block of the largest grid.
+int64_t partial_rows() {
+  const int64_t most = (int64_t)num_sms() * BWD_BLOCKS_PER_SM;
+  return most > LONG_DW_ROWS ? most : LONG_DW_ROWS;
 }
 
-template <typename T, int EPV, int NV>
-void launch_fwd(const FwdArgs& a, int wpr, cudaStream_t s) {
-  const int threads = wpr * 32 < 128 ? 128 : wpr * 32;
-  const int64_t rpb = threads / 32 / wpr;
-  k_rms_fwd<T, EPV, NV><<<(unsigned)cdiv64(a.N, rpb), threads, 0, s>>>(a, wpr);
-}
-
-template <typename T>
-cudaError_t fwd(const FwdArgs& a, bool wide, cudaStream_t s) {
-  constexpr int W = 16 / sizeof(T);
-  const Shape p = row_shape(a.H, wide ? W : 1);
+template <typename T, int EPV>
+cudaError_t fwd_w(const FwdArgs& a, cudaStream_t s) {
+  constexpr int NV = EPV == 1 ? 8 : 16 / EPV;
+  const Shape p = row_shape(a.H, EPV);
   if (p.wpr == 0) {
     k_rms_fwd_long<T><<<(unsigned)a.N, 512, 0, s>>>(a);
-  } else if (wide) {
-    if (p.nv == 2) launch_fwd<T, W, 2>(a, p.wpr, s);
-    else launch_fwd<T, W, 4>(a, p.wpr, s);
   } else {
-    if (p.nv == 8) launch_fwd<T, 1, 8>(a, p.wpr, s);
-    else launch_fwd<T, 1, 16>(a, p.wpr, s);
+    const int64_t rpb = p.wpr >= 4 ? 1 : 4 / p.wpr;
+    const unsigned blocks = (unsigned)cdiv64(a.N, rpb);
+    const int threads = (int)rpb * p.wpr * 32;
+    if (p.nv == NV) k_rms_fwd<T, EPV, NV><<<blocks, threads, 0, s>>>(a, p.wpr);
+    else k_rms_fwd<T, EPV, 2 * NV><<<blocks, threads, 0, s>>>(a, p.wpr);
   }
   return cudaGetLastError();
 }
-
-// Grid of the backward and the number of partial rows it writes.
-template <typename T, int EPV, int NV>
-int64_t launch_bwd(const BwdArgs& a, int wpr, cudaStream_t s) {
-  const int threads = 512;
-  const int64_t rpb = threads / 32 / wpr;
-  int64_t blocks = (int64_t)num_sms() * BWD_BLOCKS_PER_SM;
-  if (blocks > cdiv64(a.N, rpb)) blocks = cdiv64(a.N, rpb);
-  if (a.h8 != nullptr) k_rms_bwd<T, EPV, NV, true><<<(unsigned)blocks, threads, 0, s>>>(a, wpr);
-  else k_rms_bwd<T, EPV, NV, false><<<(unsigned)blocks, threads, 0, s>>>(a, wpr);
-  return blocks * rpb;
+template <typename T>
+cudaError_t fwd(const FwdArgs& a, Width w, cudaStream_t s) {
+  constexpr int E = 16 / sizeof(T);
+  return w == W32 ? fwd_w<T, 2 * E>(a, s) : w == W16 ? fwd_w<T, E>(a, s) : fwd_w<T, 1>(a, s);
 }
 
-template <typename T>
-cudaError_t bwd(const BwdArgs& a, bool wide, int64_t& part_rows, cudaStream_t s) {
-  constexpr int W = 16 / sizeof(T);
-  const Shape p = row_shape(a.H, wide ? W : 1);
+template <typename T, int EPV, int NV>
+int64_t launch_bwd(const BwdArgs& a, int wpr, cudaStream_t s) {
+  const int64_t rpb = 16 / wpr;
+  const int threads = (int)rpb * wpr * 32;
+  const size_t smem = rpb > 1 ? (size_t)a.H * 4 : 0;
+  int64_t blocks = (int64_t)num_sms() * BWD_BLOCKS_PER_SM;
+  if (blocks > cdiv64(a.N, rpb)) blocks = cdiv64(a.N, rpb);
+  if (a.h8 != nullptr) k_rms_bwd<T, EPV, NV, true><<<(unsigned)blocks, threads, smem, s>>>(a, wpr);
+  else k_rms_bwd<T, EPV, NV, false><<<(unsigned)blocks, threads, smem, s>>>(a, wpr);
+  return blocks;
+}
+template <typename T, int EPV>
+cudaError_t bwd_w(const BwdArgs& a, int64_t& part_rows, cudaStream_t s) {
+  constexpr int NV = EPV == 1 ? 8 : 16 / EPV;
+  const Shape p = row_shape(a.H, EPV);
   if (p.wpr == 0) {
     if (a.dx != nullptr) k_rms_bwd_long<T><<<(unsigned)a.N, 512, 0, s>>>(a);
     if (a.part != nullptr) {
       part_rows = LONG_DW_ROWS;
       k_rms_dw_long<T><<<dim3((unsigned)cdiv64(a.H, 256), LONG_DW_ROWS), 256, 0, s>>>(a);
     }
-  } else if (wide) {
-    part_rows = p.nv == 2 ? launch_bwd<T, W, 2>(a, p.wpr, s) : launch_bwd<T, W, 4>(a, p.wpr, s);
   } else {
-    part_rows = p.nv == 8 ? launch_bwd<T, 1, 8>(a, p.wpr, s) : launch_bwd<T, 1, 16>(a, p.wpr, s);
+    part_rows = p.nv == NV ? launch_bwd<T, EPV, NV>(a, p.wpr, s) : launch_bwd<T, EPV, 2 * NV>(a, p.wpr, s);
   }
   return cudaGetLastError();
+}
+template <typename T>
+cudaError_t bwd(const BwdArgs& a, Width w, int64_t& part_rows, cudaStream_t s) {
+  constexpr int E = 16 / sizeof(T);
+  return w == W32   ? bwd_w<T, 2 * E>(a, part_rows, s)
+         : w == W16 ? bwd_w<T, E>(a, part_rows, s)
+                    : bwd_w<T, 1>(a, part_rows, s);
 }
 
 bool sizes_ok(int64_t N, int64_t H) { return N >= 0 && H >= 1 && N <= 0x7fffffffLL && H <= 0x7fffffffLL; }
@@ -431,22 +453,26 @@ extern "C" int32_t flce_rmsnorm_fwd(const flce_rmsnorm_args* x, void* stream) {
   a.ldh8 = x->ldh8;
   a.h8s = x->h8_scale;
   a.nblk = cdiv64(H, Q_BLOCK);
-  const int epv = 16 / esz;
-  const bool wide = H % epv == 0 && rows16(a.x, a.ldx, esz) && (!a.res || rows16(a.res, a.ldres, esz)) &&
-                    aligned_to(a.w, 16) && (!a.h || rows16(a.h, a.ldh, esz)) && (!a.y || rows16(a.y, a.ldy, esz)) &&
-                    (!a.y8 || (aligned_to(a.y8, epv) && a.ldy8 % epv == 0)) &&
-                    (!a.h8 || (aligned_to(a.h8, epv) && a.ldh8 % epv == 0));
+  // the widest accesses that every operand's rows allow
+  auto fits = [&](int bytes) {
+    const int e = bytes / esz;  // elements, and bytes of the 8-bit rows
+    return H % e == 0 && rows_by(a.x, a.ldx, esz, bytes) && (!a.res || rows_by(a.res, a.ldres, esz, bytes)) &&
+           aligned_to(a.w, bytes) && (!a.h || rows_by(a.h, a.ldh, esz, bytes)) &&
+           (!a.y || rows_by(a.y, a.ldy, esz, bytes)) && (!a.y8 || rows_by(a.y8, a.ldy8, 1, e)) &&
+           (!a.h8 || rows_by(a.h8, a.ldh8, 1, e));
+  };
+  const Width w = fits(32) ? W32 : fits(16) ? W16 : W1;
   cudaStream_t s = (cudaStream_t)stream;
   switch (x->dtype) {
-    case FLCE_F32: return cuda_status(fwd<float>(a, wide, s));
-    case FLCE_BF16: return cuda_status(fwd<__nv_bfloat16>(a, wide, s));
-    default: return cuda_status(fwd<__half>(a, wide, s));
+    case FLCE_F32: return cuda_status(fwd<float>(a, w, s));
+    case FLCE_BF16: return cuda_status(fwd<__nv_bfloat16>(a, w, s));
+    default: return cuda_status(fwd<__half>(a, w, s));
   }
 }
 
 extern "C" size_t flce_rmsnorm_workspace_size(int64_t N, int64_t H) {
   if (!sizes_ok(N, H)) return 0;
-  return round_up((size_t)partial_rows(N) * (size_t)H * 4, 256);
+  return round_up((size_t)partial_rows() * (size_t)H * 4, 256);
 }
 
 extern "C" int32_t flce_rmsnorm_bwd(const flce_rmsnorm_bwd_args* x, void* stream) {
@@ -492,24 +518,27 @@ extern "C" int32_t flce_rmsnorm_bwd(const flce_rmsnorm_bwd_args* x, void* stream
   a.dx = x->dx;
   a.lddx = x->lddx;
   a.part = x->dweight ? (float*)x->workspace : nullptr;
-  const int epv = 16 / esz;
-  const bool wide = H % epv == 0 && rows16(a.dy, a.lddy, esz) && (!a.h || rows16(a.h, a.ldh, esz)) &&
-                    (!a.h8 || (aligned_to(a.h8, epv) && a.ldh8 % epv == 0)) && aligned_to(a.w, 16) &&
-                    (!a.dh || rows16(a.dh, a.lddh, esz)) && (!a.dx || rows16(a.dx, a.lddx, esz));
+  auto fits = [&](int bytes) {
+    const int e = bytes / esz;
+    return H % e == 0 && rows_by(a.dy, a.lddy, esz, bytes) && (!a.h || rows_by(a.h, a.ldh, esz, bytes)) &&
+           (!a.h8 || rows_by(a.h8, a.ldh8, 1, e)) && aligned_to(a.w, bytes) &&
+           (!a.dh || rows_by(a.dh, a.lddh, esz, bytes)) && (!a.dx || rows_by(a.dx, a.lddx, esz, bytes));
+  };
+  const Width w = fits(32) ? W32 : fits(16) ? W16 : W1;
   int64_t rows = 0;
   cudaError_t e;
   switch (x->dtype) {
-    case FLCE_F32: e = bwd<float>(a, wide, rows, s); break;
-    case FLCE_BF16: e = bwd<__nv_bfloat16>(a, wide, rows, s); break;
-    default: e = bwd<__half>(a, wide, rows, s); break;
+    case FLCE_F32: e = bwd<float>(a, w, rows, s); break;
+    case FLCE_BF16: e = bwd<__nv_bfloat16>(a, w, rows, s); break;
+    default: e = bwd<__half>(a, w, rows, s); break;
   }
   if (e != cudaSuccess || !x->dweight) return cuda_status(e);
   const unsigned blocks = (unsigned)cdiv64(H, 32);
   if (x->dweight_dtype == FLCE_F32)
-    k_rms_dw_sum<float><<<blocks, 256, 0, s>>>(a.part, rows, H, (float*)x->dweight, ovw);
+    k_rms_dw_sum<float><<<blocks, 1024, 0, s>>>(a.part, rows, H, (float*)x->dweight, ovw);
   else if (x->dweight_dtype == FLCE_BF16)
-    k_rms_dw_sum<__nv_bfloat16><<<blocks, 256, 0, s>>>(a.part, rows, H, (__nv_bfloat16*)x->dweight, ovw);
+    k_rms_dw_sum<__nv_bfloat16><<<blocks, 1024, 0, s>>>(a.part, rows, H, (__nv_bfloat16*)x->dweight, ovw);
   else
-    k_rms_dw_sum<__half><<<blocks, 256, 0, s>>>(a.part, rows, H, (__half*)x->dweight, ovw);
+    k_rms_dw_sum<__half><<<blocks, 1024, 0, s>>>(a.part, rows, H, (__half*)x->dweight, ovw);
   return cuda_status(cudaGetLastError());
 }

@@ -4,6 +4,8 @@
 
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "flce_internal.cuh"
 
 namespace flce {
@@ -16,54 +18,98 @@ inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t round_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
 inline bool valid_dtype(int32_t dt) { return dt == FLCE_F32 || dt == FLCE_BF16 || dt == FLCE_F16; }
 inline bool aligned_to(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
-// Base and pitch of a row-major matrix allow 16-byte accesses to every row.
-inline bool rows16(const void* p, int64_t ld, int esz) {
-  return aligned_to(p, 16) && (size_t)ld * esz % 16 == 0;
+// Base and pitch of a row-major matrix allow accesses of `bytes` bytes in every row.
+inline bool rows_by(const void* p, int64_t ld, int esz, size_t bytes) {
+  return aligned_to(p, bytes) && (size_t)ld * esz % bytes == 0;
 }
+inline bool rows16(const void* p, int64_t ld, int esz) { return rows_by(p, ld, esz, 16); }
 
-// EPV consecutive elements as fp32: one 16-byte access (EPV * sizeof(T) == 16), one 8-byte
-// access, or single elements (EPV == 1).
+// EPV consecutive elements of a row as they lie in memory: 32 or 16 bytes in one access, or a
+// single element (EPV == 1).
 template <typename T, int EPV>
-struct Vec {
-  static_assert(EPV == 1 || EPV * sizeof(T) == 16, "vector width");
-  static __device__ __forceinline__ void load(const T* p, float (&v)[EPV]) {
+struct Raw {
+  static constexpr int BYTES = EPV * (int)sizeof(T);
+  static_assert(EPV == 1 || BYTES == 32 || BYTES == 16, "vector width");
+  static constexpr int W = EPV == 1 ? 1 : BYTES / 4;
+  uint32_t w[W];
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const T* p) {
     if constexpr (EPV == 1) {
-      v[0] = to_f<T>(*p);
+      if constexpr (sizeof(T) == 4) w[0] = *(const uint32_t*)p;
+      else w[0] = *(const uint16_t*)p;
+    } else if constexpr (BYTES == 32) {
+      asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                   : "l"(p)
+                   : "memory");
     } else {
       const uint4 u = *(const uint4*)p;
-      unpack(u, v);
+      w[0] = u.x;
+      w[1] = u.y;
+      w[2] = u.z;
+      w[3] = u.w;
     }
   }
-  static __device__ __forceinline__ void unpack(const uint4& u, float (&v)[EPV]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 4) {
-        v[i] = __uint_as_float(w[i]);
-      } else {
-        const T* h = (const T*)&w[i];
-        v[2 * i] = to_f<T>(h[0]);
-        v[2 * i + 1] = to_f<T>(h[1]);
-      }
-    }
-  }
-  static __device__ __forceinline__ void store(T* p, const float (&v)[EPV]) {
+  __device__ __forceinline__ void store(T* p) const {
     if constexpr (EPV == 1) {
-      *p = from_f<T>(v[0]);
+      if constexpr (sizeof(T) == 4) *(uint32_t*)p = w[0];
+      else *(uint16_t*)p = (uint16_t)w[0];
+    } else if constexpr (BYTES == 32) {
+      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                   "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                   : "memory");
     } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4) {
-          w[i] = __float_as_uint(v[i]);
-        } else {
-          T* h = (T*)&w[i];
-          h[0] = from_f<T>(v[2 * i]);
-          h[1] = from_f<T>(v[2 * i + 1]);
-        }
-      }
       *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
     }
+  }
+  __device__ __forceinline__ float get(int e) const {  // e is a compile-time constant where it is called
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[e]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      return __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+    } else {
+      const __half2 h = *(const __half2*)&w[e >> 1];
+      return e & 1 ? __high2float(h) : __low2float(h);
+    }
+  }
+  __device__ __forceinline__ void unpack(float (&v)[EPV]) const {
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) v[e] = get(e);
+  }
+  __device__ __forceinline__ void pack(const float (&v)[EPV]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = __float_as_uint(v[i]);
+    } else if constexpr (EPV == 1) {
+      const T t = from_f<T>(v[0]);
+      w[0] = *(const uint16_t*)&t;
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        T* h = (T*)&w[i];
+        h[0] = from_f<T>(v[2 * i]);
+        h[1] = from_f<T>(v[2 * i + 1]);
+      }
+    }
+  }
+};
+
+// The same as fp32 values.
+template <typename T, int EPV>
+struct Vec {
+  static __device__ __forceinline__ void load(const T* p, float (&v)[EPV]) {
+    Raw<T, EPV> r;
+    r.load(p);
+    r.unpack(v);
+  }
+  static __device__ __forceinline__ void store(T* p, const float (&v)[EPV]) {
+    Raw<T, EPV> r;
+    r.pack(v);
+    r.store(p);
   }
 };
 
@@ -77,13 +123,6 @@ __device__ __forceinline__ float warp_sum(float v) {
 constexpr int Q_BLOCK = 128;
 constexpr int Q_MIN_EXP = -117;  // 2^-117 times e4m3's smallest value 2^-9 is still normal in fp32 and bf16
 
-// The value to be stored for x: infinities become NaN (e4m3 has none).
-__device__ __forceinline__ float q_input(float x) { return fabsf(x) < INFINITY ? x : NAN; }
-// Its share in the block's maximum: non-finite values take no part.
-__device__ __forceinline__ float q_abs(float x) {
-  const float a = fabsf(x);
-  return a < INFINITY ? a : 0.0f;
-}
 // Exponent e of the smallest power of two 2^e >= 2^Q_MIN_EXP with amax <= 448 * 2^e; 448 =
 // 1.75 * 2^8, so e = exponent(amax) - 8, one more where amax's significand is over 1.75.
 __device__ __forceinline__ int q_exponent(float amax) {
@@ -108,9 +147,50 @@ __device__ __forceinline__ float2 q_unpack2(uint32_t u) {
   return __half22float2(*(const __half2*)&h);
 }
 
+// EPV e4m3 values as they lie in memory.
+template <int EPV>
+struct RawQ {
+  static_assert(EPV == 16 || EPV == 8 || EPV == 4 || EPV == 1, "vector width");
+  static constexpr int W = EPV < 4 ? 1 : EPV / 4;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    if constexpr (EPV == 16) {
+      const uint4 u = *(const uint4*)p;
+      w[0] = u.x;
+      w[1] = u.y;
+      w[2] = u.z;
+      w[3] = u.w;
+    } else if constexpr (EPV == 8) {
+      const uint2 u = *(const uint2*)p;
+      w[0] = u.x;
+      w[1] = u.y;
+    } else if constexpr (EPV == 4) {
+      w[0] = *(const uint32_t*)p;
+    } else {
+      w[0] = *p;
+    }
+  }
+  __device__ __forceinline__ void unpack(float (&v)[EPV]) const {
+    if constexpr (EPV == 1) {
+      v[0] = q_unpack2(w[0]).x;
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const float2 a = q_unpack2(w[i]), b = q_unpack2(w[i] >> 16);
+        v[4 * i] = a.x;
+        v[4 * i + 1] = a.y;
+        v[4 * i + 2] = b.x;
+        v[4 * i + 3] = b.y;
+      }
+    }
+  }
+};
 template <int EPV>
 __device__ __forceinline__ void q_store(uint8_t* p, const float (&v)[EPV]) {
-  if constexpr (EPV == 8) {
+  if constexpr (EPV == 16) {
+    *(uint4*)p = make_uint4(q_pack4(v[0], v[1], v[2], v[3]), q_pack4(v[4], v[5], v[6], v[7]),
+                            q_pack4(v[8], v[9], v[10], v[11]), q_pack4(v[12], v[13], v[14], v[15]));
+  } else if constexpr (EPV == 8) {
     *(uint2*)p = make_uint2(q_pack4(v[0], v[1], v[2], v[3]), q_pack4(v[4], v[5], v[6], v[7]));
   } else if constexpr (EPV == 4) {
     *(uint32_t*)p = q_pack4(v[0], v[1], v[2], v[3]);
@@ -118,51 +198,43 @@ __device__ __forceinline__ void q_store(uint8_t* p, const float (&v)[EPV]) {
     *p = q_pack1(v[0]);
   }
 }
-template <int EPV>
-__device__ __forceinline__ void q_load(const uint8_t* p, float (&v)[EPV]) {
-  if constexpr (EPV == 8) {
-    const uint2 u = *(const uint2*)p;
-    const uint32_t w[2] = {u.x, u.y};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float2 a = q_unpack2(w[i]), b = q_unpack2(w[i] >> 16);
-      v[4 * i] = a.x;
-      v[4 * i + 1] = a.y;
-      v[4 * i + 2] = b.x;
-      v[4 * i + 3] = b.y;
-    }
-  } else if constexpr (EPV == 4) {
-    const uint32_t w = *(const uint32_t*)p;
-    const float2 a = q_unpack2(w), b = q_unpack2(w >> 16);
-    v[0] = a.x;
-    v[1] = a.y;
-    v[2] = b.x;
-    v[3] = b.y;
-  } else {
-    v[0] = q_unpack2(*p).x;
-  }
-}
 
 // A row held by a group of warps: warp w of the group holds vectors (w * NV + j) * 32 + lane,
 // j < NV, of EPV elements each, so that every access of a warp is contiguous and a 128-column
-// block lies in 16 lanes (EPV 8), one vector of a warp (EPV 4) or four vectors (EPV 1).
+// block lies in 128 / EPV neighbouring lanes (EPV 16, 8, 4) or four vectors of a warp (EPV 1).
 // Quantises such a row piece: block maxima of |v| by shuffles, then e4m3 values to q and one
-// scale per block (the power of two times `factor`) to s. cols[j]: first column of vector j.
+// scale per block (the power of two times `factor`) to s. A NaN takes no part in a maximum
+// (fmaxf) and is stored as NaN; a warp that meets an infinity makes the maxima again without
+// it and stores NaN for it (e4m3 has no infinity).
 template <int EPV, int NV>
 __device__ __forceinline__ void q_row_piece(const float (&v)[NV][EPV], int warp, int lane, int64_t H, uint8_t* q,
                                             float* s, float factor) {
   static_assert(EPV != 1 || NV % 4 == 0, "a block of single elements spans four vectors");
-  constexpr int JB = EPV == 1 ? 4 : 1;      // vectors per block
-  constexpr int LB = EPV == 8 ? 16 : 32;    // lanes per block
+  constexpr int JB = EPV == 1 ? 4 : 1;                // vectors per block
+  constexpr int LB = EPV == 1 ? 32 : Q_BLOCK / EPV;   // lanes per block
 #pragma unroll
   for (int j0 = 0; j0 < NV; j0 += JB) {
     float m = 0.0f;
 #pragma unroll
     for (int j = j0; j < j0 + JB; ++j)
 #pragma unroll
-      for (int e = 0; e < EPV; ++e) m = fmaxf(m, q_abs(v[j][e]));
+      for (int e = 0; e < EPV; ++e) m = fmaxf(m, fabsf(v[j][e]));
 #pragma unroll
     for (int o = LB / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    bool inf = false;
+    if (__any_sync(0xffffffffu, m == INFINITY)) {
+      inf = true;
+      m = 0.0f;
+#pragma unroll
+      for (int j = j0; j < j0 + JB; ++j)
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) {
+          const float a = fabsf(v[j][e]);
+          m = fmaxf(m, a < INFINITY ? a : 0.0f);
+        }
+#pragma unroll
+      for (int o = LB / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
     const int e2 = q_exponent(m);
     const float inv = exp2_int(-e2);
     const int64_t c0 = ((int64_t)(warp * NV + j0) * 32 + lane) * EPV;
@@ -172,7 +244,11 @@ __device__ __forceinline__ void q_row_piece(const float (&v)[NV][EPV], int warp,
       if (c < H) {
         float o[EPV];
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) o[e] = q_input(v[j][e]) * inv;
+        for (int e = 0; e < EPV; ++e) o[e] = v[j][e] * inv;
+        if (inf) {
+#pragma unroll
+          for (int e = 0; e < EPV; ++e) o[e] = fabsf(o[e]) < INFINITY ? o[e] : NAN;
+        }
         q_store<EPV>(q + c, o);
       }
     }
