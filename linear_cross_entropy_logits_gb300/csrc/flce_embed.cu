@@ -10,6 +10,8 @@
 // on every run. Bound by HBM: dout once, the touched rows of dE read and written once.
 #include <math.h>
 
+#include <atomic>
+
 #include "flce_ops.cuh"
 
 namespace flce {
@@ -74,19 +76,22 @@ cudaError_t fwd(const flce_embed_args& a, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------------ sort
-// Stable radix sort of (token, position) by one cluster of CTAS blocks (one block for short
-// lists: no cluster barriers, no distributed shared memory). Keys are the tokens, V for ignored
-// and out-of-range ones (they sort last and are left out). Each block owns a contiguous share
-// of the list, each of its warps a contiguous part of that; a pass counts the digits per warp,
-// adds the counts up over the warps, the blocks (through distributed shared memory) and the
-// digits, and scatters each pair to its place. Sixteen warps a block: more would lengthen the
-// sums over the warps, which is what a pass over a short list consists of.
+// Stable radix sort of (token, position) by one cluster of blocks. Keys are the tokens, V for
+// ignored and out-of-range ones (they sort last and are left out). Each warp owns a contiguous
+// part of the list; a pass counts the digits per warp, adds the counts up over the warps, the
+// blocks (through distributed shared memory) and the digits, and scatters each pair to its
+// place. Two passes of up to 10 bits do for a vocabulary below 2^20.
+//
+// Short lists are bound by latency: k_sort_reg keeps its pairs and their ranks in registers and
+// passes the pairs on through the cluster's shared memory (8192 tokens: 9 us; with the pairs in
+// L2 and ranked twice a pass: 15 us). One block without cluster barriers takes up to 1024
+// tokens. k_sort takes lists of any length, with the pairs in L2.
 constexpr int SORT_CTAS = 8;
 constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
-constexpr int SORT_ONE = 1024;  // longest list for a single block: two tiles of 32 per warp
-constexpr int MAX_BINS = 512;
-static_assert(MAX_BINS <= SORT_THREADS, "a thread per digit");
+constexpr int MAX_BITS = 10;
+constexpr int MAX_BINS = 1 << MAX_BITS;
+constexpr int BPT = MAX_BINS / SORT_THREADS;  // digits per thread
 
 struct SortArgs {
   const int64_t* tokens;
@@ -94,8 +99,8 @@ struct SortArgs {
   int64_t V;
   int N;
   int passes, bits;    // passes of `bits` bits each
-  uint32_t *k0, *p0;   // ping
-  uint32_t *k1, *p1;   // pong
+  uint32_t *k0, *p0;   // sorted keys and positions
+  uint32_t *k1, *p1;   // the other list of k_sort, which starts in the one that makes it end in k0
   int* status;
   int* count;          // [pieces][slices] zeroed for k_embed_sum
   int ncount;
@@ -111,123 +116,242 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ uint32_t ld_remote(const uint32_t* p, uint32_t rank) {
-  uint32_t a, v;
+__device__ __forceinline__ uint32_t remote_addr(const void* p, uint32_t rank) {
+  uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return a;
+}
+__device__ __forceinline__ uint32_t ld_remote(const uint32_t* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote_addr(p, rank)) : "memory");
   return v;
 }
-
 template <int CTAS>
 __device__ __forceinline__ void sort_barrier() {
   if constexpr (CTAS > 1) cluster_barrier();
   else __syncthreads();
 }
 
+// The key of position i: its token, V where that takes no part.
+__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int i) {
+  const int64_t t = a.tokens[i];
+  const bool live = t >= 0 && t < a.V && t != a.ignore_index;
+  if (!live && t != a.ignore_index && a.status != nullptr) atomicOr(a.status, ST_TARGET_RANGE);
+  return live ? (uint32_t)t : (uint32_t)a.V;
+}
+__device__ __forceinline__ void mark_used(const SortArgs& a, uint32_t key) {
+  if (a.used != nullptr && key < (uint32_t)a.V) atomicOr(a.used + (key >> 5), 1u << (key & 31));
+}
+
+// The lanes of `act` whose digit (of `bits` bits) is this lane's: a ballot per bit (the match
+// instruction takes a step per different digit: 1500 cycles for a tile of each of 32 warps).
+__device__ __forceinline__ unsigned same_digit(unsigned act, uint32_t d, int bits) {
+  unsigned peers = act;
+#pragma unroll
+  for (int b = 0; b < MAX_BITS; ++b) {
+    if (b < bits) {
+      const unsigned m = __ballot_sync(act, d >> b & 1u);
+      peers &= d >> b & 1u ? m : ~m;
+    }
+  }
+  return peers;
+}
+
+// Turns the warps' digit counts hist[w][bin] into the places of their first elements: sums over
+// the warps, the blocks of the cluster, and the digits before. Thread t has digits t * BPT ....
 template <int CTAS>
-__global__ void __launch_bounds__(SORT_THREADS, 1) k_sort(const __grid_constant__ SortArgs a) {
-  __shared__ uint32_t hist[SORT_WARPS][MAX_BINS];
-  __shared__ uint32_t tot[MAX_BINS];   // this block's digit counts
-  __shared__ uint32_t wsum[MAX_BINS / 32];
+__device__ __forceinline__ void sort_places(uint32_t* hist, uint32_t* tot, uint32_t* wsum, int bins, int rank) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = CTAS > 1 ? (int)cluster_rank() : 0;
-  const int bins = 1 << a.bits;
-  const uint32_t mask = (uint32_t)bins - 1;
-  for (int i = rank * SORT_THREADS + tid; i < a.ncount; i += CTAS * SORT_THREADS) a.count[i] = 0;
+  uint32_t own[BPT], before[BPT], all[BPT], sum = 0;
+#pragma unroll
+  for (int i = 0; i < BPT; ++i) {
+    const int b = tid * BPT + i;
+    own[i] = before[i] = all[i] = 0;
+    if (b < bins) {
+#pragma unroll
+      for (int w = 0; w < SORT_WARPS; ++w) own[i] += hist[w * bins + b];
+      if (CTAS > 1) tot[b] = own[i];
+    }
+  }
+  if constexpr (CTAS > 1) {
+    cluster_barrier();
+#pragma unroll
+    for (int i = 0; i < BPT; ++i) {
+      const int b = tid * BPT + i;
+      if (b < bins) {
+#pragma unroll
+        for (int c = 0; c < CTAS; ++c) {
+          const uint32_t v = ld_remote(tot + b, c);
+          before[i] += c < rank ? v : 0;
+          all[i] += v;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < BPT; ++i) all[i] = own[i];
+  }
+#pragma unroll
+  for (int i = 0; i < BPT; ++i) sum += all[i];
+  uint32_t x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) wsum[warp] = x;
+  __syncthreads();
+  uint32_t base = x - sum;
+  for (int w = 0; w < warp; ++w) base += wsum[w];
+#pragma unroll
+  for (int i = 0; i < BPT; ++i) {
+    const int b = tid * BPT + i;
+    if (b < bins) {
+      uint32_t at = base + before[i];
+#pragma unroll
+      for (int w = 0; w < SORT_WARPS; ++w) {
+        const uint32_t c = hist[w * bins + b];
+        hist[w * bins + b] = at;
+        at += c;
+      }
+    }
+    base += all[i];
+  }
+  __syncthreads();
+}
+
+template <int CTAS>
+__device__ __forceinline__ void sort_prepare(const SortArgs& a, int rank) {
+  for (int i = rank * SORT_THREADS + (int)threadIdx.x; i < a.ncount; i += CTAS * SORT_THREADS) a.count[i] = 0;
   if (a.used != nullptr) {
-    for (int i = rank * SORT_THREADS + tid; i < a.nused; i += CTAS * SORT_THREADS) a.used[i] = 0u;
+    for (int i = rank * SORT_THREADS + (int)threadIdx.x; i < a.nused; i += CTAS * SORT_THREADS) a.used[i] = 0u;
     sort_barrier<CTAS>();
   }
-  // this warp's part of the list, in whole tiles of 32
-  const int64_t tiles = (a.N + 31) / 32;
-  const int64_t gw = (int64_t)rank * SORT_WARPS + warp, nw = CTAS * SORT_WARPS;
-  const int i0 = (int)(tiles * gw / nw) * 32, i1 = min((int)(tiles * (gw + 1) / nw) * 32, a.N);
-  uint32_t* h = hist[warp];
+}
+
+constexpr size_t sort_smem(int bits, int held) {
+  return ((size_t)(SORT_WARPS + 1) << bits) * 4 + SORT_WARPS * 4 + (size_t)held * 8;
+}
+
+// TILES tiles of 32 pairs per warp. Pairs past N have the largest key and stay behind the others.
+template <int CTAS, int TILES>
+__global__ void __launch_bounds__(SORT_THREADS, 1) k_sort_reg(const __grid_constant__ SortArgs a) {
+  constexpr int PER = SORT_WARPS * TILES * 32;  // pairs per block
+  extern __shared__ uint2 dyn[];
+  uint2* buf = dyn;                             // [PER]
+  const int bins = 1 << a.bits;
+  uint32_t* hist = (uint32_t*)(dyn + PER);      // [SORT_WARPS][bins]
+  uint32_t* tot = hist + SORT_WARPS * bins;     // [bins]
+  uint32_t* wsum = tot + bins;                  // [SORT_WARPS]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = CTAS > 1 ? (int)cluster_rank() : 0;
+  const uint32_t mask = (uint32_t)bins - 1;
+  uint32_t* h = hist + warp * bins;
+  sort_prepare<CTAS>(a, rank);
+  uint32_t key[TILES], pos[TILES], off[TILES];
+#pragma unroll
+  for (int j = 0; j < TILES; ++j) {
+    const int i = rank * PER + (warp * TILES + j) * 32 + lane;
+    pos[j] = (uint32_t)i;
+    key[j] = i < a.N ? sort_key(a, i) : 0xffffffffu;
+  }
+  if (a.used != nullptr) {
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) mark_used(a, key[j]);
+  }
   for (int pass = 0; pass < a.passes; ++pass) {
-    const uint32_t* ks = pass & 1 ? a.k1 : a.k0;
-    const uint32_t* ps = pass & 1 ? a.p1 : a.p0;
-    uint32_t* kd = pass & 1 ? a.k0 : a.k1;
-    uint32_t* pd = pass & 1 ? a.p0 : a.p1;
     const int shift = pass * a.bits;
-    auto load = [&](int i, uint32_t& key, uint32_t& pos) {
-      if (pass == 0) {
-        const int64_t t = a.tokens[i];
-        const bool live = t >= 0 && t < a.V && t != a.ignore_index;
-        if (!live && t != a.ignore_index && a.status != nullptr) atomicOr(a.status, ST_TARGET_RANGE);
-        key = live ? (uint32_t)t : (uint32_t)a.V;
-        pos = (uint32_t)i;
-      } else {
-        key = __ldcg(ks + i);
-        pos = __ldcg(ps + i);
-      }
-    };
     for (int b = lane; b < bins; b += 32) h[b] = 0;
     __syncwarp();
-    for (int i = i0 + lane; i - lane < i1; i += 32) {
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) {
+      const uint32_t d = (key[j] >> shift) & mask;
+      const unsigned peers = same_digit(0xffffffffu, d, a.bits);
+      off[j] = h[d] + __popc(peers & ((1u << lane) - 1));
+      __syncwarp();
+      if (lane == __ffs(peers) - 1) h[d] = off[j] + __popc(peers);
+      __syncwarp();
+    }
+    __syncthreads();
+    sort_places<CTAS>(hist, tot, wsum, bins, rank);
+    const bool last = pass + 1 == a.passes;
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) {
+      const uint32_t at = h[(key[j] >> shift) & mask] + off[j];
+      if (last) {
+        if (at < (uint32_t)a.N) {
+          a.k0[at] = key[j];
+          a.p0[at] = pos[j];
+        }
+      } else if constexpr (CTAS > 1) {
+        // every block has read its pairs of this pass (the barrier in sort_places)
+        asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(remote_addr(buf + at % PER, at / PER)),
+                     "r"(key[j]), "r"(pos[j])
+                     : "memory");
+      } else {
+        buf[at] = make_uint2(key[j], pos[j]);
+      }
+    }
+    sort_barrier<CTAS>();  // the pairs are in place, and every block has read the counts
+    if (!last) {
+#pragma unroll
+      for (int j = 0; j < TILES; ++j) {
+        const uint2 v = buf[(warp * TILES + j) * 32 + lane];
+        key[j] = v.x;
+        pos[j] = v.y;
+      }
+      if constexpr (CTAS == 1) __syncthreads();  // (a cluster's next scatter comes after its own barrier)
+    }
+  }
+}
+
+__global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS, 1)
+    k_sort(const __grid_constant__ SortArgs a) {
+  extern __shared__ uint2 dyn[];
+  const int bins = 1 << a.bits;
+  uint32_t* hist = (uint32_t*)dyn;              // [SORT_WARPS][bins]
+  uint32_t* tot = hist + SORT_WARPS * bins;     // [bins]
+  uint32_t* wsum = tot + bins;                  // [SORT_WARPS]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = (int)cluster_rank();
+  const uint32_t mask = (uint32_t)bins - 1;
+  uint32_t* h = hist + warp * bins;
+  sort_prepare<SORT_CTAS>(a, rank);
+  // this warp's part of the list, in whole tiles of 32
+  const int64_t tiles = ((int64_t)a.N + 31) / 32;
+  const int64_t gw = (int64_t)rank * SORT_WARPS + warp, nw = SORT_CTAS * SORT_WARPS;
+  const int64_t i0 = tiles * gw / nw * 32, i1 = min(tiles * (gw + 1) / nw * 32, (int64_t)a.N);
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const bool to0 = ((a.passes - pass) & 1) != 0;  // the last pass ends in k0, p0
+    const uint32_t* ks = to0 ? a.k1 : a.k0;
+    const uint32_t* ps = to0 ? a.p1 : a.p0;
+    uint32_t* kd = to0 ? a.k0 : a.k1;
+    uint32_t* pd = to0 ? a.p0 : a.p1;
+    const int shift = pass * a.bits;
+    for (int b = lane; b < bins; b += 32) h[b] = 0;
+    __syncwarp();
+    for (int64_t i = i0 + lane; i - lane < i1; i += 32) {
       const bool in = i < i1;
       const unsigned act = __ballot_sync(0xffffffffu, in);
       if (in) {
-        uint32_t key, pos;
-        load(i, key, pos);
+        const uint32_t key = pass == 0 ? sort_key(a, (int)i) : __ldcg(ks + i);
         const uint32_t d = (key >> shift) & mask;
-        const unsigned peers = __match_any_sync(act, d);
+        const unsigned peers = same_digit(act, d, a.bits);
         if (lane == __ffs(peers) - 1) h[d] += __popc(peers);
-        if (pass == 0 && a.used != nullptr && key < (uint32_t)a.V) atomicOr(a.used + (key >> 5), 1u << (key & 31));
+        if (pass == 0) mark_used(a, key);
       }
       __syncwarp();
     }
     __syncthreads();
-    // counts over the block's warps: each digit's column becomes an exclusive sum
-    uint32_t before = 0, all = 0;
-    if (tid < bins) {
-      uint32_t c[SORT_WARPS], s = 0;
-#pragma unroll
-      for (int w = 0; w < SORT_WARPS; ++w) c[w] = hist[w][tid];
-#pragma unroll
-      for (int w = 0; w < SORT_WARPS; ++w) {
-        hist[w][tid] = s;
-        s += c[w];
-      }
-      all = s;
-      if (CTAS > 1) tot[tid] = s;
-    }
-    if constexpr (CTAS > 1) {
-      cluster_barrier();
-      if (tid < bins) {
-        all = 0;
-#pragma unroll
-        for (int c = 0; c < CTAS; ++c) {
-          const uint32_t v = ld_remote(tot + tid, c);
-          before += c < rank ? v : 0;
-          all += v;
-        }
-      }
-    }
-    // exclusive sum of `all` over the digits (zero past bins)
-    uint32_t x = all;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (tid < MAX_BINS && lane == 31) wsum[warp] = x;
-    __syncthreads();
-    uint32_t base = x - all + before;
-    if (tid < MAX_BINS)
-      for (int w = 0; w < warp; ++w) base += wsum[w];
-    if (tid < bins) {
-#pragma unroll
-      for (int w = 0; w < SORT_WARPS; ++w) hist[w][tid] += base;
-    }
-    __syncthreads();
-    for (int i = i0 + lane; i - lane < i1; i += 32) {
+    sort_places<SORT_CTAS>(hist, tot, wsum, bins, rank);
+    for (int64_t i = i0 + lane; i - lane < i1; i += 32) {
       const bool in = i < i1;
       const unsigned act = __ballot_sync(0xffffffffu, in);
       if (in) {
-        uint32_t key, pos;
-        load(i, key, pos);
+        const uint32_t key = pass == 0 ? sort_key(a, (int)i) : __ldcg(ks + i);
+        const uint32_t pos = pass == 0 ? (uint32_t)i : __ldcg(ps + i);
         const uint32_t d = (key >> shift) & mask;
-        const unsigned peers = __match_any_sync(act, d);
+        const unsigned peers = same_digit(act, d, a.bits);
         const uint32_t at = h[d] + __popc(peers & ((1u << lane) - 1));
         kd[at] = key;
         pd[at] = pos;
@@ -236,16 +360,67 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) k_sort(const __grid_constant_
       }
       __syncwarp();
     }
-    sort_barrier<CTAS>();  // the scattered list is complete; every block has read the counts
+    cluster_barrier();  // the scattered list is complete; every block has read the counts
   }
+}
+
+template <int CTAS, int TILES>
+cudaError_t launch_sort_reg(const SortArgs& a, cudaStream_t s) {
+  constexpr int held = SORT_WARPS * TILES * 32;
+  // the shared-memory limit, once per device
+  static std::atomic<bool> raised[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!raised[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(k_sort_reg<CTAS, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sort_smem(MAX_BITS, held));
+    if (e != cudaSuccess) return e;
+    raised[dev].store(true, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CTAS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(CTAS, 1, 1);
+  cfg.blockDim = dim3(SORT_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = sort_smem(a.bits, held);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_sort_reg<CTAS, TILES>, a);
+}
+
+cudaError_t launch_sort(const SortArgs& a, cudaStream_t s) {
+  const int64_t tiles = cdiv64(a.N, 32), warps = SORT_CTAS * SORT_WARPS;
+  if (tiles <= SORT_WARPS) return launch_sort_reg<1, 1>(a, s);
+  if (tiles <= 2 * SORT_WARPS) return launch_sort_reg<1, 2>(a, s);
+  if (tiles <= warps) return launch_sort_reg<SORT_CTAS, 1>(a, s);
+  if (tiles <= 2 * warps) return launch_sort_reg<SORT_CTAS, 2>(a, s);
+  if (tiles <= 4 * warps) return launch_sort_reg<SORT_CTAS, 4>(a, s);
+  if (tiles <= 8 * warps) return launch_sort_reg<SORT_CTAS, 8>(a, s);
+  if (tiles <= 16 * warps) return launch_sort_reg<SORT_CTAS, 16>(a, s);
+  static std::atomic<bool> raised[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!raised[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(k_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sort_smem(MAX_BITS, 0));
+    if (e != cudaSuccess) return e;
+    raised[dev].store(true, std::memory_order_relaxed);
+  }
+  k_sort<<<SORT_CTAS, SORT_THREADS, sort_smem(a.bits, 0), s>>>(a);
+  return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ sums
 constexpr int PIECE = 32;       // sorted positions per block
 constexpr int BATCH = 4;        // rows in flight per thread
 constexpr int ZERO_ROWS = 64;   // rows of dE per block that zeroes unused ones
-
-__device__ __forceinline__ int64_t cdiv_dev(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct SumArgs {
   const uint32_t *keys, *pos;  // sorted
@@ -327,17 +502,17 @@ __global__ void __launch_bounds__(128) k_embed_sum(const __grid_constant__ SumAr
   const int sums = a.pieces * a.slices;
   if ((int)blockIdx.x >= sums) {
     const int64_t v0 = (int64_t)(blockIdx.x - sums) * ZERO_ROWS;
-    float z[EPV];
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) z[e] = 0.0f;
-    RowOf<D, EPV> row;
-    row.zero();
-    const int64_t nvec = cdiv_dev(a.H, EPV);
     for (int r = 0; r < ZERO_ROWS && v0 + r < a.V; ++r) {
       const int64_t v = v0 + r;
       if (a.used[v >> 5] >> (v & 31) & 1u) continue;
-      for (int64_t i = threadIdx.x; i < nvec; i += blockDim.x)
-        row.add_store((D*)a.dE + v * a.lddE + i * EPV, z, 0.0f);
+      // single elements up to a 16-byte boundary, 16 bytes at a time, single elements again
+      D* p = (D*)a.dE + v * a.lddE;
+      const int64_t head = min((int64_t)((16 - (uintptr_t)p % 16) % 16 / sizeof(D)), a.H);
+      const int64_t body = (a.H - head) / (16 / (int)sizeof(D));
+      const int64_t tail = head + body * (16 / (int)sizeof(D));
+      if (threadIdx.x < head) p[threadIdx.x] = from_f<D>(0.0f);
+      for (int64_t i = threadIdx.x; i < body; i += blockDim.x) ((uint4*)(p + head))[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (tail + threadIdx.x < a.H) p[tail + threadIdx.x] = from_f<D>(0.0f);
     }
     return;
   }
@@ -565,7 +740,7 @@ extern "C" int32_t flce_embed_bwd(const flce_embed_args* x, void* stream) {
   so.N = (int)x->N;
   int kb = 1;
   while ((x->V >> kb) != 0) ++kb;  // bits of the largest key, V
-  so.passes = (kb + 8) / 9;
+  so.passes = (kb + MAX_BITS - 1) / MAX_BITS;
   so.bits = (kb + so.passes - 1) / so.passes;
   so.k0 = (uint32_t*)(ws + l.k0);
   so.p0 = (uint32_t*)(ws + l.p0);
@@ -576,25 +751,9 @@ extern "C" int32_t flce_embed_bwd(const flce_embed_args* x, void* stream) {
   so.ncount = a.pieces * a.slices;
   so.used = ovw ? (uint32_t*)(ws + l.used) : nullptr;
   so.nused = l.nused;
-  a.keys = so.passes & 1 ? so.k1 : so.k0;
-  a.pos = so.passes & 1 ? so.p1 : so.p0;
-  if (x->N <= SORT_ONE) {
-    k_sort<1><<<1, SORT_THREADS, 0, s>>>(so);
-    e = cudaGetLastError();
-  } else {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = SORT_CTAS;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(SORT_CTAS, 1, 1);
-    cfg.blockDim = dim3(SORT_THREADS, 1, 1);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_sort<SORT_CTAS>, so);
-  }
+  a.keys = so.k0;
+  a.pos = so.p0;
+  e = launch_sort(so, s);
   if (e != cudaSuccess) return cuda_status(e);
 
   const bool same = x->dE_dtype == x->dtype;

@@ -85,7 +85,8 @@ BWD = [(1, 64, 10, "uniform", "bf16", "f32"), (7, 1, 5, "uniform", "f32", "f32")
        (9001, 72, 32000, "skewed", "bf16", "bf16"), (3000, 8, 128256, "skewed", "bf16", "f32"),
        (40000, 16, 262144, "skewed", "f16", "f32"), (200, 33, 511, "ignored", "bf16", "f32"),
        (300, 40, 512, "uniform", "bf16", "f32"), (64, 5000, 20, "uniform", "bf16", "f32"),
-       (2000, 16, 1, "uniform", "f32", "f32")]
+       (2000, 16, 1, "uniform", "f32", "f32"), (70000, 8, 300000, "skewed", "bf16", "f32"),
+       (4097, 24, 1 << 20, "skewed", "f32", "f32"), (600, 24, 40, "skewed", "f32", "f32"), (66000, 8, 90, "uniform", "f16", "f32")]
 
 
 @pytest.mark.parametrize("N,H,V,kind,dt,dE_dt", BWD)
