@@ -439,65 +439,79 @@ def raw_call(args: FlceArgs, stream_handle: int) -> int:
 
 def _matrix(name, t, rows, cols, dtype, dev):
     """Checks a [rows, cols] CUDA matrix of unit column stride; returns (pointer, row pitch)."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (rows, cols) or t.device != dev:
-        raise ValueError(f"{name} must be [{rows}, {cols}] on {dev}, got {tuple(t.shape)} on {t.device}")
-    ld, inner = t.stride()
-    if rows <= 1:
-        ld = cols if rows == 0 else max(ld, cols)
-    if (inner != 1 and cols > 1) or ld < cols:
+    if t.dtype is dtype and t.device == dev and t.shape == (rows, cols):
+        if t.is_contiguous():
+            return t.data_ptr(), cols
+        ld, inner = t.stride()
+        if rows <= 1:
+            ld = max(ld, cols)
+        if (inner == 1 or cols == 1) and ld >= cols:
+            return t.data_ptr(), ld
         raise ValueError(f"{name} must have unit column stride and rows that do not overlap, got strides {t.stride()}")
-    return t.data_ptr(), ld
+    raise ValueError(f"{name} must be {dtype} [{rows}, {cols}] on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _vector(name, t, n, dtype, dev):
-    if t.dtype != dtype or t.shape != (n,) or t.device != dev or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a dense {dtype} vector of {n} on {dev}, got {t.dtype} {tuple(t.shape)} "
-                         f"strides {t.stride()} on {t.device}")
-    return t.data_ptr()
-
-
-def _dense(name, t, rows, cols, dev):
-    """Checks a dense fp32 [rows, cols] (block scales)."""
-    if t.dtype != torch.float32 or t.shape != (rows, cols) or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be dense fp32 [{rows}, {cols}] on {dev}")
-    return t.data_ptr()
+def _dense(name, t, shape, dtype, dev):
+    """Checks a dense tensor; returns its pointer."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a dense {dtype} tensor {shape} on {dev}, got {t.dtype} {tuple(t.shape)} "
+                     f"strides {t.stride()} on {t.device}")
 
 
 def _cuda_2d(name, t):
-    if t.device.type != "cuda":
+    """Checks the operand that decides device and dtype; returns (device, shape, flce_dtype)."""
+    dev = t.device
+    if dev.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
-    if t.dtype not in DTYPES:
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(shape)}")
+    dt = DTYPES.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{name} must be fp32, bf16 or fp16, got {t.dtype}")
-    return t.device
+    return dev, shape, dt
+
+
+def _grad_dtype(name, t):
+    dt = DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be fp32, bf16 or fp16, got {t.dtype}")
+    return dt
 
 
 def empty_rows8(N, H, device):
     """An [N, H] e4m3 tensor whose rows start at multiples of 16 bytes."""
     p = (H + 15) & ~15
-    t = torch.empty(N, p, dtype=torch.float8_e4m3fn, device=device)
+    t = torch.empty((N, p), dtype=torch.float8_e4m3fn, device=device)
     return t if p == H else t[:, :H]
 
 
-def _scales(N, H, device):
-    return torch.empty(N, (H + Q_BLOCK - 1) // Q_BLOCK, dtype=torch.float32, device=device)
+def _workspace(ws, nbytes, dev, stream):
+    """The caller's byte workspace, or a new one owned by the stream that uses it."""
+    if ws is not None:
+        if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev:
+            raise ValueError(f"workspace must be a dense uint8 tensor on {dev}")
+        return ws
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
 def _launch(fn, where, args, dev, stream, used):
-    """Enqueue on `stream` (None: the current one). Tensors used on a stream other than the
-    current one are recorded on it, so that the allocator does not hand their memory out
-    before the kernels are done."""
+    """Enqueue on `stream` (None: the current one); returns the stream's handle. Tensors used on
+    a stream other than the current one are recorded on it, so that the allocator does not hand
+    their memory out before the kernels are done."""
+    index = dev.index
     if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
+        handle = torch._C._cuda_getCurrentRawStream(index)
     else:
         handle = stream.cuda_stream
         for t in used:
             if t is not None:
                 t.record_stream(stream)
-    if dev.index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         rc = fn(args, handle)
     else:
         with torch.cuda.device(dev):
@@ -505,6 +519,16 @@ def _launch(fn, where, args, dev, stream, used):
     if rc != FLCE_OK:
         raise FlceError(rc, where)
     return handle
+
+
+def _status(o, status, check, dev):
+    """Pointer of the status word: the caller's, a new one when the status is to be checked."""
+    if status is None:
+        if not check:
+            return None
+        status = torch.empty(1, dtype=torch.int32, device=dev)
+    o["status"] = status
+    return _dense("status", status, (1,), torch.int32, dev)
 
 
 def _finish(o, lib, check, handle):
@@ -521,23 +545,17 @@ def embed_fwd(tokens, E, *, scale=1.0, ignore_index=-100, out=None, status=None,
     outside [0, V) gives a zero row and FLCE_ERR_TARGET_RANGE. ``status`` (int32 [1]) receives
     the device status word without a check.
     """
-    lib = load()
-    dev = _cuda_2d("E", E)
-    V, H = E.shape
+    lib = _lib or load()
+    dev, (V, H), dt = _cuda_2d("E", E)
     N = tokens.shape[0]
     if out is None:
-        out = torch.empty(N, H, dtype=E.dtype, device=dev)
+        out = torch.empty((N, H), dtype=E.dtype, device=dev)
     o = {"out": out}
-    if status is None and check:
-        status = torch.empty(1, dtype=torch.int32, device=dev)
-    if status is not None:
-        o["status"] = status
     pE, ldE = _matrix("E", E, V, H, E.dtype, dev)
     po, ldo = _matrix("out", out, N, H, E.dtype, dev)
-    a = FlceEmbedArgs(N, H, V, DTYPES[E.dtype], 0, _vector("tokens", tokens, N, torch.int64, dev), ignore_index,
-                      scale, 0, pE, ldE, po, ldo, None, 0, None, 0, None, 0,
-                      None if status is None else _vector("status", status, 1, torch.int32, dev))
-    h = _launch(lib.flce_embed_fwd, "flce_embed_fwd", a, dev, stream, (tokens, E, out, status))
+    a = FlceEmbedArgs(N, H, V, dt, 0, _dense("tokens", tokens, (N,), torch.int64, dev), ignore_index, scale, 0,
+                      pE, ldE, po, ldo, None, 0, None, 0, None, 0, _status(o, status, check, dev))
+    h = _launch(lib.flce_embed_fwd, "flce_embed_fwd", a, dev, stream, (tokens, E, out, o.get("status")))
     return _finish(o, lib, check, h)
 
 
@@ -549,44 +567,23 @@ def embed_bwd(tokens, dout, *, V=None, dE=None, scale=1.0, ignore_index=-100, wo
     it is written), for instance the head's own dW of a tied embedding. Without dE a new fp32
     one of ``V`` rows is written. Returns a dict with dE (and status_code when ``check``).
     """
-    lib = load()
-    dev = _cuda_2d("dout", dout)
-    N, H = dout.shape
+    lib = _lib or load()
+    dev, (N, H), dt = _cuda_2d("dout", dout)
     if dE is None:
         if V is None:
             raise ValueError("embed_bwd needs V or dE")
-        dE = torch.empty(V, H, dtype=torch.float32, device=dev)
+        dE = torch.empty((V, H), dtype=torch.float32, device=dev)
         flags |= FLAG_DW_OVERWRITE
     V = dE.shape[0]
-    if dE.dtype not in DTYPES:
-        raise ValueError(f"dE must be fp32, bf16 or fp16, got {dE.dtype}")
-    nbytes = int(lib.flce_embed_workspace_size(N, H, V))
-    workspace = _workspace(workspace, nbytes, dev, stream)
+    workspace = _workspace(workspace, lib.flce_embed_workspace_size(N, H, V), dev, stream)
     o = {"dE": dE, "workspace": workspace}
-    if status is None and check:
-        status = torch.empty(1, dtype=torch.int32, device=dev)
-    if status is not None:
-        o["status"] = status
     pd, ldd = _matrix("dout", dout, N, H, dout.dtype, dev)
     pE, ldE = _matrix("dE", dE, V, H, dE.dtype, dev)
-    a = FlceEmbedArgs(N, H, V, DTYPES[dout.dtype], DTYPES[dE.dtype], _vector("tokens", tokens, N, torch.int64, dev),
-                      ignore_index, scale, flags, None, 0, None, 0, pd, ldd, pE, ldE,
-                      workspace.data_ptr(), workspace.numel(),
-                      None if status is None else _vector("status", status, 1, torch.int32, dev))
-    h = _launch(lib.flce_embed_bwd, "flce_embed_bwd", a, dev, stream, (tokens, dout, dE, workspace, status))
+    a = FlceEmbedArgs(N, H, V, dt, _grad_dtype("dE", dE), _dense("tokens", tokens, (N,), torch.int64, dev),
+                      ignore_index, scale, flags, None, 0, None, 0, pd, ldd, pE, ldE, workspace.data_ptr(),
+                      workspace.numel(), _status(o, status, check, dev))
+    h = _launch(lib.flce_embed_bwd, "flce_embed_bwd", a, dev, stream, (tokens, dout, dE, workspace, o.get("status")))
     return _finish(o, lib, check, h)
-
-
-def _workspace(ws, nbytes, dev, stream):
-    """The caller's byte workspace, or a new one owned by the stream that uses it."""
-    if ws is not None:
-        if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev:
-            raise ValueError(f"workspace must be a dense uint8 tensor on {dev}")
-        return ws
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
 def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, weight_offset=0.0, want_y=True, want_h=None, want_y8=False,
@@ -598,52 +595,53 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, weight_offset=0.0, want_y
     h8, h8_scale (8-bit checkpoint of h for ``rmsnorm_bwd``). ``outputs`` may carry preallocated
     tensors under the same keys; h may be x or residual itself.
     """
-    lib = load()
-    dev = _cuda_2d("x", x)
-    N, H = x.shape
-    dt = x.dtype
+    lib = _lib or load()
+    dev, (N, H), dt = _cuda_2d("x", x)
+    dtype = x.dtype
     o = dict(outputs) if outputs else {}
+    given = o.get
+    px, ldx = _matrix("x", x, N, H, dtype, dev)
+    pr, ldr = (None, 0) if residual is None else _matrix("residual", residual, N, H, dtype, dev)
+    rstd = given("rstd")
+    if rstd is None:
+        rstd = o["rstd"] = torch.empty(N, dtype=torch.float32, device=dev)
+        prstd = rstd.data_ptr()
+    else:
+        prstd = _dense("rstd", rstd, (N,), torch.float32, dev)
+    (py, ldy) = _row_output(o, "y", N, H, dtype, dev) if want_y else (None, 0)
     if want_h is None:
         want_h = residual is not None
-    pr, ldr = (None, 0) if residual is None else _matrix("residual", residual, N, H, dt, dev)
-    px, ldx = _matrix("x", x, N, H, dt, dev)
-    y = h = y8 = h8 = None
-    py = ph = py8 = ph8 = psy = psh = None
-    ldy = ldh = ldy8 = ldh8 = 0
-    if o.get("rstd") is None:
-        o["rstd"] = torch.empty(N, dtype=torch.float32, device=dev)
-    if want_y:
-        y = o.get("y")
-        if y is None:
-            y = o["y"] = torch.empty(N, H, dtype=dt, device=dev)
-        py, ldy = _matrix("y", y, N, H, dt, dev)
-    if want_h:
-        h = o.get("h")
-        if h is None:
-            h = o["h"] = torch.empty(N, H, dtype=dt, device=dev)
-        ph, ldh = _matrix("h", h, N, H, dt, dev)
-    if want_y8:
-        y8, psy = _rows8(o, "y8", N, H, dev)
-        py8, ldy8 = _matrix("y8", y8, N, H, torch.float8_e4m3fn, dev)
-    if want_h8:
-        h8, psh = _rows8(o, "h8", N, H, dev)
-        ph8, ldh8 = _matrix("h8", h8, N, H, torch.float8_e4m3fn, dev)
-    a = FlceRmsnormArgs(N, H, DTYPES[dt], eps, weight_offset, 0, px, ldx, pr, ldr, _vector("weight", weight, H, dt, dev),
-                        ph, ldh, py, ldy, _vector("rstd", o["rstd"], N, torch.float32, dev), py8, ldy8, psy, ph8, ldh8,
-                        psh)
-    _launch(lib.flce_rmsnorm_fwd, "flce_rmsnorm_fwd", a, dev, stream,
-            (x, residual, weight, y, h, y8, h8, o["rstd"], o.get("y8_scale"), o.get("h8_scale")))
+    (ph, ldh) = _row_output(o, "h", N, H, dtype, dev) if want_h else (None, 0)
+    (py8, ldy8, psy) = _rows8(o, "y8", "y8_scale", N, H, dev) if want_y8 else (None, 0, None)
+    (ph8, ldh8, psh) = _rows8(o, "h8", "h8_scale", N, H, dev) if want_h8 else (None, 0, None)
+    a = FlceRmsnormArgs(N, H, dt, eps, weight_offset, 0, px, ldx, pr, ldr, _dense("weight", weight, (H,), dtype, dev),
+                        ph, ldh, py, ldy, prstd, py8, ldy8, psy, ph8, ldh8, psh)
+    _launch(lib.flce_rmsnorm_fwd, "flce_rmsnorm_fwd", a, dev, stream, (x, residual, weight, *o.values()))
     return o
 
 
-def _rows8(o, key, N, H, dev):
-    """The 8-bit rows o[key] and the pointer of their scales o[key + "_scale"], made if absent."""
-    if o.get(key) is None:
-        o[key] = empty_rows8(N, H, dev)
-    sk = "scale" if key == "q" else key + "_scale"
-    if o.get(sk) is None:
-        o[sk] = _scales(N, H, dev)
-    return o[key], _dense(sk, o[sk], N, (H + Q_BLOCK - 1) // Q_BLOCK, dev)
+def _row_output(o, key, N, H, dtype, dev):
+    """Pointer and pitch of the output matrix o[key], made if absent."""
+    t = o.get(key)
+    if t is None:
+        t = o[key] = torch.empty((N, H), dtype=dtype, device=dev)
+        return t.data_ptr(), H
+    return _matrix(key, t, N, H, dtype, dev)
+
+
+def _rows8(o, key, scale_key, N, H, dev):
+    """Pointer and pitch of the 8-bit rows o[key] and the pointer of their scales, made if absent."""
+    t, s = o.get(key), o.get(scale_key)
+    shape = (N, (H + Q_BLOCK - 1) // Q_BLOCK)
+    if t is None:
+        t = o[key] = empty_rows8(N, H, dev)
+        p, ld = t.data_ptr(), (H + 15) & ~15
+    else:
+        p, ld = _matrix(key, t, N, H, torch.float8_e4m3fn, dev)
+    if s is None:
+        s = o[scale_key] = torch.empty(shape, dtype=torch.float32, device=dev)
+        return p, ld, s.data_ptr()
+    return p, ld, _dense(scale_key, s, shape, torch.float32, dev)
 
 
 def rmsnorm_bwd(dy, weight, rstd, h=None, *, h8=None, h8_scale=None, dh=None, weight_offset=0.0, want_dx=True,
@@ -652,60 +650,50 @@ def rmsnorm_bwd(dy, weight, rstd, h=None, *, h8=None, h8_scale=None, dh=None, we
     stream's own gradient, added) and dweight, accumulated into when given (fp32 or dy's dtype;
     FLAG_DW_OVERWRITE: written), else a new fp32 vector. The norm's input is ``h`` or its 8-bit
     checkpoint ``h8, h8_scale``. Returns a dict with dx and dweight."""
-    lib = load()
-    dev = _cuda_2d("dy", dy)
-    N, H = dy.shape
-    dt = dy.dtype
+    lib = _lib or load()
+    dev, (N, H), dt = _cuda_2d("dy", dy)
+    dtype = dy.dtype
     if (h is None) == (h8 is None) or (h8 is not None and h8_scale is None):
         raise ValueError("rmsnorm_bwd takes h, or h8 with h8_scale")
     o = dict(outputs) if outputs else {}
-    pdx, lddx = None, 0
-    if want_dx:
-        if o.get("dx") is None:
-            o["dx"] = torch.empty(N, H, dtype=dt, device=dev)
-        pdx, lddx = _matrix("dx", o["dx"], N, H, dt, dev)
+    (pdx, lddx) = _row_output(o, "dx", N, H, dtype, dev) if want_dx else (None, 0)
     pw = pws = None
     wbytes, wdt = 0, 0
     if want_dweight:
         if dweight is None:
             dweight = torch.empty(H, dtype=torch.float32, device=dev)
             flags |= FLAG_DW_OVERWRITE
-        if dweight.dtype not in DTYPES:
-            raise ValueError(f"dweight must be fp32, bf16 or fp16, got {dweight.dtype}")
-        pw, wdt = _vector("dweight", dweight, H, dweight.dtype, dev), DTYPES[dweight.dtype]
-        workspace = _workspace(workspace, int(lib.flce_rmsnorm_workspace_size(N, H)), dev, stream)
+        wdt = _grad_dtype("dweight", dweight)
+        pw = _dense("dweight", dweight, (H,), dweight.dtype, dev)
+        workspace = _workspace(workspace, lib.flce_rmsnorm_workspace_size(N, H), dev, stream)
         pws, wbytes = workspace.data_ptr(), workspace.numel()
         o["dweight"], o["workspace"] = dweight, workspace
-    else:
-        workspace = None
-    ph, ldh = (None, 0) if h is None else _matrix("h", h, N, H, dt, dev)
+    (ph, ldh) = (None, 0) if h is None else _matrix("h", h, N, H, dtype, dev)
     p8 = ps8 = None
     ld8 = 0
     if h8 is not None:
         p8, ld8 = _matrix("h8", h8, N, H, torch.float8_e4m3fn, dev)
-        ps8 = _dense("h8_scale", h8_scale, N, (H + Q_BLOCK - 1) // Q_BLOCK, dev)
-    pdh, lddh = (None, 0) if dh is None else _matrix("dh", dh, N, H, dt, dev)
-    pdy, lddy = _matrix("dy", dy, N, H, dt, dev)
-    a = FlceRmsnormBwdArgs(N, H, DTYPES[dt], wdt, weight_offset, flags, pdy, lddy, ph, ldh, p8, ld8, ps8,
-                           _vector("rstd", rstd, N, torch.float32, dev), _vector("weight", weight, H, dt, dev),
-                           pdh, lddh, pdx, lddx, pw, pws, wbytes)
+        ps8 = _dense("h8_scale", h8_scale, (N, (H + Q_BLOCK - 1) // Q_BLOCK), torch.float32, dev)
+    (pdh, lddh) = (None, 0) if dh is None else _matrix("dh", dh, N, H, dtype, dev)
+    pdy, lddy = _matrix("dy", dy, N, H, dtype, dev)
+    a = FlceRmsnormBwdArgs(N, H, dt, wdt, weight_offset, flags, pdy, lddy, ph, ldh, p8, ld8, ps8,
+                           _dense("rstd", rstd, (N,), torch.float32, dev),
+                           _dense("weight", weight, (H,), dtype, dev), pdh, lddh, pdx, lddx, pw, pws, wbytes)
     _launch(lib.flce_rmsnorm_bwd, "flce_rmsnorm_bwd", a, dev, stream,
-            (dy, weight, rstd, h, h8, h8_scale, dh, dweight, workspace, o.get("dx")))
+            (dy, weight, rstd, h, h8, h8_scale, dh, *o.values()))
     return o
 
 
 def ckpt8_pack(x, *, outputs=None, stream=None):
     """8-bit checkpoint of x [N, H]: a dict with q (e4m3 [N, H], rows at multiples of 16 bytes)
     and scale (fp32 [N, ceil(H/128)], powers of two); the value kept is q * scale."""
-    lib = load()
-    dev = _cuda_2d("x", x)
-    N, H = x.shape
+    lib = _lib or load()
+    dev, (N, H), dt = _cuda_2d("x", x)
     o = dict(outputs) if outputs else {}
-    q, ps = _rows8(o, "q", N, H, dev)
     px, ldx = _matrix("x", x, N, H, x.dtype, dev)
-    pq, ldq = _matrix("q", q, N, H, torch.float8_e4m3fn, dev)
-    _launch(lib.flce_ckpt8_pack, "flce_ckpt8_pack", FlceCkpt8Args(N, H, DTYPES[x.dtype], 0, px, ldx, pq, ldq, ps), dev,
-            stream, (x, q, o["scale"]))
+    pq, ldq, ps = _rows8(o, "q", "scale", N, H, dev)
+    _launch(lib.flce_ckpt8_pack, "flce_ckpt8_pack", FlceCkpt8Args(N, H, dt, 0, px, ldx, pq, ldq, ps), dev, stream,
+            (x, *o.values()))
     return o
 
 
@@ -717,30 +705,21 @@ def ckpt8_dw(dy, q, scale, *, dW=None, workspace=None, flags=0, wait_timeout_ms=
     fp32 or dy's dtype, accumulated into (FLAG_DW_OVERWRITE: written), else a new fp32 one.
     Returns a dict with dW (and status_code when ``check``, which synchronises the stream).
     """
-    lib = load()
-    dev = _cuda_2d("dy", dy)
-    M, N = dy.shape
+    lib = _lib or load()
+    dev, (M, N), dt = _cuda_2d("dy", dy)
     if q.dim() != 2:
         raise ValueError(f"q must be 2-D, got {tuple(q.shape)}")
     K = q.shape[1]
     if dW is None:
-        dW = torch.empty(N, K, dtype=torch.float32, device=dev)
+        dW = torch.empty((N, K), dtype=torch.float32, device=dev)
         flags |= FLAG_DW_OVERWRITE
-    if dW.dtype not in DTYPES:
-        raise ValueError(f"dW must be fp32, bf16 or fp16, got {dW.dtype}")
-    dt = DTYPES[dy.dtype]
-    workspace = _workspace(workspace, int(lib.flce_ckpt8_dw_workspace_size(M, N, K, dt)), dev, stream)
+    workspace = _workspace(workspace, lib.flce_ckpt8_dw_workspace_size(M, N, K, dt), dev, stream)
     o = {"dW": dW, "workspace": workspace}
-    if status is None and check:
-        status = torch.empty(1, dtype=torch.int32, device=dev)
-    if status is not None:
-        o["status"] = status
     pdy, lddy = _matrix("dy", dy, M, N, dy.dtype, dev)
     pq, ldq = _matrix("q", q, M, K, torch.float8_e4m3fn, dev)
     pW, ldW = _matrix("dW", dW, N, K, dW.dtype, dev)
-    a = FlceCkpt8DwArgs(M, N, K, dt, DTYPES[dW.dtype], flags, wait_timeout_ms, pdy, lddy, pq, ldq,
-                        _dense("scale", scale, M, (K + Q_BLOCK - 1) // Q_BLOCK, dev), pW, ldW,
-                        workspace.data_ptr(), workspace.numel(),
-                        None if status is None else _vector("status", status, 1, torch.int32, dev))
-    h = _launch(lib.flce_ckpt8_dw, "flce_ckpt8_dw", a, dev, stream, (dy, q, scale, dW, workspace, status))
+    a = FlceCkpt8DwArgs(M, N, K, dt, _grad_dtype("dW", dW), flags, wait_timeout_ms, pdy, lddy, pq, ldq,
+                        _dense("scale", scale, (M, (K + Q_BLOCK - 1) // Q_BLOCK), torch.float32, dev), pW, ldW,
+                        workspace.data_ptr(), workspace.numel(), _status(o, status, check, dev))
+    h = _launch(lib.flce_ckpt8_dw, "flce_ckpt8_dw", a, dev, stream, (dy, q, scale, dW, workspace, o.get("status")))
     return _finish(o, lib, check, h)

@@ -163,9 +163,9 @@ def test_matrix_check():
         with pytest.raises(ValueError):
             flce._matrix("x", bad, 6, bad.shape[1], torch.float32, cpu)
     with pytest.raises(ValueError):
-        flce._vector("v", x[:, 0], 6, torch.float32, cpu)
+        flce._dense("v", x[:, 0], (6,), torch.float32, cpu)
     with pytest.raises(ValueError):
-        flce._dense("s", x[:, :4], 6, 4, cpu)
+        flce._dense("s", x[:, :4], (6, 4), torch.float32, cpu)
 
 
 # ---- the oracles
