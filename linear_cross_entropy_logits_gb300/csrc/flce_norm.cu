@@ -10,6 +10,8 @@
 // (k_rms_fwd_long / k_rms_bwd_long) are read twice, the second time mostly from L2.
 #include <math.h>
 
+#include <atomic>
+
 #include "flce_ops.cuh"
 
 namespace flce {
@@ -163,7 +165,188 @@ __global__ void __launch_bounds__(512) k_rms_fwd_long(const __grid_constant__ Fw
   }
 }
 
-// Backward: a row group walks the rows group, group + groups, ...; its threads keep their
+// Sum over a row group by a barrier of its own (wpr > 1), for groups that walk their rows
+// independently. Two buffers are used in turn.
+__device__ __forceinline__ float group_sum_own(float v, float* red, int wpr, int wb, int group) {
+  v = warp_sum(v);
+  if (wpr == 1) return v;
+  if ((threadIdx.x & 31) == 0) red[wb] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(wpr * 32) : "memory");
+  float t = 0.0f;
+  for (int i = 0; i < wpr; ++i) t += red[group * wpr + i];
+  return t;
+}
+
+// The dweight sums of a block's groups, added in group order, as row blockIdx.x of a.part.
+template <int EPV, int NV>
+__device__ __forceinline__ void put_partials(const BwdArgs& a, const float (&dw)[NV][EPV], float* sums, int rpb,
+                                             int group, int w, int lane) {
+  float* out = a.part + (int64_t)blockIdx.x * a.H;
+  for (int g = 0; g < rpb; ++g) {
+    if (group == g) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
+        if (c < a.H) {
+#pragma unroll
+          for (int e = 0; e < EPV; ++e) {
+            const float u = g == 0 ? dw[j][e] : sums[c + e] + dw[j][e];
+            if (g == rpb - 1) out[c + e] = u;
+            else sums[c + e] = u;
+          }
+        }
+      }
+    }
+    if (g < rpb - 1) __syncthreads();
+  }
+}
+
+// Copies to shared memory without registers; nothing when !in.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool in) {
+  if constexpr (BYTES == 16)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n}" ::"r"(dst),
+                 "l"(src), "r"((int)in)
+                 : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.ca.shared.global [%0], [%1], %3;\n}" ::"r"(dst),
+                 "l"(src), "r"((int)in), "n"(BYTES)
+                 : "memory");
+}
+
+// Backward of rows whose operands allow 16-byte copies: a row group walks the rows group,
+// group + groups, .... Each thread copies its own pieces of the next RING - 1 rows to shared
+// memory (cp.async) and reads back only those, before and after the row's sum: no registers and
+// no barriers for what is in flight. Its columns' dweight sums stay in registers. 8192 x 4096
+// bf16 from the 8-bit checkpoint: see the table's line; rows held in registers, with two blocks
+// of 512 threads an SM, took 66 us.
+constexpr int RING = 4;
+template <typename T>
+constexpr int RING_WARPS = sizeof(T) == 4 ? 8 : 16;  // a block's, for its ring to fit
+template <typename T, int NV, bool Q8>
+__global__ void __launch_bounds__(512, 1) k_rms_bwd_ring(const __grid_constant__ BwdArgs a, int wpr) {
+  constexpr int EPV = 16 / sizeof(T);
+  constexpr int HB = Q8 ? EPV : 16;  // bytes of a vector of h
+  extern __shared__ uint4 ring[];    // [RING][thread's vectors: dy, dh, h][NV][threads], then the groups' sums
+  __shared__ float red[2][MAX_WARPS];
+  const int lane = threadIdx.x & 31, wb = threadIdx.x >> 5;
+  const int rpb = blockDim.x / 32 / wpr;
+  const int group = wb / wpr, w = wb - group * wpr;
+  const int64_t g0 = (int64_t)blockIdx.x * rpb + group, step = (int64_t)gridDim.x * rpb;
+  const int stage = (int)blockDim.x * NV * (32 + HB);  // bytes
+  uint8_t* base = (uint8_t*)ring + threadIdx.x * 16;
+  uint8_t* hbase = (uint8_t*)ring + blockDim.x * NV * 32 + threadIdx.x * HB;
+  const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(base), shbase = (uint32_t)__cvta_generic_to_shared(hbase);
+  const uint32_t vstep = blockDim.x * 16, hstep = blockDim.x * HB;
+  auto fetch = [&](int64_t row, int slot) {
+    const bool live = row < a.N;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
+      const bool in = live && c < a.H;
+      copy_async<16>(sbase + slot * stage + j * vstep, (const T*)a.dy + row * a.lddy + c, in);
+      copy_async<16>(sbase + slot * stage + (NV + j) * vstep, (const T*)a.dh + row * a.lddh + c, in && a.dh != nullptr);
+      if constexpr (Q8) copy_async<HB>(shbase + slot * stage + j * hstep, a.h8 + row * a.ldh8 + c, in);
+      else copy_async<16>(shbase + slot * stage + j * hstep, (const T*)a.h + row * a.ldh + c, in);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  Raw<T, EPV> wt[NV];
+  float dw[NV][EPV];
+#pragma unroll
+  for (int r = 0; r < RING - 1; ++r) fetch(g0 + r * step, r);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
+    wt[j].zero();
+    if (c < a.H) wt[j].load((const T*)a.w + c);
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) dw[j][e] = 0.0f;
+  }
+  auto factors = [&](int64_t row, float& rs, float (&f)[NV]) {
+    rs = row < a.N ? a.rstd[row] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
+      f[j] = Q8 && row < a.N && c < a.H ? a.h8s[row * a.nblk + c / Q_BLOCK] : 1.0f;
+    }
+  };
+  float rs_next, f_next[NV];
+  factors(g0, rs_next, f_next);
+  int slot = 0, buf = 0;
+  for (int64_t row = g0; row < a.N; row += step, buf ^= 1) {
+    const float rstd = rs_next;
+    float f[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) f[j] = f_next[j] * rstd;
+    factors(row + step, rs_next, f_next);
+    fetch(row + (RING - 1) * step, slot == 0 ? RING - 1 : slot - 1);  // the slot read last turn
+    asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
+    const uint8_t* p = base + slot * stage;
+    const uint8_t* ph = hbase + slot * stage;
+    auto xhat = [&](int j, float (&x)[EPV]) {
+      if constexpr (Q8) {
+        RawQ<EPV> q;
+        q.load(ph + j * hstep);
+        q.unpack(x);
+      } else {
+        Raw<T, EPV> r;
+        const uint4 u = *(const uint4*)(ph + j * hstep);
+        r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
+        r.unpack(x);
+      }
+#pragma unroll
+      for (int e = 0; e < EPV; ++e) x[e] *= f[j];
+    };
+    auto vec = [&](int i, float (&x)[EPV]) {
+      Raw<T, EPV> r;
+      const uint4 u = *(const uint4*)(p + i * vstep);
+      r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
+      r.unpack(x);
+    };
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (((int64_t)(w * NV + j) * 32 + lane) * EPV < a.H) {
+        float x[EPV], d[EPV];
+        xhat(j, x);
+        vec(j, d);
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) {
+          dot = fmaf(d[e] * (wt[j].get(e) + a.off), x[e], dot);
+          dw[j][e] = fmaf(d[e], x[e], dw[j][e]);
+        }
+      }
+    }
+    const float m = group_sum_own(dot, red[buf], wpr, wb, group) * a.inv_h;
+    if (a.dx != nullptr) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
+        if (c < a.H) {
+          float x[EPV], d[EPV], o[EPV];
+          xhat(j, x);
+          vec(j, d);
+#pragma unroll
+          for (int e = 0; e < EPV; ++e) o[e] = rstd * (d[e] * (wt[j].get(e) + a.off) - x[e] * m);
+          if (a.dh != nullptr) {
+            vec(NV + j, d);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) o[e] += d[e];
+          }
+          Vec<T, EPV>::store((T*)a.dx + row * a.lddx + c, o);
+        }
+      }
+    }
+    slot = slot == RING - 1 ? 0 : slot + 1;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (a.part == nullptr) return;
+  __syncthreads();  // the ring's memory is free: it takes the groups' sums
+  put_partials<EPV, NV>(a, dw, (float*)ring, rpb, group, w, lane);
+}
+
+// Backward of other rows: a row group walks the rows group, group + groups, ...; its threads keep their
 // columns' dweight sums in registers. All of a row is loaded before its sum is taken and kept as
 // it lies in memory (unpacked again after the sum), so that two blocks of 512 threads fit an SM
 // and enough loads are in flight. At the end the block's groups add their sums in group order
@@ -246,24 +429,7 @@ __global__ void __launch_bounds__(512, NV * EPV <= 16 ? 2 : 1) k_rms_bwd(const _
     }
   }
   if (a.part == nullptr) return;
-  float* out = a.part + (int64_t)blockIdx.x * a.H;
-  for (int g = 0; g < rpb; ++g) {
-    if (group == g) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
-        if (c < a.H) {
-#pragma unroll
-          for (int e = 0; e < EPV; ++e) {
-            const float u = g == 0 ? dw[j][e] : sums[c + e] + dw[j][e];
-            if (g == rpb - 1) out[c + e] = u;
-            else sums[c + e] = u;
-          }
-        }
-      }
-    }
-    if (g < rpb - 1) __syncthreads();
-  }
+  put_partials<EPV, NV>(a, dw, sums, rpb, group, w, lane);
 }
 
 template <typename T>
@@ -399,12 +565,41 @@ cudaError_t bwd_w(const BwdArgs& a, int64_t& part_rows, cudaStream_t s) {
   }
   return cudaGetLastError();
 }
+template <typename T, int NV, bool Q8>
+cudaError_t launch_ring(const BwdArgs& a, int wpr, int64_t& part_rows, cudaStream_t s) {
+  constexpr int EPV = 16 / sizeof(T);
+  const int64_t sms = num_sms();
+  // as many groups a block as there are rows for
+  int64_t rpb = cdiv64(a.N, sms);
+  if (rpb > RING_WARPS<T> / wpr) rpb = RING_WARPS<T> / wpr;
+  const int threads = (int)rpb * wpr * 32;
+  constexpr int most = RING * 32 * RING_WARPS<T> * NV * (32 + (Q8 ? EPV : 16));
+  static_assert(most <= 232448 - 1024, "shared memory per block");
+  const size_t smem = (size_t)RING * threads * NV * (32 + (Q8 ? EPV : 16));
+  static std::atomic<bool> raised[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!raised[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(k_rms_bwd_ring<T, NV, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    raised[dev].store(true, std::memory_order_relaxed);
+  }
+  part_rows = cdiv64(a.N, rpb) < sms ? cdiv64(a.N, rpb) : sms;
+  k_rms_bwd_ring<T, NV, Q8><<<(unsigned)part_rows, threads, smem, s>>>(a, wpr);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t bwd(const BwdArgs& a, Width w, int64_t& part_rows, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
-  return w == W32   ? bwd_w<T, 2 * E>(a, part_rows, s)
-         : w == W16 ? bwd_w<T, E>(a, part_rows, s)
-                    : bwd_w<T, 1>(a, part_rows, s);
+  if (w == W1) return bwd_w<T, 1>(a, part_rows, s);
+  const int64_t wpr = cdiv64(a.H, 512);  // 16 elements a thread
+  if (wpr <= RING_WARPS<T>)
+    return a.h8 ? launch_ring<T, 16 / E, true>(a, (int)wpr, part_rows, s)
+                : launch_ring<T, 16 / E, false>(a, (int)wpr, part_rows, s);
+  return bwd_w<T, E>(a, part_rows, s);
 }
 
 bool sizes_ok(int64_t N, int64_t H) { return N >= 0 && H >= 1 && N <= 0x7fffffffLL && H <= 0x7fffffffLL; }
@@ -518,13 +713,11 @@ extern "C" int32_t flce_rmsnorm_bwd(const flce_rmsnorm_bwd_args* x, void* stream
   a.dx = x->dx;
   a.lddx = x->lddx;
   a.part = x->dweight ? (float*)x->workspace : nullptr;
-  auto fits = [&](int bytes) {
-    const int e = bytes / esz;
-    return H % e == 0 && rows_by(a.dy, a.lddy, esz, bytes) && (!a.h || rows_by(a.h, a.ldh, esz, bytes)) &&
-           (!a.h8 || rows_by(a.h8, a.ldh8, 1, e)) && aligned_to(a.w, bytes) &&
-           (!a.dh || rows_by(a.dh, a.lddh, esz, bytes)) && (!a.dx || rows_by(a.dx, a.lddx, esz, bytes));
-  };
-  const Width w = fits(32) ? W32 : fits(16) ? W16 : W1;
+  const int e16 = 16 / esz;
+  const bool wide = H % e16 == 0 && rows16(a.dy, a.lddy, esz) && (!a.h || rows16(a.h, a.ldh, esz)) &&
+                    (!a.h8 || rows_by(a.h8, a.ldh8, 1, e16)) && aligned_to(a.w, 16) &&
+                    (!a.dh || rows16(a.dh, a.lddh, esz)) && (!a.dx || rows16(a.dx, a.lddx, esz));
+  const Width w = wide ? W16 : W1;
   int64_t rows = 0;
   cudaError_t e;
   switch (x->dtype) {
