@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) k_sort_reg(const __grid_const
   const int rank = CTAS > 1 ? (int)cluster_rank() : 0;
   const uint32_t mask = (uint32_t)bins - 1;
   uint32_t* h = hist + warp * bins;
+  let_next_start();
   sort_prepare<CTAS>(a, rank);
   uint32_t key[TILES], pos[TILES], off[TILES];
 #pragma unroll
@@ -316,6 +317,7 @@ __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS
   const int rank = (int)cluster_rank();
   const uint32_t mask = (uint32_t)bins - 1;
   uint32_t* h = hist + warp * bins;
+  let_next_start();
   sort_prepare<SORT_CTAS>(a, rank);
   // this warp's part of the list, in whole tiles of 32
   const int64_t tiles = ((int64_t)a.N + 31) / 32;
@@ -500,6 +502,7 @@ struct RowOf {  // EPV elements of dE in accesses of at most 32 bytes
 template <typename T, typename D, int EPV>
 __global__ void __launch_bounds__(128) k_embed_sum(const __grid_constant__ SumArgs a) {
   const int sums = a.pieces * a.slices;
+  after_previous();
   if ((int)blockIdx.x >= sums) {
     const int64_t v0 = (int64_t)(blockIdx.x - sums) * ZERO_ROWS;
     for (int r = 0; r < ZERO_ROWS && v0 + r < a.V; ++r) {
@@ -643,9 +646,8 @@ template <typename T, typename D>
 cudaError_t sums(SumArgs a, int epv, int threads, cudaStream_t s) {
   constexpr int W = 16 / sizeof(T);
   const unsigned blocks = (unsigned)(a.pieces * a.slices + (a.ovw ? cdiv64(a.V, ZERO_ROWS) : 0));
-  if (epv == W) k_embed_sum<T, D, W><<<blocks, threads, 0, s>>>(a);
-  else k_embed_sum<T, D, 1><<<blocks, threads, 0, s>>>(a);
-  return cudaGetLastError();
+  if (epv == W) return launch_after(k_embed_sum<T, D, W>, blocks, threads, 0, s, a);
+  return launch_after(k_embed_sum<T, D, 1>, blocks, threads, 0, s, a);
 }
 
 bool sizes_ok(int64_t N, int64_t H, int64_t V) {

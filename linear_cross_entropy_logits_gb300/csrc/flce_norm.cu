@@ -166,14 +166,18 @@ __global__ void __launch_bounds__(512) k_rms_fwd_long(const __grid_constant__ Fw
 }
 
 // Sum over a row group by a barrier of its own (wpr > 1), for groups that walk their rows
-// independently. Two buffers are used in turn.
-__device__ __forceinline__ float group_sum_own(float v, float* red, int wpr, int wb, int group) {
+// independently. `red`: the group's floats, wpr of them and zeros up to a multiple of four; two
+// buffers are used in turn.
+__device__ __forceinline__ float group_sum_own(float v, float* red, int wpr, int w, int group) {
   v = warp_sum(v);
   if (wpr == 1) return v;
-  if ((threadIdx.x & 31) == 0) red[wb] = v;
+  if ((threadIdx.x & 31) == 0) red[w] = v;
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(wpr * 32) : "memory");
   float t = 0.0f;
-  for (int i = 0; i < wpr; ++i) t += red[group * wpr + i];
+  for (int i = 0; i < wpr; i += 4) {
+    const float4 u = *(const float4*)(red + i);
+    t += (u.x + u.y) + (u.z + u.w);
+  }
   return t;
 }
 
@@ -201,149 +205,186 @@ __device__ __forceinline__ void put_partials(const BwdArgs& a, const float (&dw)
   }
 }
 
-// Copies to shared memory without registers; nothing when !in.
+// Copies to shared memory without registers.
 template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool in) {
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
   if constexpr (BYTES == 16)
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n}" ::"r"(dst),
-                 "l"(src), "r"((int)in)
-                 : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   else
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.ca.shared.global [%0], [%1], %3;\n}" ::"r"(dst),
-                 "l"(src), "r"((int)in), "n"(BYTES)
-                 : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
 // Backward of rows whose operands allow 16-byte copies: a row group walks the rows group,
 // group + groups, .... Each thread copies its own pieces of the next RING - 1 rows to shared
-// memory (cp.async) and reads back only those, before and after the row's sum: no registers and
-// no barriers for what is in flight. Its columns' dweight sums stay in registers. 8192 x 4096
-// bf16 from the 8-bit checkpoint: see the table's line; rows held in registers, with two blocks
-// of 512 threads an SM, took 66 us.
+// memory (cp.async) and reads back only those: no registers and no barriers for what is in
+// flight. g and xhat stay in registers over the row's sum, and the arithmetic is done two
+// elements at a time (packed fp32): with everything unpacked again after the sum, and single
+// operations, the instructions took as long as the copies. The columns' dweight sums stay in
+// registers throughout.
 constexpr int RING = 4;
 template <typename T>
 constexpr int RING_WARPS = sizeof(T) == 4 ? 8 : 16;  // a block's, for its ring to fit
 template <typename T, int NV, bool Q8>
 __global__ void __launch_bounds__(512, 1) k_rms_bwd_ring(const __grid_constant__ BwdArgs a, int wpr) {
   constexpr int EPV = 16 / sizeof(T);
+  constexpr int NP = EPV / 2;        // pairs per vector
   constexpr int HB = Q8 ? EPV : 16;  // bytes of a vector of h
-  extern __shared__ uint4 ring[];    // [RING][thread's vectors: dy, dh, h][NV][threads], then the groups' sums
-  __shared__ float red[2][MAX_WARPS];
+  constexpr int VSTEP = 32 * EPV;    // elements from one of a thread's vectors to the next
+  extern __shared__ uint4 ring[];    // [RING][dy, dh, h of the threads' vectors], then the groups' sums
+  __shared__ __align__(16) float red[2][4 * MAX_WARPS];
+  let_next_start();
   const int lane = threadIdx.x & 31, wb = threadIdx.x >> 5;
   const int rpb = blockDim.x / 32 / wpr;
   const int group = wb / wpr, w = wb - group * wpr;
   const int64_t g0 = (int64_t)blockIdx.x * rpb + group, step = (int64_t)gridDim.x * rpb;
-  const int stage = (int)blockDim.x * NV * (32 + HB);  // bytes
-  uint8_t* base = (uint8_t*)ring + threadIdx.x * 16;
-  uint8_t* hbase = (uint8_t*)ring + blockDim.x * NV * 32 + threadIdx.x * HB;
-  const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(base), shbase = (uint32_t)__cvta_generic_to_shared(hbase);
-  const uint32_t vstep = blockDim.x * 16, hstep = blockDim.x * HB;
-  auto fetch = [&](int64_t row, int slot) {
-    const bool live = row < a.N;
+  const int64_t c0 = ((int64_t)w * NV * 32 + lane) * EPV;
+  bool in[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
-      const bool in = live && c < a.H;
-      copy_async<16>(sbase + slot * stage + j * vstep, (const T*)a.dy + row * a.lddy + c, in);
-      copy_async<16>(sbase + slot * stage + (NV + j) * vstep, (const T*)a.dh + row * a.lddh + c, in && a.dh != nullptr);
-      if constexpr (Q8) copy_async<HB>(shbase + slot * stage + j * hstep, a.h8 + row * a.ldh8 + c, in);
-      else copy_async<16>(shbase + slot * stage + j * hstep, (const T*)a.h + row * a.ldh + c, in);
+  for (int j = 0; j < NV; ++j) in[j] = c0 + j * VSTEP < a.H;
+  for (int i = threadIdx.x; i < 8 * MAX_WARPS; i += blockDim.x) (&red[0][0])[i] = 0.0f;
+  __syncthreads();
+  float* gred = &red[0][0] + group * ((wpr + 3) & ~3);
+
+  const uint32_t stage = blockDim.x * NV * (32 + HB);  // bytes
+  const uint32_t vstep = blockDim.x * 16, hstep = blockDim.x * HB;
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+  const uint32_t hat = (uint32_t)__cvta_generic_to_shared(ring) + blockDim.x * NV * 32 + threadIdx.x * HB;
+  // where the next row to be copied lies
+  int64_t left = a.N - g0;  // rows from it on
+  const T* s_dy = (const T*)a.dy + g0 * a.lddy + c0;
+  const T* s_dh = (const T*)a.dh + g0 * a.lddh + c0;
+  const uint8_t* s_h = Q8 ? a.h8 + g0 * a.ldh8 + c0 : (const uint8_t*)((const T*)a.h + g0 * a.ldh + c0);
+  const int64_t hpitch = Q8 ? step * a.ldh8 : step * a.ldh * (int64_t)sizeof(T);
+  constexpr int HSTEP = VSTEP * (Q8 ? 1 : (int)sizeof(T));
+  const bool has_dh = a.dh != nullptr;
+  auto fetch = [&](uint32_t off) {
+    if (left > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (in[j]) {
+          copy_async<16>(at + off + j * vstep, s_dy + j * VSTEP);
+          if (has_dh) copy_async<16>(at + off + (NV + j) * vstep, s_dh + j * VSTEP);
+          copy_async<HB>(hat + off + j * hstep, s_h + j * HSTEP);
+        }
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    left -= step;
+    s_dy += step * a.lddy;
+    s_dh += step * a.lddh;
+    s_h += hpitch;
   };
-  Raw<T, EPV> wt[NV];
-  float dw[NV][EPV];
 #pragma unroll
-  for (int r = 0; r < RING - 1; ++r) fetch(g0 + r * step, r);
+  for (int r = 0; r < RING - 1; ++r) fetch(r * stage);
+
+  f2 wt[NV][NP], dw[NV][NP];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
-    wt[j].zero();
-    if (c < a.H) wt[j].load((const T*)a.w + c);
+    float v[EPV];
 #pragma unroll
-    for (int e = 0; e < EPV; ++e) dw[j][e] = 0.0f;
+    for (int e = 0; e < EPV; ++e) v[e] = 0.0f;
+    if (in[j]) Vec<T, EPV>::load((const T*)a.w + c0 + j * VSTEP, v);
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      wt[j][e] = f2_make(v[2 * e] + a.off, v[2 * e + 1] + a.off);
+      dw[j][e] = f2_make(0.0f, 0.0f);
+    }
   }
-  auto factors = [&](int64_t row, float& rs, float (&f)[NV]) {
-    rs = row < a.N ? a.rstd[row] : 0.0f;
+  // a row's 1/rms and block scales, read one turn ahead
+  const float* s_r = a.rstd + g0;
+  const float* s_f = Q8 ? a.h8s + g0 * a.nblk + c0 / Q_BLOCK : nullptr;
+  float rs_next = 0.0f, f_next[NV];
+  auto factors = [&](bool live) {
+    if (live) {
+      rs_next = *s_r;
+      s_r += step;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
-      f[j] = Q8 && row < a.N && c < a.H ? a.h8s[row * a.nblk + c / Q_BLOCK] : 1.0f;
+      for (int j = 0; j < NV; ++j) f_next[j] = Q8 && in[j] ? s_f[j * VSTEP / Q_BLOCK] : 1.0f;
+      s_f += step * a.nblk;
     }
   };
-  float rs_next, f_next[NV];
-  factors(g0, rs_next, f_next);
-  int slot = 0, buf = 0;
-  for (int64_t row = g0; row < a.N; row += step, buf ^= 1) {
+  factors(g0 < a.N);
+  T* dx = (T*)a.dx + g0 * a.lddx + c0;
+  uint32_t off = 0, free_off = (RING - 1) * stage;  // the slot of this row, and the one read last turn
+  int buf = 0;
+  for (int64_t row = g0; row < a.N; row += step, buf ^= 4 * MAX_WARPS) {
     const float rstd = rs_next;
     float f[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) f[j] = f_next[j] * rstd;
-    factors(row + step, rs_next, f_next);
-    fetch(row + (RING - 1) * step, slot == 0 ? RING - 1 : slot - 1);  // the slot read last turn
+    factors(row + step < a.N);
+    fetch(free_off);
     asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
-    const uint8_t* p = base + slot * stage;
-    const uint8_t* ph = hbase + slot * stage;
-    auto xhat = [&](int j, float (&x)[EPV]) {
-      if constexpr (Q8) {
-        RawQ<EPV> q;
-        q.load(ph + j * hstep);
-        q.unpack(x);
-      } else {
-        Raw<T, EPV> r;
-        const uint4 u = *(const uint4*)(ph + j * hstep);
-        r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
-        r.unpack(x);
-      }
-#pragma unroll
-      for (int e = 0; e < EPV; ++e) x[e] *= f[j];
-    };
-    auto vec = [&](int i, float (&x)[EPV]) {
+    auto vec = [&](uint32_t p, f2 (&x)[NP]) {
       Raw<T, EPV> r;
-      const uint4 u = *(const uint4*)(p + i * vstep);
-      r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
-      r.unpack(x);
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "r"(p));
+#pragma unroll
+      for (int e = 0; e < NP; ++e) x[e] = f2_make(r.get(2 * e), r.get(2 * e + 1));
     };
-    float dot = 0.0f;
+    f2 g[NV][NP], xh[NV][NP], dot = f2_make(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (((int64_t)(w * NV + j) * 32 + lane) * EPV < a.H) {
-        float x[EPV], d[EPV];
-        xhat(j, x);
-        vec(j, d);
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-          dot = fmaf(d[e] * (wt[j].get(e) + a.off), x[e], dot);
-          dw[j][e] = fmaf(d[e], x[e], dw[j][e]);
+      for (int e = 0; e < NP; ++e) g[j][e] = xh[j][e] = f2_make(0.0f, 0.0f);
+      if (in[j]) {
+        f2 d[NP], x[NP];
+        vec(at + off + j * vstep, d);
+        if constexpr (Q8) {
+          RawQ<EPV> q;
+          if constexpr (EPV == 8)
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q.w[0]), "=r"(q.w[1]) : "r"(hat + off + j * hstep));
+          else
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(q.w[0]) : "r"(hat + off + j * hstep));
+          float v[EPV];
+          q.unpack(v);
+#pragma unroll
+          for (int e = 0; e < NP; ++e) x[e] = f2_make(v[2 * e], v[2 * e + 1]);
+        } else {
+          vec(hat + off + j * hstep, x);
+        }
+        const f2 ff = f2_make(f[j], f[j]);
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+          xh[j][e] = f2_mul(x[e], ff);
+          g[j][e] = f2_mul(d[e], wt[j][e]);
+          dot = f2_fma(g[j][e], xh[j][e], dot);
+          dw[j][e] = f2_fma(d[e], xh[j][e], dw[j][e]);
         }
       }
     }
-    const float m = group_sum_own(dot, red[buf], wpr, wb, group) * a.inv_h;
+    float dlo, dhi;
+    f2_get(dot, dlo, dhi);
+    const float m = group_sum_own(dlo + dhi, gred + buf, wpr, w, group) * a.inv_h;
     if (a.dx != nullptr) {
+      const f2 r2 = f2_make(rstd, rstd), m2 = f2_make(-rstd * m, -rstd * m);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
-        if (c < a.H) {
-          float x[EPV], d[EPV], o[EPV];
-          xhat(j, x);
-          vec(j, d);
+        if (in[j]) {
+          f2 d[NP];
 #pragma unroll
-          for (int e = 0; e < EPV; ++e) o[e] = rstd * (d[e] * (wt[j].get(e) + a.off) - x[e] * m);
-          if (a.dh != nullptr) {
-            vec(NV + j, d);
+          for (int e = 0; e < NP; ++e) d[e] = f2_make(0.0f, 0.0f);
+          if (has_dh) vec(at + off + (NV + j) * vstep, d);
+          float o[EPV];
 #pragma unroll
-            for (int e = 0; e < EPV; ++e) o[e] += d[e];
-          }
-          Vec<T, EPV>::store((T*)a.dx + row * a.lddx + c, o);
+          for (int e = 0; e < NP; ++e)
+            f2_get(f2_fma(r2, g[j][e], f2_fma(m2, xh[j][e], d[e])), o[2 * e], o[2 * e + 1]);
+          Vec<T, EPV>::store(dx + j * VSTEP, o);
         }
       }
+      dx += step * a.lddx;
     }
-    slot = slot == RING - 1 ? 0 : slot + 1;
+    free_off = off;
+    off = off == (RING - 1) * stage ? 0 : off + stage;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (a.part == nullptr) return;
   __syncthreads();  // the ring's memory is free: it takes the groups' sums
-  put_partials<EPV, NV>(a, dw, (float*)ring, rpb, group, w, lane);
+  float dws[NV][EPV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < NP; ++e) f2_get(dw[j][e], dws[j][2 * e], dws[j][2 * e + 1]);
+  put_partials<EPV, NV>(a, dws, (float*)ring, rpb, group, w, lane);
 }
 
 // Backward of other rows: a row group walks the rows group, group + groups, ...; its threads keep their
@@ -355,6 +396,7 @@ template <typename T, int EPV, int NV, bool Q8>
 __global__ void __launch_bounds__(512, NV * EPV <= 16 ? 2 : 1) k_rms_bwd(const __grid_constant__ BwdArgs a, int wpr) {
   __shared__ float red[2][MAX_WARPS];
   extern __shared__ float sums[];  // [H] where the block has several groups
+  let_next_start();
   const int lane = threadIdx.x & 31, wb = threadIdx.x >> 5;
   const int rpb = blockDim.x / 32 / wpr;
   const int group = wb / wpr, w = wb - group * wpr;
@@ -475,6 +517,7 @@ __global__ void __launch_bounds__(256) k_rms_dw_long(const __grid_constant__ Bwd
 template <typename D>
 __global__ void __launch_bounds__(1024) k_rms_dw_sum(const float* part, int64_t rows, int64_t H, D* dw, bool ovw) {
   __shared__ float s[32][33];
+  after_previous();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float t = 0.0f;
@@ -728,10 +771,10 @@ extern "C" int32_t flce_rmsnorm_bwd(const flce_rmsnorm_bwd_args* x, void* stream
   if (e != cudaSuccess || !x->dweight) return cuda_status(e);
   const unsigned blocks = (unsigned)cdiv64(H, 32);
   if (x->dweight_dtype == FLCE_F32)
-    k_rms_dw_sum<float><<<blocks, 1024, 0, s>>>(a.part, rows, H, (float*)x->dweight, ovw);
+    e = launch_after(k_rms_dw_sum<float>, blocks, 1024, 0, s, a.part, rows, H, (float*)x->dweight, ovw);
   else if (x->dweight_dtype == FLCE_BF16)
-    k_rms_dw_sum<__nv_bfloat16><<<blocks, 1024, 0, s>>>(a.part, rows, H, (__nv_bfloat16*)x->dweight, ovw);
+    e = launch_after(k_rms_dw_sum<__nv_bfloat16>, blocks, 1024, 0, s, a.part, rows, H, (__nv_bfloat16*)x->dweight, ovw);
   else
-    k_rms_dw_sum<__half><<<blocks, 1024, 0, s>>>(a.part, rows, H, (__half*)x->dweight, ovw);
-  return cuda_status(cudaGetLastError());
+    e = launch_after(k_rms_dw_sum<__half>, blocks, 1024, 0, s, a.part, rows, H, (__half*)x->dweight, ovw);
+  return cuda_status(e);
 }
