@@ -86,19 +86,18 @@ cudaError_t fwd(const flce_embed_args& a, cudaStream_t s) {
 // passes the pairs on through the cluster's shared memory (8192 tokens: 9 us; with the pairs in
 // L2 and ranked twice a pass: 15 us). One block without cluster barriers takes up to 1024
 // tokens. k_sort takes lists of any length, with the pairs in L2.
+// Digits have 8, 9 or 10 bits, known to the compiler: the fewest that keep the passes.
 constexpr int SORT_CTAS = 8;
 constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int MAX_BITS = 10;
-constexpr int MAX_BINS = 1 << MAX_BITS;
-constexpr int BPT = MAX_BINS / SORT_THREADS;  // digits per thread
 
 struct SortArgs {
   const int64_t* tokens;
   int64_t ignore_index;
   int64_t V;
   int N;
-  int passes, bits;    // passes of `bits` bits each
+  int passes;
   uint32_t *k0, *p0;   // sorted keys and positions
   uint32_t *k1, *p1;   // the other list of k_sort, which starts in the one that makes it end in k0
   int* status;
@@ -121,10 +120,8 @@ __device__ __forceinline__ uint32_t remote_addr(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ uint32_t ld_remote(const uint32_t* p, uint32_t rank) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote_addr(p, rank)) : "memory");
-  return v;
+__device__ __forceinline__ void st_remote(const void* p, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote_addr(p, rank)), "r"(v) : "memory");
 }
 template <int CTAS>
 __device__ __forceinline__ void sort_barrier() {
@@ -143,53 +140,57 @@ __device__ __forceinline__ void mark_used(const SortArgs& a, uint32_t key) {
   if (a.used != nullptr && key < (uint32_t)a.V) atomicOr(a.used + (key >> 5), 1u << (key & 31));
 }
 
-// The lanes of `act` whose digit (of `bits` bits) is this lane's: a ballot per bit (the match
-// instruction takes a step per different digit: 1500 cycles for a tile of each of 32 warps).
-__device__ __forceinline__ unsigned same_digit(unsigned act, uint32_t d, int bits) {
+// The lanes of `act` whose digit is this lane's: a ballot per bit (the match instruction takes a
+// step per different digit: 1500 cycles for a tile of each of 32 warps).
+template <int BITS>
+__device__ __forceinline__ unsigned same_digit(unsigned act, uint32_t d) {
   unsigned peers = act;
 #pragma unroll
-  for (int b = 0; b < MAX_BITS; ++b) {
-    if (b < bits) {
-      const unsigned m = __ballot_sync(act, d >> b & 1u);
-      peers &= d >> b & 1u ? m : ~m;
-    }
+  for (int b = 0; b < BITS; ++b) {
+    const unsigned m = __ballot_sync(act, d >> b & 1u);
+    peers &= d >> b & 1u ? m : ~m;
   }
   return peers;
 }
 
 // Turns the warps' digit counts hist[w][bin] into the places of their first elements: sums over
 // the warps, the blocks of the cluster, and the digits before. Thread t has digits t * BPT ....
-template <int CTAS>
-__device__ __forceinline__ void sort_places(uint32_t* hist, uint32_t* tot, uint32_t* wsum, int bins, int rank) {
+// tot: [CTAS][bins], where every block leaves its counts in every block.
+template <int CTAS, int BITS>
+__device__ __forceinline__ void sort_places(uint32_t* hist, uint32_t* tot, uint32_t* wsum, int rank) {
+  constexpr int BINS = 1 << BITS, BPT = BINS > SORT_THREADS ? BINS / SORT_THREADS : 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t own[BPT], before[BPT], all[BPT], sum = 0;
+  const bool mine = tid * BPT < BINS;
+  uint32_t c[BPT][SORT_WARPS], before[BPT], all[BPT], sum = 0;
 #pragma unroll
   for (int i = 0; i < BPT; ++i) {
     const int b = tid * BPT + i;
-    own[i] = before[i] = all[i] = 0;
-    if (b < bins) {
+    before[i] = all[i] = 0;
+    if (mine) {
 #pragma unroll
-      for (int w = 0; w < SORT_WARPS; ++w) own[i] += hist[w * bins + b];
-      if (CTAS > 1) tot[b] = own[i];
+      for (int w = 0; w < SORT_WARPS; ++w) c[i][w] = hist[w * BINS + b];
+#pragma unroll
+      for (int w = 0; w < SORT_WARPS; ++w) all[i] += c[i][w];
+      if constexpr (CTAS > 1) {
+#pragma unroll
+        for (int r = 0; r < CTAS; ++r) st_remote(tot + rank * BINS + b, r, all[i]);
+      }
     }
   }
   if constexpr (CTAS > 1) {
     cluster_barrier();
 #pragma unroll
     for (int i = 0; i < BPT; ++i) {
-      const int b = tid * BPT + i;
-      if (b < bins) {
+      if (mine) {
+        all[i] = 0;
 #pragma unroll
-        for (int c = 0; c < CTAS; ++c) {
-          const uint32_t v = ld_remote(tot + b, c);
-          before[i] += c < rank ? v : 0;
+        for (int r = 0; r < CTAS; ++r) {
+          const uint32_t v = tot[r * BINS + tid * BPT + i];
+          before[i] += r < rank ? v : 0;
           all[i] += v;
         }
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < BPT; ++i) all[i] = own[i];
   }
 #pragma unroll
   for (int i = 0; i < BPT; ++i) sum += all[i];
@@ -202,17 +203,16 @@ __device__ __forceinline__ void sort_places(uint32_t* hist, uint32_t* tot, uint3
   if (lane == 31) wsum[warp] = x;
   __syncthreads();
   uint32_t base = x - sum;
-  for (int w = 0; w < warp; ++w) base += wsum[w];
+#pragma unroll
+  for (int w = 0; w < SORT_WARPS; ++w) base += w < warp ? wsum[w] : 0;
 #pragma unroll
   for (int i = 0; i < BPT; ++i) {
-    const int b = tid * BPT + i;
-    if (b < bins) {
+    if (mine) {
       uint32_t at = base + before[i];
 #pragma unroll
       for (int w = 0; w < SORT_WARPS; ++w) {
-        const uint32_t c = hist[w * bins + b];
-        hist[w * bins + b] = at;
-        at += c;
+        hist[w * BINS + tid * BPT + i] = at;
+        at += c[i][w];
       }
     }
     base += all[i];
@@ -229,26 +229,26 @@ __device__ __forceinline__ void sort_prepare(const SortArgs& a, int rank) {
   }
 }
 
-constexpr size_t sort_smem(int bits, int held) {
-  return ((size_t)(SORT_WARPS + 1) << bits) * 4 + SORT_WARPS * 4 + (size_t)held * 8;
+// hist, tot, wsum and the pairs held in shared memory
+constexpr size_t sort_smem(int ctas, int bits, int held) {
+  return ((size_t)(SORT_WARPS + ctas) << bits) * 4 + SORT_WARPS * 4 + (size_t)held * 8;
 }
 
 // TILES tiles of 32 pairs per warp. Pairs past N have the largest key and stay behind the others.
-template <int CTAS, int TILES>
+template <int CTAS, int TILES, int BITS>
 __global__ void __launch_bounds__(SORT_THREADS, 1) k_sort_reg(const __grid_constant__ SortArgs a) {
   constexpr int PER = SORT_WARPS * TILES * 32;  // pairs per block
+  constexpr int BINS = 1 << BITS;
+  constexpr uint32_t MASK = BINS - 1;
   extern __shared__ uint2 dyn[];
   uint2* buf = dyn;                             // [PER]
-  const int bins = 1 << a.bits;
-  uint32_t* hist = (uint32_t*)(dyn + PER);      // [SORT_WARPS][bins]
-  uint32_t* tot = hist + SORT_WARPS * bins;     // [bins]
-  uint32_t* wsum = tot + bins;                  // [SORT_WARPS]
+  uint32_t* hist = (uint32_t*)(dyn + PER);      // [SORT_WARPS][BINS]
+  uint32_t* tot = hist + SORT_WARPS * BINS;     // [CTAS][BINS]
+  uint32_t* wsum = tot + CTAS * BINS;           // [SORT_WARPS]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = CTAS > 1 ? (int)cluster_rank() : 0;
-  const uint32_t mask = (uint32_t)bins - 1;
-  uint32_t* h = hist + warp * bins;
+  uint32_t* h = hist + warp * BINS;
   let_next_start();
-  sort_prepare<CTAS>(a, rank);
   uint32_t key[TILES], pos[TILES], off[TILES];
 #pragma unroll
   for (int j = 0; j < TILES; ++j) {
@@ -256,29 +256,34 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) k_sort_reg(const __grid_const
     pos[j] = (uint32_t)i;
     key[j] = i < a.N ? sort_key(a, i) : 0xffffffffu;
   }
+  sort_prepare<CTAS>(a, rank);
   if (a.used != nullptr) {
 #pragma unroll
     for (int j = 0; j < TILES; ++j) mark_used(a, key[j]);
   }
+  if (CTAS > 1) cluster_barrier();  // every block has started: its shared memory may be written
   for (int pass = 0; pass < a.passes; ++pass) {
-    const int shift = pass * a.bits;
-    for (int b = lane; b < bins; b += 32) h[b] = 0;
+    const int shift = pass * BITS;
+    const bool last = pass + 1 == a.passes;
+#pragma unroll
+    for (int b = 0; b < BINS / 32; ++b) h[b * 32 + lane] = 0;
     __syncwarp();
+    unsigned peers[TILES];
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) peers[j] = same_digit<BITS>(0xffffffffu, (key[j] >> shift) & MASK);
 #pragma unroll
     for (int j = 0; j < TILES; ++j) {
-      const uint32_t d = (key[j] >> shift) & mask;
-      const unsigned peers = same_digit(0xffffffffu, d, a.bits);
-      off[j] = h[d] + __popc(peers & ((1u << lane) - 1));
+      const uint32_t d = (key[j] >> shift) & MASK;
+      off[j] = h[d] + __popc(peers[j] & ((1u << lane) - 1));
       __syncwarp();
-      if (lane == __ffs(peers) - 1) h[d] = off[j] + __popc(peers);
+      if (lane == __ffs(peers[j]) - 1) h[d] = off[j] + __popc(peers[j]);
       __syncwarp();
     }
     __syncthreads();
-    sort_places<CTAS>(hist, tot, wsum, bins, rank);
-    const bool last = pass + 1 == a.passes;
+    sort_places<CTAS, BITS>(hist, tot, wsum, rank);
 #pragma unroll
     for (int j = 0; j < TILES; ++j) {
-      const uint32_t at = h[(key[j] >> shift) & mask] + off[j];
+      const uint32_t at = h[(key[j] >> shift) & MASK] + off[j];
       if (last) {
         if (at < (uint32_t)a.N) {
           a.k0[at] = key[j];
@@ -293,32 +298,32 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) k_sort_reg(const __grid_const
         buf[at] = make_uint2(key[j], pos[j]);
       }
     }
+    if (last) break;      // nothing of another block's is touched after the last barrier
     sort_barrier<CTAS>();  // the pairs are in place, and every block has read the counts
-    if (!last) {
 #pragma unroll
-      for (int j = 0; j < TILES; ++j) {
-        const uint2 v = buf[(warp * TILES + j) * 32 + lane];
-        key[j] = v.x;
-        pos[j] = v.y;
-      }
-      if constexpr (CTAS == 1) __syncthreads();  // (a cluster's next scatter comes after its own barrier)
+    for (int j = 0; j < TILES; ++j) {
+      const uint2 v = buf[(warp * TILES + j) * 32 + lane];
+      key[j] = v.x;
+      pos[j] = v.y;
     }
   }
 }
 
+template <int BITS>
 __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS, 1)
     k_sort(const __grid_constant__ SortArgs a) {
+  constexpr int BINS = 1 << BITS;
+  constexpr uint32_t MASK = BINS - 1;
   extern __shared__ uint2 dyn[];
-  const int bins = 1 << a.bits;
-  uint32_t* hist = (uint32_t*)dyn;              // [SORT_WARPS][bins]
-  uint32_t* tot = hist + SORT_WARPS * bins;     // [bins]
-  uint32_t* wsum = tot + bins;                  // [SORT_WARPS]
+  uint32_t* hist = (uint32_t*)dyn;              // [SORT_WARPS][BINS]
+  uint32_t* tot = hist + SORT_WARPS * BINS;     // [SORT_CTAS][BINS]
+  uint32_t* wsum = tot + SORT_CTAS * BINS;      // [SORT_WARPS]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = (int)cluster_rank();
-  const uint32_t mask = (uint32_t)bins - 1;
-  uint32_t* h = hist + warp * bins;
+  uint32_t* h = hist + warp * BINS;
   let_next_start();
   sort_prepare<SORT_CTAS>(a, rank);
+  cluster_barrier();  // every block has started: its shared memory may be written
   // this warp's part of the list, in whole tiles of 32
   const int64_t tiles = ((int64_t)a.N + 31) / 32;
   const int64_t gw = (int64_t)rank * SORT_WARPS + warp, nw = SORT_CTAS * SORT_WARPS;
@@ -329,31 +334,31 @@ __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS
     const uint32_t* ps = to0 ? a.p1 : a.p0;
     uint32_t* kd = to0 ? a.k0 : a.k1;
     uint32_t* pd = to0 ? a.p0 : a.p1;
-    const int shift = pass * a.bits;
-    for (int b = lane; b < bins; b += 32) h[b] = 0;
+    const int shift = pass * BITS;
+    for (int b = lane; b < BINS; b += 32) h[b] = 0;
     __syncwarp();
     for (int64_t i = i0 + lane; i - lane < i1; i += 32) {
       const bool in = i < i1;
       const unsigned act = __ballot_sync(0xffffffffu, in);
       if (in) {
         const uint32_t key = pass == 0 ? sort_key(a, (int)i) : __ldcg(ks + i);
-        const uint32_t d = (key >> shift) & mask;
-        const unsigned peers = same_digit(act, d, a.bits);
+        const uint32_t d = (key >> shift) & MASK;
+        const unsigned peers = same_digit<BITS>(act, d);
         if (lane == __ffs(peers) - 1) h[d] += __popc(peers);
         if (pass == 0) mark_used(a, key);
       }
       __syncwarp();
     }
     __syncthreads();
-    sort_places<SORT_CTAS>(hist, tot, wsum, bins, rank);
+    sort_places<SORT_CTAS, BITS>(hist, tot, wsum, rank);
     for (int64_t i = i0 + lane; i - lane < i1; i += 32) {
       const bool in = i < i1;
       const unsigned act = __ballot_sync(0xffffffffu, in);
       if (in) {
         const uint32_t key = pass == 0 ? sort_key(a, (int)i) : __ldcg(ks + i);
         const uint32_t pos = pass == 0 ? (uint32_t)i : __ldcg(ps + i);
-        const uint32_t d = (key >> shift) & mask;
-        const unsigned peers = same_digit(act, d, a.bits);
+        const uint32_t d = (key >> shift) & MASK;
+        const unsigned peers = same_digit<BITS>(act, d);
         const uint32_t at = h[d] + __popc(peers & ((1u << lane) - 1));
         kd[at] = key;
         pd[at] = pos;
@@ -366,57 +371,58 @@ __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS
   }
 }
 
-template <int CTAS, int TILES>
-cudaError_t launch_sort_reg(const SortArgs& a, cudaStream_t s) {
-  constexpr int held = SORT_WARPS * TILES * 32;
-  // the shared-memory limit, once per device
-  static std::atomic<bool> raised[64];
+// One cluster of `ctas` blocks of kern; the shared-memory limit is raised once per kernel and device.
+template <typename K>
+cudaError_t launch_cluster(K kern, int ctas, size_t smem, const SortArgs& a, cudaStream_t s, std::atomic<bool>* raised) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!raised[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(k_sort_reg<CTAS, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sort_smem(MAX_BITS, held));
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     raised[dev].store(true, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CTAS;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(CTAS, 1, 1);
+  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
   cfg.blockDim = dim3(SORT_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = sort_smem(a.bits, held);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_sort_reg<CTAS, TILES>, a);
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-cudaError_t launch_sort(const SortArgs& a, cudaStream_t s) {
-  const int64_t tiles = cdiv64(a.N, 32), warps = SORT_CTAS * SORT_WARPS;
-  if (tiles <= SORT_WARPS) return launch_sort_reg<1, 1>(a, s);
-  if (tiles <= 2 * SORT_WARPS) return launch_sort_reg<1, 2>(a, s);
-  if (tiles <= warps) return launch_sort_reg<SORT_CTAS, 1>(a, s);
-  if (tiles <= 2 * warps) return launch_sort_reg<SORT_CTAS, 2>(a, s);
-  if (tiles <= 4 * warps) return launch_sort_reg<SORT_CTAS, 4>(a, s);
-  if (tiles <= 8 * warps) return launch_sort_reg<SORT_CTAS, 8>(a, s);
-  if (tiles <= 16 * warps) return launch_sort_reg<SORT_CTAS, 16>(a, s);
+template <int CTAS, int TILES, int BITS>
+cudaError_t launch_sort_reg(const SortArgs& a, cudaStream_t s) {
   static std::atomic<bool> raised[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!raised[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(k_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sort_smem(MAX_BITS, 0));
-    if (e != cudaSuccess) return e;
-    raised[dev].store(true, std::memory_order_relaxed);
-  }
-  k_sort<<<SORT_CTAS, SORT_THREADS, sort_smem(a.bits, 0), s>>>(a);
-  return cudaGetLastError();
+  return launch_cluster(k_sort_reg<CTAS, TILES, BITS>, CTAS, sort_smem(CTAS, BITS, SORT_WARPS * TILES * 32), a, s, raised);
+}
+
+template <int BITS>
+cudaError_t launch_sort_bits(const SortArgs& a, cudaStream_t s) {
+  const int64_t tiles = cdiv64(a.N, 32), warps = SORT_CTAS * SORT_WARPS;
+  if (tiles <= SORT_WARPS) return launch_sort_reg<1, 1, BITS>(a, s);
+  if (tiles <= 2 * SORT_WARPS) return launch_sort_reg<1, 2, BITS>(a, s);
+  if (tiles <= warps) return launch_sort_reg<SORT_CTAS, 1, BITS>(a, s);
+  if (tiles <= 2 * warps) return launch_sort_reg<SORT_CTAS, 2, BITS>(a, s);
+  if (tiles <= 4 * warps) return launch_sort_reg<SORT_CTAS, 4, BITS>(a, s);
+  if (tiles <= 8 * warps) return launch_sort_reg<SORT_CTAS, 8, BITS>(a, s);
+  if (tiles <= 16 * warps) return launch_sort_reg<SORT_CTAS, 16, BITS>(a, s);
+  static std::atomic<bool> raised[64];
+  return launch_cluster(k_sort<BITS>, SORT_CTAS, sort_smem(SORT_CTAS, BITS, 0), a, s, raised);
+}
+
+// kb: bits of the largest key
+cudaError_t launch_sort(SortArgs a, int kb, cudaStream_t s) {
+  a.passes = (kb + MAX_BITS - 1) / MAX_BITS;
+  const int bits = (kb + a.passes - 1) / a.passes;
+  return bits <= 8 ? launch_sort_bits<8>(a, s) : bits == 9 ? launch_sort_bits<9>(a, s) : launch_sort_bits<10>(a, s);
 }
 
 // ------------------------------------------------------------------ sums
@@ -742,8 +748,6 @@ extern "C" int32_t flce_embed_bwd(const flce_embed_args* x, void* stream) {
   so.N = (int)x->N;
   int kb = 1;
   while ((x->V >> kb) != 0) ++kb;  // bits of the largest key, V
-  so.passes = (kb + MAX_BITS - 1) / MAX_BITS;
-  so.bits = (kb + so.passes - 1) / so.passes;
   so.k0 = (uint32_t*)(ws + l.k0);
   so.p0 = (uint32_t*)(ws + l.p0);
   so.k1 = (uint32_t*)(ws + l.k1);
@@ -755,7 +759,7 @@ extern "C" int32_t flce_embed_bwd(const flce_embed_args* x, void* stream) {
   so.nused = l.nused;
   a.keys = so.k0;
   a.pos = so.p0;
-  e = launch_sort(so, s);
+  e = launch_sort(so, kb, s);
   if (e != cudaSuccess) return cuda_status(e);
 
   const bool same = x->dE_dtype == x->dtype;
