@@ -83,7 +83,7 @@ cudaError_t fwd(const flce_embed_args& a, cudaStream_t s) {
 // place. Two passes of up to 10 bits do for a vocabulary below 2^20.
 //
 // Short lists are bound by latency: k_sort_reg keeps its pairs and their ranks in registers and
-// passes the pairs on through the cluster's shared memory (8192 tokens: 9 us; with the pairs in
+// passes the pairs on through the cluster's shared memory (8192 tokens: 10 us; with the pairs in
 // L2 and ranked twice a pass: 15 us). One block without cluster barriers takes up to 1024
 // tokens. k_sort takes lists of any length, with the pairs in L2.
 // Digits have 8, 9 or 10 bits, known to the compiler: the fewest that keep the passes.
@@ -103,8 +103,10 @@ struct SortArgs {
   int* status;
   int* count;          // [pieces][slices] zeroed for k_embed_sum
   int ncount;
-  uint32_t* used;      // bit v: token v occurs; null when not wanted
-  int nused;           // its words
+  // what the launch's other blocks zero (FLCE_FLAG_DW_OVERWRITE): `zrows` rows of `zlen` bytes, at
+  // a pitch of `zpitch`; zrows = 0: nothing, and no other blocks
+  uint8_t* zero;
+  int64_t zrows, zlen, zpitch;
 };
 
 __device__ __forceinline__ void cluster_barrier() {
@@ -136,10 +138,6 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int i) {
   if (!live && t != a.ignore_index && a.status != nullptr) atomicOr(a.status, ST_TARGET_RANGE);
   return live ? (uint32_t)t : (uint32_t)a.V;
 }
-__device__ __forceinline__ void mark_used(const SortArgs& a, uint32_t key) {
-  if (a.used != nullptr && key < (uint32_t)a.V) atomicOr(a.used + (key >> 5), 1u << (key & 31));
-}
-
 // The lanes of `act` whose digit is this lane's: a ballot per bit (the match instruction takes a
 // step per different digit: 1500 cycles for a tile of each of 32 warps).
 template <int BITS>
@@ -223,9 +221,24 @@ __device__ __forceinline__ void sort_places(uint32_t* hist, uint32_t* tot, uint3
 template <int CTAS>
 __device__ __forceinline__ void sort_prepare(const SortArgs& a, int rank) {
   for (int i = rank * SORT_THREADS + (int)threadIdx.x; i < a.ncount; i += CTAS * SORT_THREADS) a.count[i] = 0;
-  if (a.used != nullptr) {
-    for (int i = rank * SORT_THREADS + (int)threadIdx.x; i < a.nused; i += CTAS * SORT_THREADS) a.used[i] = 0u;
-    sort_barrier<CTAS>();
+}
+
+// The blocks behind those that sort: zeroes, while few SMs are busy with the list. The rows that
+// tokens point to are written again by the sums; that costs less than finding out which they are.
+// Block z of nz takes every nz-th piece of 64 KB (of a row, where rows lie apart).
+__device__ __forceinline__ void zero_rows(const SortArgs& a, int z, int nz) {
+  constexpr int64_t CHUNK = 65536;
+  const int64_t per = (a.zlen + CHUNK - 1) / CHUNK, all = a.zrows * per;
+  for (int64_t i = z; i < all; i += nz) {
+    const int64_t row = i / per, o = (i - row * per) * CHUNK;
+    uint8_t* p = a.zero + row * a.zpitch + o;
+    const int64_t len = min(CHUNK, a.zlen - o);
+    // two bytes at a time up to a 16-byte boundary, 16 bytes at a time, two bytes at a time again
+    const int64_t head = min((int64_t)((16 - (uintptr_t)p % 16) % 16), len);
+    const int64_t body = (len - head) / 16, tail = head + body * 16;
+    for (int64_t t = 2 * threadIdx.x; t < head; t += 2 * SORT_THREADS) *(uint16_t*)(p + t) = 0;
+    for (int64_t t = threadIdx.x; t < body; t += SORT_THREADS) ((uint4*)(p + head))[t] = make_uint4(0u, 0u, 0u, 0u);
+    for (int64_t t = tail + 2 * threadIdx.x; t < len; t += 2 * SORT_THREADS) *(uint16_t*)(p + t) = 0;
   }
 }
 
@@ -249,6 +262,10 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) k_sort_reg(const __grid_const
   const int rank = CTAS > 1 ? (int)cluster_rank() : 0;
   uint32_t* h = hist + warp * BINS;
   let_next_start();
+  if ((int)blockIdx.x >= CTAS) {
+    zero_rows(a, (int)blockIdx.x - CTAS, (int)gridDim.x - CTAS);
+    return;
+  }
   uint32_t key[TILES], pos[TILES], off[TILES];
 #pragma unroll
   for (int j = 0; j < TILES; ++j) {
@@ -257,10 +274,6 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) k_sort_reg(const __grid_const
     key[j] = i < a.N ? sort_key(a, i) : 0xffffffffu;
   }
   sort_prepare<CTAS>(a, rank);
-  if (a.used != nullptr) {
-#pragma unroll
-    for (int j = 0; j < TILES; ++j) mark_used(a, key[j]);
-  }
   if (CTAS > 1) cluster_barrier();  // every block has started: its shared memory may be written
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = pass * BITS;
@@ -322,6 +335,10 @@ __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS
   const int rank = (int)cluster_rank();
   uint32_t* h = hist + warp * BINS;
   let_next_start();
+  if ((int)blockIdx.x >= SORT_CTAS) {
+    zero_rows(a, (int)blockIdx.x - SORT_CTAS, (int)gridDim.x - SORT_CTAS);
+    return;
+  }
   sort_prepare<SORT_CTAS>(a, rank);
   cluster_barrier();  // every block has started: its shared memory may be written
   // this warp's part of the list, in whole tiles of 32
@@ -345,7 +362,6 @@ __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS
         const uint32_t d = (key >> shift) & MASK;
         const unsigned peers = same_digit<BITS>(act, d);
         if (lane == __ffs(peers) - 1) h[d] += __popc(peers);
-        if (pass == 0) mark_used(a, key);
       }
       __syncwarp();
     }
@@ -371,7 +387,8 @@ __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS
   }
 }
 
-// One cluster of `ctas` blocks of kern; the shared-memory limit is raised once per kernel and device.
+// One cluster of `ctas` blocks of kern that sorts, and with something to zero a block for each
+// other SM (in whole clusters); the shared-memory limit is raised once per kernel and device.
 template <typename K>
 cudaError_t launch_cluster(K kern, int ctas, size_t smem, const SortArgs& a, cudaStream_t s, std::atomic<bool>* raised) {
   int dev = 0;
@@ -389,7 +406,7 @@ cudaError_t launch_cluster(K kern, int ctas, size_t smem, const SortArgs& a, cud
   attr[0].val.clusterDim.x = (unsigned)ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  cfg.gridDim = dim3((unsigned)(a.zrows ? (num_sms() + ctas - 1) / ctas * ctas : ctas), 1, 1);
   cfg.blockDim = dim3(SORT_THREADS, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -427,8 +444,7 @@ cudaError_t launch_sort(SortArgs a, int kb, cudaStream_t s) {
 
 // ------------------------------------------------------------------ sums
 constexpr int PIECE = 32;       // sorted positions per block
-constexpr int BATCH = 4;        // rows in flight per thread
-constexpr int ZERO_ROWS = 64;   // rows of dE per block that zeroes unused ones
+constexpr int BATCH = 8;        // rows in flight per thread
 
 struct SumArgs {
   const uint32_t *keys, *pos;  // sorted
@@ -440,37 +456,51 @@ struct SumArgs {
   int64_t lddE;
   float scale;
   int ovw;
-  int pieces, slices;   // blocks: pieces x slices that sum, then those that zero
+  int pieces, slices;   // blocks: pieces x slices
   float* part;          // [pieces][2][H]: a piece's run that began before it, and its last run
                         // where that goes on past it
   int* count;           // [pieces][slices]: parts left of the run that begins in the piece
-  const uint32_t* used;
 };
 
 // A run whose rows lie in several pieces: each piece leaves a partial row, and the block that
-// leaves the last one adds them up in piece order. x0: the piece where the run begins, k: its
-// key. Returns whether this block is the last; np: the number of pieces.
-__device__ __forceinline__ bool last_of_run(const SumArgs& a, int x0, uint32_t k, int slice, int& np) {
-  __shared__ int sh[2];
+// leaves the last one adds them up in piece order. x: this piece, whose first key is k when the
+// run began before it (head). Returns whether this block is the last; x0: the piece where the
+// run begins, np: the number of pieces. The piece borders are looked at 32 at a time.
+__device__ __forceinline__ bool last_of_run(const SumArgs& a, int x, bool head, uint32_t k, int slice, int& x0, int& np) {
+  __shared__ int sh[3];
   __threadfence();
   __syncthreads();
   if (threadIdx.x < 32) {
-    // pieces x0 + 1 ... that begin with the key
-    int n = 1;
-    for (;;) {
-      const int p = x0 + n + (int)threadIdx.x;
-      const bool in = p < a.pieces && __ldg(a.keys + (int64_t)p * PIECE) == k;
-      const unsigned b = __ballot_sync(0xffffffffu, in);
-      n += b == 0xffffffffu ? 32 : __ffs(~b) - 1;
-      if (b != 0xffffffffu) break;
+    const int lane = (int)threadIdx.x;
+    int b0 = x;
+    if (head) {
+      for (b0 = x - 1;; b0 -= 32) {  // back over the pieces that it runs into from the one before
+        const int p = b0 - lane;
+        const bool in = p > 0 && __ldg(a.keys + (int64_t)p * PIECE - 1) == k;
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        if (m != 0xffffffffu) {
+          b0 -= __ffs(~m) - 1;
+          break;
+        }
+      }
     }
-    if (threadIdx.x == 0) {
-      sh[0] = atomicAdd(a.count + (int64_t)x0 * a.slices + slice, 1) == n - 1;
+    int n = x - b0 + 1;
+    for (;;) {  // and on over those that begin with it
+      const int p = b0 + n + lane;
+      const bool in = p < a.pieces && __ldg(a.keys + (int64_t)p * PIECE) == k;
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      n += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+      if (m != 0xffffffffu) break;
+    }
+    if (lane == 0) {
+      sh[0] = atomicAdd(a.count + (int64_t)b0 * a.slices + slice, 1) == n - 1;
       sh[1] = n;
+      sh[2] = b0;
     }
   }
   __syncthreads();
   np = sh[1];
+  x0 = sh[2];
   const bool last = sh[0] != 0;
   if (last) __threadfence();
   return last;
@@ -503,28 +533,10 @@ struct RowOf {  // EPV elements of dE in accesses of at most 32 bytes
 
 // Blocks 0 .. pieces * slices - 1: piece x = block / slices, columns (block % slices) * threads *
 // EPV .... BATCH rows of dout are loaded together, and with them the rows of dE that their runs
-// end at. The blocks after those zero the rows of dE that no token points to
-// (FLCE_FLAG_DW_OVERWRITE).
+// end at.
 template <typename T, typename D, int EPV>
 __global__ void __launch_bounds__(128) k_embed_sum(const __grid_constant__ SumArgs a) {
-  const int sums = a.pieces * a.slices;
   after_previous();
-  if ((int)blockIdx.x >= sums) {
-    const int64_t v0 = (int64_t)(blockIdx.x - sums) * ZERO_ROWS;
-    for (int r = 0; r < ZERO_ROWS && v0 + r < a.V; ++r) {
-      const int64_t v = v0 + r;
-      if (a.used[v >> 5] >> (v & 31) & 1u) continue;
-      // single elements up to a 16-byte boundary, 16 bytes at a time, single elements again
-      D* p = (D*)a.dE + v * a.lddE;
-      const int64_t head = min((int64_t)((16 - (uintptr_t)p % 16) % 16 / sizeof(D)), a.H);
-      const int64_t body = (a.H - head) / (16 / (int)sizeof(D));
-      const int64_t tail = head + body * (16 / (int)sizeof(D));
-      if (threadIdx.x < head) p[threadIdx.x] = from_f<D>(0.0f);
-      for (int64_t i = threadIdx.x; i < body; i += blockDim.x) ((uint4*)(p + head))[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (tail + threadIdx.x < a.H) p[tail + threadIdx.x] = from_f<D>(0.0f);
-    }
-    return;
-  }
   __shared__ uint32_t key[PIECE + 2], pos[PIECE];
   const int x = blockIdx.x / a.slices, slice = blockIdx.x - x * a.slices;
   const int i0 = x * PIECE;
@@ -544,7 +556,7 @@ __global__ void __launch_bounds__(128) k_embed_sum(const __grid_constant__ SumAr
 #pragma unroll
   for (int e = 0; e < EPV; ++e) s[e] = 0.0f;
   const bool head = key[0] == key[1];   // the first run began in an earlier piece
-  bool first = true;
+  bool first = true, left_head = false, left_tail = false;
   for (int b = 0; b < n; b += BATCH) {
     Raw<T, EPV> r[BATCH];
     RowOf<D, EPV> old[BATCH];
@@ -574,34 +586,8 @@ __global__ void __launch_bounds__(128) k_embed_sum(const __grid_constant__ SumAr
 #pragma unroll
               for (int e = 0; e < EPV; ++e) __stcg(p + e, s[e]);
             }
-            int x0 = x;
-            if (began) {  // where did it begin? the first piece whose last key is k
-              int lo = 0, hi = x - 1;
-              while (lo < hi) {
-                const int m = (lo + hi) / 2;
-                if (__ldg(a.keys + (int64_t)(m + 1) * PIECE - 1) < k) lo = m + 1;
-                else hi = m;
-              }
-              x0 = lo;
-            }
-            int np;
-            if (last_of_run(a, x0, k, slice, np) && in) {
-              const float* q = a.part + ((int64_t)x0 * 2 + 1) * a.H + c;
-              float t[EPV];
-#pragma unroll
-              for (int e = 0; e < EPV; ++e) t[e] = __ldcg(q + e);
-              q += a.H;  // slot 0 of the next piece
-#pragma unroll 4
-              for (int m = 1; m < np; ++m, q += 2 * a.H) {
-#pragma unroll
-                for (int e = 0; e < EPV; ++e) t[e] += __ldcg(q + e);
-              }
-              D* d = (D*)a.dE + (int64_t)k * a.lddE + c;
-              RowOf<D, EPV> o;
-              o.zero();
-              if (!a.ovw) o.load(d);
-              o.add_store(d, t, a.scale);
-            }
+            left_head |= began;
+            left_tail |= !began;
           } else if (in) {
             old[j].add_store((D*)a.dE + (int64_t)k * a.lddE + c, s, a.scale);
           }
@@ -612,15 +598,36 @@ __global__ void __launch_bounds__(128) k_embed_sum(const __grid_constant__ SumAr
       }
     }
   }
+  // the partial rows left: of the run that began before the piece, and of the one that goes on
+  for (int tail = 0; tail < 2; ++tail) {
+    if (!(tail ? left_tail : left_head)) continue;
+    const uint32_t k = tail ? key[n] : key[1];
+    int x0, np;
+    if (!last_of_run(a, x, tail == 0, k, slice, x0, np) || !in) continue;
+    const float* q = a.part + ((int64_t)x0 * 2 + 1) * a.H + c;
+    float t[EPV];
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) t[e] = __ldcg(q + e);
+    q += a.H;  // slot 0 of the next piece
+#pragma unroll 4
+    for (int m = 1; m < np; ++m, q += 2 * a.H) {
+#pragma unroll
+      for (int e = 0; e < EPV; ++e) t[e] += __ldcg(q + e);
+    }
+    D* d = (D*)a.dE + (int64_t)k * a.lddE + c;
+    RowOf<D, EPV> o;
+    o.zero();
+    if (!a.ovw) o.load(d);
+    o.add_store(d, t, a.scale);
+  }
 }
 
 struct Layout {
-  size_t k0, p0, k1, p1, count, used, part, total;
-  int ncount, nused;
+  size_t k0, p0, k1, p1, count, part, total;
 };
 // Column slices of the sums: the narrowest (single elements) decide the counters' size.
 int64_t max_slices(int64_t H) { return cdiv64(H, 32); }
-Layout layout(int64_t N, int64_t H, int64_t V) {
+Layout layout(int64_t N, int64_t H) {
   Layout l;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -634,8 +641,6 @@ Layout layout(int64_t N, int64_t H, int64_t V) {
   l.k1 = take(4 * (size_t)N);
   l.p1 = take(4 * (size_t)N);
   l.count = take(4 * (size_t)pieces * max_slices(H));
-  l.nused = (int)cdiv64(V, 32);
-  l.used = take(N > 0 ? 4 * (size_t)l.nused : 0);
   l.part = take((size_t)pieces * 2 * (size_t)H * 4);
   l.total = off ? off : 256;
   return l;
@@ -651,7 +656,7 @@ void sum_shape(int64_t H, int epv, int& threads, int& slices) {
 template <typename T, typename D>
 cudaError_t sums(SumArgs a, int epv, int threads, cudaStream_t s) {
   constexpr int W = 16 / sizeof(T);
-  const unsigned blocks = (unsigned)(a.pieces * a.slices + (a.ovw ? cdiv64(a.V, ZERO_ROWS) : 0));
+  const unsigned blocks = (unsigned)(a.pieces * a.slices);
   if (epv == W) return launch_after(k_embed_sum<T, D, W>, blocks, threads, 0, s, a);
   return launch_after(k_embed_sum<T, D, 1>, blocks, threads, 0, s, a);
 }
@@ -695,7 +700,7 @@ extern "C" int32_t flce_embed_fwd(const flce_embed_args* x, void* stream) {
 }
 
 extern "C" size_t flce_embed_workspace_size(int64_t N, int64_t H, int64_t V) {
-  return sizes_ok(N, H, V) ? layout(N, H, V).total : 0;
+  return sizes_ok(N, H, V) ? layout(N, H).total : 0;
 }
 
 extern "C" int32_t flce_embed_bwd(const flce_embed_args* x, void* stream) {
@@ -708,7 +713,7 @@ extern "C" int32_t flce_embed_bwd(const flce_embed_args* x, void* stream) {
   if (x->N > 0) {
     if (!x->dout || !aligned_to(x->dout, esz) || x->lddout < x->H) return FLCE_ERR_INVALID_ARG;
     if (!x->workspace || !aligned_to(x->workspace, 256)) return FLCE_ERR_INVALID_ARG;
-    if (x->workspace_bytes < layout(x->N, x->H, x->V).total) return FLCE_ERR_WORKSPACE;
+    if (x->workspace_bytes < layout(x->N, x->H).total) return FLCE_ERR_WORKSPACE;
   }
   const bool ovw = (x->flags & FLCE_FLAG_DW_OVERWRITE) != 0;
   cudaStream_t s = (cudaStream_t)stream;
@@ -718,7 +723,7 @@ extern "C" int32_t flce_embed_bwd(const flce_embed_args* x, void* stream) {
     e = cudaMemset2DAsync(x->dE, (size_t)x->lddE * dsz, 0, (size_t)x->H * dsz, (size_t)x->V, s);
   if (e != cudaSuccess || x->N == 0) return cuda_status(e);
 
-  const Layout l = layout(x->N, x->H, x->V);
+  const Layout l = layout(x->N, x->H);
   char* ws = (char*)x->workspace;
   SumArgs a = {};
   a.N = (int)x->N;
@@ -733,7 +738,6 @@ extern "C" int32_t flce_embed_bwd(const flce_embed_args* x, void* stream) {
   a.pieces = (int)cdiv64(x->N, PIECE);
   a.part = (float*)(ws + l.part);
   a.count = (int*)(ws + l.count);
-  a.used = (const uint32_t*)(ws + l.used);
   const int wide = 16 / esz;
   const bool fits = x->H % wide == 0 && rows16(x->dout, x->lddout, esz) &&
                     rows_by(x->dE, x->lddE, dsz, (size_t)(wide * dsz > 32 ? 32 : wide * dsz));
@@ -755,8 +759,13 @@ extern "C" int32_t flce_embed_bwd(const flce_embed_args* x, void* stream) {
   so.status = x->status;
   so.count = a.count;
   so.ncount = a.pieces * a.slices;
-  so.used = ovw ? (uint32_t*)(ws + l.used) : nullptr;
-  so.nused = l.nused;
+  if (ovw) {
+    const bool dense = x->lddE == x->H;
+    so.zero = (uint8_t*)x->dE;
+    so.zrows = dense ? 1 : x->V;
+    so.zlen = (dense ? x->V : 1) * x->H * dsz;
+    so.zpitch = x->lddE * dsz;
+  }
   a.keys = so.k0;
   a.pos = so.p0;
   e = launch_sort(so, kb, s);
