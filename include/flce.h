@@ -425,15 +425,18 @@ typedef struct flce_ckpt8_dw_args {
   const float* scale;       /* [M, cdiv(K,128)]                                          */
   void* dW;                 /* [N,K]                                                     */
   int64_t lddW;
-  void* workspace;          /* 256-byte aligned, flce_ckpt8_dw_workspace_size            */
+  void* workspace;          /* 256-byte aligned                                          */
   size_t workspace_bytes;
   int32_t* status;          /* device int, reset to 0 by the call, or NULL: a word in the
                                workspace is used                                         */
 } flce_ckpt8_dw_args;
 
 FLCE_API int32_t flce_ckpt8_dw(const flce_ckpt8_dw_args* args, void* stream);
-/* Workspace bytes of flce_ckpt8_dw (0 on invalid sizes or dtype). */
-FLCE_API size_t flce_ckpt8_dw_workspace_size(int64_t M, int64_t N, int64_t K, int32_t dtype);
+/* Workspace bytes that flce_ckpt8_dw needs for these arguments (0 on invalid sizes or dtype);
+ * the fields from workspace on are not looked at. Partial sums of a part of the output tiles,
+ * tens of MB at most; fp32 dy adds 6 bytes an element, and rows of dy or q that do not start at
+ * multiples of 16 bytes a copy of that operand. Host-only. */
+FLCE_API size_t flce_ckpt8_dw_workspace_size(const flce_ckpt8_dw_args* args);
 
 /* Size of the fixed device scratch used by flce_fwd_bwd_noalloc (128 MiB). */
 #define FLCE_NOALLOC_SCRATCH_BYTES ((size_t)128 << 20)

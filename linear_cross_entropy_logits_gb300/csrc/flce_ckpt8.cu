@@ -124,9 +124,17 @@ extern "C" int32_t flce_ckpt8_pack(const flce_ckpt8_args* x, void* stream) {
   }
 }
 
-extern "C" size_t flce_ckpt8_dw_workspace_size(int64_t M, int64_t N, int64_t K, int32_t dtype) {
-  if (!sizes_ok(M, N, K) || !valid_dtype(dtype)) return 0;
-  return dw_tc_workspace(M, N, K, dtype);
+namespace {
+DwArgs dw_args(const flce_ckpt8_dw_args& x) {
+  return {x.M, x.N, x.K, cdiv64(x.K, Q_BLOCK), x.dy, x.lddy, (const uint8_t*)x.q, x.ldq,
+          x.scale, x.dW, x.lddW, (x.flags & FLCE_FLAG_DW_OVERWRITE) != 0};
+}
+}  // namespace
+
+extern "C" size_t flce_ckpt8_dw_workspace_size(const flce_ckpt8_dw_args* x) {
+  if (x == nullptr || !sizes_ok(x->M, x->N, x->K) || !valid_dtype(x->dtype)) return 0;
+  if (x->M == 0 || (x->flags & FLCE_FLAG_FORCE_SIMT)) return sizeof(Ctrl);
+  return dw_tc_workspace(dw_args(*x), x->dtype);
 }
 
 extern "C" int32_t flce_ckpt8_dw(const flce_ckpt8_dw_args* x, void* stream) {
@@ -141,7 +149,7 @@ extern "C" int32_t flce_ckpt8_dw(const flce_ckpt8_dw_args* x, void* stream) {
         x->ldq < x->K)
       return FLCE_ERR_INVALID_ARG;
     if (!x->workspace || !aligned_to(x->workspace, 256)) return FLCE_ERR_INVALID_ARG;
-    if (x->workspace_bytes < flce_ckpt8_dw_workspace_size(x->M, x->N, x->K, x->dtype)) return FLCE_ERR_WORKSPACE;
+    if (x->workspace_bytes < flce_ckpt8_dw_workspace_size(x)) return FLCE_ERR_WORKSPACE;
   }
   const bool ovw = (x->flags & FLCE_FLAG_DW_OVERWRITE) != 0;
   const bool simt = (x->flags & FLCE_FLAG_FORCE_SIMT) != 0;
@@ -154,8 +162,7 @@ extern "C" int32_t flce_ckpt8_dw(const flce_ckpt8_dw_args* x, void* stream) {
   if (e == cudaSuccess && x->M == 0 && ovw)
     e = cudaMemset2DAsync(x->dW, (size_t)x->lddW * wsz, 0, (size_t)x->K * wsz, (size_t)x->N, s);
   if (e != cudaSuccess || x->M == 0) return cuda_status(e);
-  const DwArgs a = {x->M, x->N, x->K, cdiv64(x->K, Q_BLOCK), x->dy, x->lddy, (const uint8_t*)x->q, x->ldq,
-                    x->scale, x->dW, x->lddW, ovw};
+  const DwArgs a = dw_args(*x);
   if (!simt) {
     const uint32_t ms = x->wait_timeout_ms ? x->wait_timeout_ms : DEFAULT_TIMEOUT_MS;
     return cuda_status(

@@ -19,7 +19,7 @@ struct DwArgs {
 };
 
 // Workspace bytes of the tensor-core path, and its launch. `dt`: dtype of dy; `wdt`: of dW.
-size_t dw_tc_workspace(int64_t M, int64_t N, int64_t K, int dt);
+size_t dw_tc_workspace(const DwArgs& a, int dt);
 bool dw_tc_supported();
 cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int* status, uint64_t timeout_ns,
                           cudaStream_t s);

@@ -12,12 +12,13 @@
 // q (TMA, 8 KB: one scale block), expands q into 16 KB of bf16 / fp16 in the swizzled MN-major
 // layout that the tensor cores read, and holds a 128 x 256 fp32 accumulator in its TMEM (two,
 // used in turn). The copies run up to six steps ahead, the expansion up to four.
-// 640 threads:
-//   warp 0   TMA producer               warps 4..11   expand q
-//   warp 1   MMA issuer (leader CTA)    warps 12..19  sums and output
+// 768 threads:
+//   warp 0   TMA producer               warps 4..15   expand q
+//   warp 1   MMA issuer (leader CTA)    warps 16..23  sums and output
 //   warp 2   the steps' scales (cp.async)
-// A step's MMAs take 512 cycles; expanding 8192 values takes about 230 instructions of each of
-// the eight warps (two per scheduler).
+// A step's MMAs take 512 cycles at the nominal rate and 640 at the library product's; expanding
+// its 8192 values takes about 230 instructions of each of 4 warps. Three groups of four warps
+// take the steps in turn (with two groups a step took 1000 cycles, with none 660).
 // The tensor cores truncate when they add to an accumulator; over M rows that adds up to an
 // error of about M * 1.1e-9 relative (9e-6 at 8192 rows). So the accumulator is read out after
 // every SEGMENT of rows and added, rounded to nearest, to fp32 sums in the registers of the
@@ -25,8 +26,8 @@
 //
 // Work split: whole tiles go round-robin over the pairs; the tiles of the last, partly filled
 // wave are split along m into S parts so that they fill the pairs. Parts are left as fp32 in
-// the workspace, and whichever warp finishes a tile's last part adds them up in part order
-// (the same order whoever is last, so the same bits) and writes dW.
+// the workspace and added in part order by a second kernel (the warp that finished a tile's
+// last part took 90 us to add 16 parts).
 //
 // fp32 dy is split into three bf16 terms beforehand (8 + 8 + 8 bits: exact), which run as
 // three passes over the same checkpoint rows.
@@ -52,17 +53,19 @@ constexpr int STAGE_BYTES = A_BYTES + Q_BYTES;
 constexpr int SLOTS = 4;                  // of expanded q
 constexpr int OFF_B = STAGES * STAGE_BYTES;
 constexpr int OFF_S = OFF_B + SLOTS * B_BYTES;
-constexpr int OFF_BARS = OFF_S + STAGES * S_BYTES;
+constexpr int OUT_BYTES = 32 * 16 * 4;     // 16 columns of an output warp's 32 rows
+constexpr int OFF_OUT = OFF_S + STAGES * S_BYTES;
+constexpr int OFF_BARS = OFF_OUT + 8 * OUT_BYTES;
 constexpr int BOX = 64 * 64 * 2;          // one 64 x 64 MN-major box
-constexpr int THREADS = 640;
-constexpr int CONV_WARPS = 8;
+constexpr int CONV_GROUPS = 3;
+constexpr int CONV_WARPS = 4 * CONV_GROUPS;
+constexpr int THREADS = 128 + 32 * CONV_WARPS + 256;
 constexpr int SMEM = OFF_BARS + 512 + 1024;
 static_assert(SMEM <= 232448, "shared memory per CTA");
 static_assert(STAGES > SLOTS, "the expanding warps watch a stage's barrier for their slot");
 constexpr int SEG16 = 32;                 // steps per accumulator for 16-bit dy (2048 rows)
 constexpr int SEG32 = 8;                  // for fp32 dy: its results are held to fp32 accuracy
 constexpr int MAX_SPLIT = 16;
-constexpr int PART_FLOATS = 32 * 128;     // sums of one output warp
 
 struct Params {
   DwArgs d;
@@ -71,8 +74,7 @@ struct Params {
   int whole;           // tiles done whole
   int S;               // parts of each other tile
   int seg;             // steps per accumulator
-  float* part;         // [split tiles][S][2 CTAs][8 warps][PART_FLOATS]
-  int* count;          // [split tiles][2][8] parts finished, zeroed before the launch
+  float* part;         // [split tiles][S][TILE][TILE]
   int* status;
   uint64_t timeout_ns;
   int vec;             // dW rows allow 16-byte accesses
@@ -124,35 +126,83 @@ __device__ __forceinline__ uint2 expand4(uint32_t u, uint64_t sc2) {
   return make_uint2(o[0], o[1]);
 }
 
-// 16 columns of a row of dW, from p on, of which `left` exist, (+)= v; the loads go out
-// together.
+// A warp's 32 rows x 128 columns of sums (lane = row) to a matrix: dst, its element (0, 0) of them,
+// of which `rows` x `cols` exist, (+)= acc. 16 columns at a time pass through shared memory
+// (16-byte chunk c of row r at c ^ (r / 2 % 4): free of bank conflicts both ways), so that a
+// store covers 64 bytes of each of 8 rows: stored a row per lane, 16 bytes of 32 rows at a time,
+// the rows' pitch puts most of a warp's accesses on few L2 slices (28 tiles of 256 x 256 at a
+// pitch of 16 KB took 77 us).
 template <typename D>
-__device__ __forceinline__ void put16(D* p, int64_t left, const float* v, int vec, int ovw) {
-  if (vec && left >= 16) {
-    constexpr int E = 16 / sizeof(D), NQ = 16 / E;  // elements per 16 bytes, and their number
-    Raw<D, E> u[NQ];
-    if (!ovw) {
+__device__ __forceinline__ void emit(D* dst, int64_t ld, int rows, int cols, bool vec, bool ovw, const float (&acc)[128],
+                                     uint32_t stage, int lane) {
+  const uint32_t wr = stage + (uint32_t)lane * 64;
+  const int sw = (lane >> 1) & 3;
+  const int c4 = (lane & 3) * 4;  // this lane's columns of a block, and its first row
+  const int r0 = lane >> 2;
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) u[i].load(p + i * E);
-    }
+  for (int j = 0; j < 8; ++j) {
+    if (16 * j >= cols) break;
+    float old[4][4];
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      float o[E];
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = v[i * E + e];
-      if (!ovw) {
-        float old[E];
-        u[i].unpack(old);
+      for (int e = 0; e < 4; ++e) old[i][e] = 0.0f;
+      const int r = r0 + 8 * i, c = 16 * j + c4;
+      if (!ovw && r < rows) {
+        const D* p = dst + r * ld + c;
+        if (vec && c + 4 <= cols) {
+          if constexpr (sizeof(D) == 4) {
+            const float4 v = *(const float4*)p;
+            old[i][0] = v.x, old[i][1] = v.y, old[i][2] = v.z, old[i][3] = v.w;
+          } else {
+            const uint2 v = *(const uint2*)p;
+            const D* h = (const D*)&v;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += old[e];
+            for (int e = 0; e < 4; ++e) old[i][e] = to_f<D>(h[e]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < cols) old[i][e] = to_f<D>(p[e]);
+        }
       }
-      Vec<D, E>::store(p + i * E, o);
     }
-    return;
-  }
+    __syncwarp();  // the block before has been read
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (i < left) p[i] = from_f<D>(ovw ? v[i] : to_f<D>(p[i]) + v[i]);
+    for (int c = 0; c < 4; ++c)
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(wr + (uint32_t)((c ^ sw) << 4)), "f"(acc[16 * j + 4 * c]),
+                   "f"(acc[16 * j + 4 * c + 1]), "f"(acc[16 * j + 4 * c + 2]), "f"(acc[16 * j + 4 * c + 3])
+                   : "memory");
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + 8 * i, c = 16 * j + c4;
+      float v[4];
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                   : "r"(stage + (uint32_t)(r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4))));
+      if (r < rows) {
+        D* p = dst + r * ld + c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += old[i][e];
+        if (vec && c + 4 <= cols) {
+          if constexpr (sizeof(D) == 4) {
+            *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+            uint2 u;
+            D* h = (D*)&u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = from_f<D>(v[e]);
+            *(uint2*)p = u;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < cols) p[e] = from_f<D>(v[e]);
+        }
+      }
+    }
+  }
 }
 
 template <typename T, typename D>
@@ -163,15 +213,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint64_t* bars = (uint64_t*)(smem + OFF_BARS);
   const uint32_t bar0 = smem_u32(bars);
-  auto full_a = [&](int s) { return bar0 + 8u * s; };                  // both CTAs' dy (leader)
-  auto full_q = [&](int s) { return bar0 + 8u * (STAGES + s); };       // this CTA's q
-  auto full_s = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };   // and its scales
-  auto empty_a = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };  // MMAs done with the stage (and its slot)
-  auto conv = [&](int s) { return bar0 + 8u * (4 * STAGES + s); };     // q expanded, both CTAs (leader)
-  auto tfull = [&](int s) { return bar0 + 8u * (4 * STAGES + SLOTS + s); };       // accumulator filled
-  auto tempty = [&](int s) { return bar0 + 8u * (4 * STAGES + SLOTS + 2 + s); };  // and read out (leader)
-  const uint32_t drain = bar0 + 8u * (4 * STAGES + SLOTS + 4);
-  constexpr int NBARS = 4 * STAGES + SLOTS + 5;
+  auto full = [&](int s) { return bar0 + 8u * s; };                    // this CTA's dy and q
+  auto full_s = [&](int s) { return bar0 + 8u * (STAGES + s); };       // and its scales
+  auto empty = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };    // MMAs done with the stage (and its slot)
+  auto conv = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };     // dy there and q expanded, both CTAs (leader)
+  auto tfull = [&](int s) { return bar0 + 8u * (3 * STAGES + SLOTS + s); };       // accumulator filled
+  auto tempty = [&](int s) { return bar0 + 8u * (3 * STAGES + SLOTS + 2 + s); };  // and read out (leader)
+  const uint32_t drain = bar0 + 8u * (3 * STAGES + SLOTS + 4);
+  constexpr int NBARS = 3 * STAGES + SLOTS + 5;
   static_assert(NBARS * 8 + 8 + STAGES * 4 <= 512, "barrier block");
   uint32_t* tmem_slot = (uint32_t*)(bars + NBARS);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
@@ -185,10 +234,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      bar_init(full_a(s), 1);
-      bar_init(full_q(s), 1);
+      bar_init(full(s), 1);
       bar_init(full_s(s), 32);
-      bar_init(empty_a(s), 1);
+      bar_init(empty(s), 1);
       copies[s] = 0;
     }
     for (int s = 0; s < SLOTS; ++s) bar_init(conv(s), 8);  // four warps of each CTA
@@ -202,6 +250,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     prefetch_map(&tm_dy);
     prefetch_map(&tm_q);
   }
+  let_next_start();
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(512u)
@@ -213,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Registers: 96 a thread at launch (5 warpgroups: 480 in all) = 32 + 2 * 56 + 2 * 168.
+  // Registers: 80 a thread at launch (6 warpgroups: 480 in all) = 32 + 3 * 48 + 2 * 152.
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp == 0 && lane == 0) {
@@ -224,18 +273,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       Item it;
       for (int i = pair; ok && get_item(p, i, it); i += npairs) {
         const int n0 = it.tile / p.tk * TILE + (int)rank * 128, k0 = it.tile % p.tk * TILE + (int)rank * 128;
+        int row = it.s0 % p.mstep;  // step within a term of dy
         for (int st = it.s0; st < it.s1; ++st) {
-          if (!bar_wait(empty_a(s), ph ^ 1u, ab, true)) {
+          if (!bar_wait(empty(s), ph ^ 1u, ab, true)) {
             ok = false;
             break;
           }
-          const uint32_t fa = leader ? full_a(s) : mapa(full_a(s), 0);
-          if (leader) bar_expect(full_a(s), 2 * A_BYTES);
-          bar_expect(full_q(s), Q_BYTES);
+          bar_expect(full(s), A_BYTES + Q_BYTES);
           const uint32_t a = smem_u32(smem + s * STAGE_BYTES);
-          tma_load(a + A_BYTES, &tm_q, full_q(s), k0, st % p.mstep * BK);
-          tma_load_pair(a, &tm_dy, fa, n0, st * BK);
-          tma_load_pair(a + BOX, &tm_dy, fa, n0 + 64, st * BK);
+          tma_load(a + A_BYTES, &tm_q, full(s), k0, row * BK);
+          tma_load(a, &tm_dy, full(s), n0, st * BK);
+          tma_load(a + BOX, &tm_dy, full(s), n0 + 64, st * BK);
+          if (++row == p.mstep) row = 0;
           copies[s] += 1;
           if (++s == STAGES) {
             s = 0;
@@ -251,8 +300,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                                  ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
       const uint64_t desc0 = desc_mn(smem_u32(smem), BOX);  // the address counts 16 bytes from bit 0
       int s = 0, b = 0, g = 0;
-      uint32_t ph = 0, bph = 0;
-      bool ok = true;
+      uint32_t bph = 0;
+      bool ok = true, ready = false;
       Item it;
       for (int i = pair; ok && get_item(p, i, it); i += npairs) {
         for (int st = it.s0; ok && st < it.s1; ++g) {
@@ -264,22 +313,23 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc_after();
           const int end = min(st + p.seg, it.s1);
           for (bool first = true; st < end; ++st, first = false) {
-            if (!bar_wait(full_a(s), ph, ab, true) || !bar_wait(conv(b), bph, ab, true)) {
+            if (!ready && !bar_wait(conv(b), bph, ab, true)) {
               ok = false;
               break;
             }
             tc_after();
+            // look at the next step's barrier while this step's MMAs are issued: the pipe holds
+            // few of them, and a wait between two steps leaves it idle
+            const int nb = b + 1 == SLOTS ? 0 : b + 1;
+            ready = bar_test(conv(nb), b + 1 == SLOTS ? bph ^ 1u : bph);
             const uint64_t da = desc0 + (uint32_t)(s * (STAGE_BYTES >> 4));
             const uint64_t db = desc0 + (uint32_t)((OFF_B + b * B_BYTES) >> 4);
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k)
               mma_pair(tmem + (uint32_t)(as * TILE), da + (uint64_t)(k * (2048 >> 4)), db + (uint64_t)(k * (2048 >> 4)),
                        idesc, !first || k != 0);
-            mma_commit_pair(empty_a(s));
-            if (++s == STAGES) {
-              s = 0;
-              ph ^= 1u;
-            }
+            mma_commit_pair(empty(s));
+            if (++s == STAGES) s = 0;
             if (++b == SLOTS) {
               b = 0;
               bph ^= 1u;
@@ -303,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float* sp = p.d.scale + (blk < p.d.nblk ? blk : 0);
         int row = it.s0 % p.mstep;  // step within a term of dy
         for (int st = it.s0; st < it.s1; ++st) {
-          ok = __all_sync(0xffffffffu, bar_wait(empty_a(s), ph ^ 1u, ab, true));
+          ok = __all_sync(0xffffffffu, bar_wait(empty(s), ph ^ 1u, ab, true));
           if (!ok) break;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -322,26 +372,26 @@ __global__ void __launch_bounds__(THREADS, 1)
       cp_async_wait_all();
     }
   } else if (warp < 4 + CONV_WARPS) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    // ---------------- expand q: two groups of four warps take the steps in turn, so a step's
-    // expansion may last two steps; thread (r, c) takes bytes 8c .. 8c + 7 of rows r + 8 j
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    // ---------------- expand q: groups of four warps take the steps in turn, so a step's
+    // expansion may last as many steps; thread (r, c) takes bytes 8c .. 8c + 7 of rows r + 8 j
     const int group = (warp - 4) >> 2;
     const int t = threadIdx.x & 127;
     const int c = t & 15, r = t >> 4;
     const uint32_t out = (uint32_t)(c >> 3) * BOX + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ r) << 4);
-    int s = 0, b = 0, turn = 0;
+    int s = 0, b = 0, turn = 0, whose = 0;
     uint32_t ph = 0;
     bool ok = true;
     Item it;
     for (int i = pair; ok && get_item(p, i, it); i += npairs) {
       for (int st = it.s0; st < it.s1; ++st, ++turn) {
-        if ((turn & 1) == group) {
-          ok = bar_wait(full_q(s), ph, ab, true) && bar_wait(full_s(s), ph, ab, true);
+        if (whose == group) {
+          ok = bar_wait(full(s), ph, ab, true) && bar_wait(full_s(s), ph, ab, true);
           if (ok && turn >= SLOTS) {
             // the slot's last user, SLOTS steps back, was in stage s - SLOTS (this round's or,
             // below 0, the round before's)
             const int u = s - SLOTS;
-            ok = bar_wait(empty_a(u < 0 ? u + STAGES : u), u < 0 ? ph ^ 1u : ph, ab, true);
+            ok = bar_wait(empty(u < 0 ? u + STAGES : u), u < 0 ? ph ^ 1u : ph, ab, true);
           }
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -372,14 +422,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           ph ^= 1u;
         }
         if (++b == SLOTS) b = 0;
+        if (++whose == CONV_GROUPS) whose = 0;
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     // ---------------- sums and output: warp w has rows 32 (w % 4) .. of this CTA's 128 and
     // columns 128 h .. of the tile's 256
     const int w = warp - 4 - CONV_WARPS, quad = warp & 3, h = w >> 2;
     const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(h * 128);
+    const uint32_t stage = smem_u32(smem + OFF_OUT + w * OUT_BYTES);
     int g = 0;
     bool ok = true;
     Item it;
@@ -404,38 +456,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) bar_arrive(mapa(tempty(as), 0));
       }
       if (!ok) break;
+      const int row = (int)rank * 128 + quad * 32, col = h * 128;  // within the tile
       if (it.part >= 0) {
-        const int64_t slot = (int64_t)(it.tile - p.whole) * p.S;
-        float4* mine = (float4*)(p.part + (((slot + it.part) * 2 + rank) * 8 + w) * PART_FLOATS) + lane;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          mine[j * 32] = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-        __threadfence();
-        __syncwarp();
-        int done = 0;
-        if (lane == 0) done = atomicAdd(p.count + ((it.tile - p.whole) * 2 + (int)rank) * 8 + w, 1);
-        done = __shfl_sync(0xffffffffu, done, 0);
-        if (done != p.S - 1) continue;  // another warp finishes this tile
-        __threadfence();
-        const float4* all = (const float4*)(p.part + ((slot * 2 + rank) * 8 + w) * PART_FLOATS) + lane;
-        for (int part = 0; part < p.S; ++part, all += 2 * 8 * PART_FLOATS / 4) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float4 v = __ldcg(all + j * 32);
-            acc[4 * j] = part == 0 ? v.x : acc[4 * j] + v.x;
-            acc[4 * j + 1] = part == 0 ? v.y : acc[4 * j + 1] + v.y;
-            acc[4 * j + 2] = part == 0 ? v.z : acc[4 * j + 2] + v.z;
-            acc[4 * j + 3] = part == 0 ? v.w : acc[4 * j + 3] + v.w;
-          }
-        }
-      }
-      const int64_t n = (int64_t)(it.tile / p.tk) * TILE + rank * 128 + quad * 32 + lane;
-      const int64_t k0 = (int64_t)(it.tile % p.tk) * TILE + h * 128;
-      if (n < p.d.N) {
-        D* row = (D*)p.d.dW + n * p.d.lddW;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (k0 + 16 * j < p.d.K) put16<D>(row + k0 + 16 * j, p.d.K - k0 - 16 * j, &acc[16 * j], p.vec, p.d.ovw);
+        const int64_t slot = (int64_t)(it.tile - p.whole) * p.S + it.part;
+        emit<float>(p.part + slot * TILE * TILE + row * TILE + col, TILE, 32, 128, true, true, acc, stage, lane);
+      } else {
+        const int64_t n = (int64_t)(it.tile / p.tk) * TILE + row, k = (int64_t)(it.tile % p.tk) * TILE + col;
+        emit<D>((D*)p.d.dW + n * p.d.lddW + k, p.d.lddW, (int)min(p.d.N - n, (int64_t)32), (int)min(p.d.K - k, (int64_t)128),
+                p.vec, p.d.ovw, acc, stage, lane);
       }
     }
   }
@@ -445,28 +473,52 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_before();
   cluster_sync();  // no role of either CTA issues anything after this point
   if (threadIdx.x == 0) {
-    // Every copy issued lands before shared memory is released. This CTA's q copies count on
-    // its own barriers; the dy copies of both on the leader's, where an aborted pipeline can
-    // have left the two producers one phase apart.
-    for (int s = 0; s < STAGES; ++s) {
-      const int mine = copies[s];
-      if (mine > 0) bar_wait(full_q(s), (uint32_t)(mine - 1) & 1u, ab, false);
-      if (!leader) continue;
-      const int peer = (int)ld_cluster(mapa(smem_u32(&copies[s]), 1));
-      int last = mine;
-      if (peer > mine) {
-        bar_expect(full_a(s), A_BYTES);
-        last = peer;
-      } else if (peer < mine) {
-        bar_complete(full_a(s), A_BYTES);
-      }
-      if (last > 0) bar_wait(full_a(s), (uint32_t)(last - 1) & 1u, ab, false);
-    }
+    // every copy issued lands before shared memory is released
+    for (int s = 0; s < STAGES; ++s)
+      if (copies[s] > 0) bar_wait(full(s), (uint32_t)(copies[s] - 1) & 1u, ab, false);
   }
   cluster_sync();
   if (warp == 1) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+// Adds up the parts of the split tiles in part order: a thread has four columns of a row, a block
+// (x, y) 8 rows from 8 y on of split tile x.
+template <typename D>
+__global__ void __launch_bounds__(512) k_dw_join(const __grid_constant__ Params p) {
+  after_previous();
+  const int tile = p.whole + (int)blockIdx.x;
+  const int r = (int)blockIdx.y * 8 + (threadIdx.x >> 6), c = (threadIdx.x & 63) * 4;
+  const int64_t n = (int64_t)(tile / p.tk) * TILE + r, k = (int64_t)(tile % p.tk) * TILE + c;
+  if (n >= p.d.N || k >= p.d.K) return;
+  const float* q = p.part + (int64_t)blockIdx.x * p.S * TILE * TILE + r * TILE + c;
+  float t[4] = {};
+#pragma unroll 4
+  for (int s = 0; s < p.S; ++s, q += TILE * TILE) {
+    const float4 v = *(const float4*)q;
+    t[0] += v.x;
+    t[1] += v.y;
+    t[2] += v.z;
+    t[3] += v.w;
+  }
+  D* o = (D*)p.d.dW + n * p.d.lddW + k;
+  if (p.vec && k + 4 <= p.d.K) {
+    if constexpr (sizeof(D) == 4) {
+      float4 v = p.d.ovw ? make_float4(0.f, 0.f, 0.f, 0.f) : *(float4*)o;
+      *(float4*)o = make_float4(v.x + t[0], v.y + t[1], v.z + t[2], v.w + t[3]);
+    } else {
+      uint2 u = p.d.ovw ? make_uint2(0u, 0u) : *(uint2*)o;
+      D* h = (D*)&u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = from_f<D>(p.d.ovw ? t[i] : to_f<D>(h[i]) + t[i]);
+      *(uint2*)o = u;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (k + i < p.d.K) o[i] = from_f<D>(p.d.ovw ? t[i] : to_f<D>(o[i]) + t[i]);
   }
 }
 
@@ -503,16 +555,19 @@ __global__ void __launch_bounds__(256) k_stage_q(const uint8_t* __restrict__ q, 
 // ------------------------------------------------------------------ plan
 struct Plan8 {
   int tn, tk, steps, mstep, whole, S;
-  size_t off_count, off_part, off_dy, off_q, total;
-  size_t count_bytes;
+  size_t off_part, off_dy, off_q, total;
 };
 
-int max_pairs() { return num_sms() / 2; }
-
 // Whole tiles fill whole waves of pairs; the rest are split S ways, S minimising the steps of
-// the remaining waves plus the cost of the parts: writing and re-reading a part's 256 KB costs
-// about a step's time per PART_COST parts over all pairs.
-Plan8 plan(int64_t M, int64_t N, int64_t K, int dt, int pairs) {
+// the remaining waves plus the cost of the parts in steps' time (0.34 us): the second kernel 9,
+// writing and reading a part's 256 KB 0.3.
+// Rows that TMA cannot read in place.
+bool stage_dy(const DwArgs& a, int dt) { return dt == FLCE_F32 || !rows16(a.dy, a.lddy, 2); }
+bool stage_q(const DwArgs& a) { return !rows16(a.q, a.ldq, 1); }
+
+Plan8 plan(const DwArgs& a, int dt) {
+  const int64_t M = a.M, N = a.N, K = a.K;
+  const int pairs = num_sms() / 2;
   Plan8 p = {};
   p.tn = (int)cdiv64(N, TILE);
   p.tk = (int)cdiv64(K, TILE);
@@ -527,7 +582,7 @@ Plan8 plan(int64_t M, int64_t N, int64_t K, int dt, int pairs) {
     double best = 0.0;
     for (int S = 1; S <= MAX_SPLIT && S <= p.steps; ++S) {
       const double waves = (double)cdiv64(rest * S, pairs) * (double)cdiv64(p.steps, S);
-      const double cost = waves + (S > 1 ? 6.0 + 0.15 * (double)(rest * S) : 0.0);
+      const double cost = waves + (S > 1 ? 9.0 + 0.3 * (double)(rest * S) : 0.0);
       if (S == 1 || cost < best) {
         best = cost;
         p.S = S;
@@ -542,11 +597,9 @@ Plan8 plan(int64_t M, int64_t N, int64_t K, int dt, int pairs) {
   };
   const size_t split = p.S > 1 ? (size_t)rest : 0;
   take(256);  // the status word (Ctrl::status)
-  p.count_bytes = split * 16 * 4;
-  p.off_count = take(p.count_bytes);
-  p.off_part = take(split * p.S * 16 * PART_FLOATS * 4);
-  p.off_dy = take((size_t)terms * p.mstep * BK * round_up((size_t)N, 8) * 2);
-  p.off_q = take((size_t)M * round_up((size_t)K, 16));
+  p.off_part = take(split * p.S * TILE * TILE * 4);
+  p.off_dy = take(stage_dy(a, dt) ? (size_t)terms * p.mstep * BK * round_up((size_t)N, 8) * 2 : 0);
+  p.off_q = take(stage_q(a) ? (size_t)M * round_up((size_t)K, 16) : 0);
   p.total = off;
   return p;
 }
@@ -575,25 +628,28 @@ cudaError_t launch(const CUtensorMap& A, const CUtensorMap& Q, const Params& p, 
   if (n == 0) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(2 * (unsigned)max_pairs(), 1, 1);
+    cfg.gridDim = dim3(2 * (unsigned)(num_sms() / 2), 1, 1);
     e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
     if (e != cudaSuccess) return e;
     if (n <= 0) return cudaErrorInvalidConfiguration;
     fit[dev].store(n, std::memory_order_relaxed);
   }
   cfg.gridDim = dim3(2 * (unsigned)(items < n ? items : n), 1, 1);
-  return cudaLaunchKernelEx(&cfg, kern, A, Q, p);
+  e = cudaLaunchKernelEx(&cfg, kern, A, Q, p);
+  if (e != cudaSuccess || p.S == 1) return e;
+  const int64_t split = (int64_t)p.tn * p.tk - p.whole;
+  return launch_after(k_dw_join<D>, dim3((unsigned)split, TILE / 8, 1), 512, 0, s, p);
 }
 
 }  // namespace
 
 bool dw_tc_supported() { return ptx::encode_fn() != nullptr; }
 
-size_t dw_tc_workspace(int64_t M, int64_t N, int64_t K, int dt) { return plan(M, N, K, dt, max_pairs()).total; }
+size_t dw_tc_workspace(const DwArgs& a, int dt) { return plan(a, dt).total; }
 
 cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int* status, uint64_t timeout_ns,
                           cudaStream_t s) {
-  const Plan8 pl = plan(a.M, a.N, a.K, dt, max_pairs());
+  const Plan8 pl = plan(a, dt);
   char* ws = (char*)workspace;
   Params p = {};
   p.d = a;
@@ -605,18 +661,15 @@ cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int
   p.S = pl.S;
   p.seg = dt == FLCE_F32 ? SEG32 : SEG16;
   p.part = (float*)(ws + pl.off_part);
-  p.count = (int*)(ws + pl.off_count);
   p.status = status;
   p.timeout_ns = timeout_ns;
   const int wsz = dtype_size(wdt);
   p.vec = rows16(a.dW, a.lddW, wsz);
   cudaError_t e = cudaSuccess;
-  if (pl.count_bytes) e = cudaMemsetAsync(p.count, 0, pl.count_bytes, s);
-  if (e != cudaSuccess) return e;
 
   const void* dy = a.dy;
   int64_t lddy = a.lddy, rows = a.M;
-  if (dt == FLCE_F32 || !rows16(a.dy, a.lddy, 2)) {
+  if (stage_dy(a, dt)) {
     dy = ws + pl.off_dy;
     lddy = (int64_t)round_up((size_t)a.N, 8);
     const int64_t plane = (int64_t)pl.mstep * BK;
@@ -631,7 +684,7 @@ cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int
   }
   const uint8_t* q = a.q;
   int64_t ldq = a.ldq;
-  if (!rows16(a.q, a.ldq, 1)) {
+  if (stage_q(a)) {
     q = (const uint8_t*)(ws + pl.off_q);
     ldq = (int64_t)round_up((size_t)a.K, 16);
     k_stage_q<<<dim3((unsigned)a.M, (unsigned)cdiv64(a.K, 256)), 256, 0, s>>>(a.q, a.ldq, a.K, (uint8_t*)q, ldq);

@@ -183,7 +183,7 @@ def load(path: str | None = None):
     lib.flce_rmsnorm_workspace_size.restype = ctypes.c_size_t
     lib.flce_rmsnorm_workspace_size.argtypes = [ctypes.c_int64] * 2
     lib.flce_ckpt8_dw_workspace_size.restype = ctypes.c_size_t
-    lib.flce_ckpt8_dw_workspace_size.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int32]
+    lib.flce_ckpt8_dw_workspace_size.argtypes = [ctypes.POINTER(FlceCkpt8DwArgs)]
     lib.flce_profile_create.restype = ctypes.c_void_p
     lib.flce_profile_create.argtypes = []
     lib.flce_profile_reset.restype = None
@@ -711,13 +711,14 @@ def ckpt8_dw(dy, q, scale, *, dW=None, workspace=None, flags=0, wait_timeout_ms=
     if dW is None:
         dW = torch.empty((N, K), dtype=torch.float32, device=dev)
         flags |= FLAG_DW_OVERWRITE
-    workspace = _workspace(workspace, lib.flce_ckpt8_dw_workspace_size(M, N, K, dt), dev, stream)
-    o = {"dW": dW, "workspace": workspace}
+    o = {"dW": dW}
     pdy, lddy = _matrix("dy", dy, M, N, dy.dtype, dev)
     pq, ldq = _matrix("q", q, M, K, torch.float8_e4m3fn, dev)
     pW, ldW = _matrix("dW", dW, N, K, dW.dtype, dev)
     a = FlceCkpt8DwArgs(M, N, K, dt, _grad_dtype("dW", dW), flags, wait_timeout_ms, pdy, lddy, pq, ldq,
                         _dense("scale", scale, (M, (K + Q_BLOCK - 1) // Q_BLOCK), torch.float32, dev), pW, ldW,
-                        workspace.data_ptr(), workspace.numel(), _status(o, status, check, dev))
+                        None, 0, _status(o, status, check, dev))
+    workspace = o["workspace"] = _workspace(workspace, lib.flce_ckpt8_dw_workspace_size(a), dev, stream)
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
     h = _launch(lib.flce_ckpt8_dw, "flce_ckpt8_dw", a, dev, stream, (dy, q, scale, dW, workspace, o.get("status")))
     return _finish(o, lib, check, h)

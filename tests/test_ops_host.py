@@ -139,8 +139,14 @@ def test_workspace_sizes(lib):
     assert lib.flce_embed_workspace_size(-1, 4, 4) == 0 and lib.flce_embed_workspace_size(4, 0, 4) == 0
     assert lib.flce_embed_workspace_size(0, 4, 4) > 0
     assert lib.flce_rmsnorm_workspace_size(4, 0) == 0 and lib.flce_rmsnorm_workspace_size(0, 8) > 0
-    assert lib.flce_ckpt8_dw_workspace_size(4, 4, 0, 1) == 0 and lib.flce_ckpt8_dw_workspace_size(4, 4, 4, 7) == 0
-    assert lib.flce_ckpt8_dw_workspace_size(0, 4, 4, 1) > 0
+    size = lib.flce_ckpt8_dw_workspace_size
+    assert size(_dw(K=0)) == 0 and size(_dw(dtype=7)) == 0 and size(None) == 0 and size(_dw(M=0)) > 0
+    big = dict(M=4096, N=1024, K=2048, lddy=1024, ldq=2048, lddW=2048)
+    plain = size(_dw(**big))
+    assert size(_dw(**big, flags=1)) < plain                              # no tensor cores, no parts
+    assert size(_dw(**dict(big, lddy=1025))) - plain >= 4096 * 1024 * 2   # dy copied to a TMA pitch
+    assert size(_dw(**dict(big, ldq=2049))) - plain >= 4096 * 2048        # q copied
+    assert size(_dw(**big, dtype=0)) - plain >= 3 * 4096 * 1024 * 2       # fp32 dy: three bf16 terms
 
 
 def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
