@@ -127,7 +127,8 @@ __device__ __forceinline__ uint2 expand4(uint32_t u, uint64_t sc2) {
 }
 
 // A warp's 32 rows x 128 columns of sums (lane = row) to a matrix: dst, its element (0, 0) of them,
-// of which `rows` x `cols` exist, (+)= acc. 16 columns at a time pass through shared memory
+// of which `rows` x `cols` exist, (+)= acc. fp32 is added by L2 (one add an element: nothing to wait
+// for, and the same bits on every run); 16-bit values are read, so that they are rounded once. 16 columns at a time pass through shared memory
 // (16-byte chunk c of row r at c ^ (r / 2 % 4): free of bank conflicts both ways), so that a
 // store covers 64 bytes of each of 8 rows: stored a row per lane, 16 bytes of 32 rows at a time,
 // the rows' pitch puts most of a warp's accesses on few L2 slices (28 tiles of 256 x 256 at a
@@ -148,18 +149,13 @@ __device__ __forceinline__ void emit(D* dst, int64_t ld, int rows, int cols, boo
 #pragma unroll
       for (int e = 0; e < 4; ++e) old[i][e] = 0.0f;
       const int r = r0 + 8 * i, c = 16 * j + c4;
-      if (!ovw && r < rows) {
+      if (sizeof(D) == 2 && !ovw && r < rows) {
         const D* p = dst + r * ld + c;
         if (vec && c + 4 <= cols) {
-          if constexpr (sizeof(D) == 4) {
-            const float4 v = *(const float4*)p;
-            old[i][0] = v.x, old[i][1] = v.y, old[i][2] = v.z, old[i][3] = v.w;
-          } else {
-            const uint2 v = *(const uint2*)p;
-            const D* h = (const D*)&v;
+          const uint2 v = *(const uint2*)p;
+          const D* h = (const D*)&v;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) old[i][e] = to_f<D>(h[e]);
-          }
+          for (int e = 0; e < 4; ++e) old[i][e] = to_f<D>(h[e]);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -183,22 +179,36 @@ __device__ __forceinline__ void emit(D* dst, int64_t ld, int rows, int cols, boo
                    : "r"(stage + (uint32_t)(r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4))));
       if (r < rows) {
         D* p = dst + r * ld + c;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += old[i][e];
-        if (vec && c + 4 <= cols) {
-          if constexpr (sizeof(D) == 4) {
-            *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+        if constexpr (sizeof(D) == 4) {
+          if (vec && c + 4 <= cols) {
+            if (ovw)
+              *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+            else
+              asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v[0]), "f"(v[1]),
+                           "f"(v[2]), "f"(v[3])
+                           : "memory");
           } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (c + e < cols) {
+                if (ovw) p[e] = v[e];
+                else atomicAdd(p + e, v[e]);
+              }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += old[i][e];
+          if (vec && c + 4 <= cols) {
             uint2 u;
             D* h = (D*)&u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) h[e] = from_f<D>(v[e]);
             *(uint2*)p = u;
-          }
-        } else {
+          } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c + e < cols) p[e] = from_f<D>(v[e]);
+            for (int e = 0; e < 4; ++e)
+              if (c + e < cols) p[e] = from_f<D>(v[e]);
+          }
         }
       }
     }
