@@ -64,7 +64,7 @@ constexpr int SMEM = OFF_BARS + 512 + 1024;
 static_assert(SMEM <= 232448, "shared memory per CTA");
 static_assert(STAGES > SLOTS, "the expanding warps watch a stage's barrier for their slot");
 constexpr int SEG16 = 32;                 // steps per accumulator for 16-bit dy (2048 rows)
-constexpr int SEG32 = 8;                  // for fp32 dy: its results are held to fp32 accuracy
+constexpr int SEG32 = 16;                 // for fp32 dy (1024 rows of a term): half that error
 constexpr int MAX_SPLIT = 16;
 
 struct Params {
@@ -535,25 +535,46 @@ __global__ void __launch_bounds__(512) k_dw_join(const __grid_constant__ Params 
 // ------------------------------------------------------------------ staging
 // dy rows that TMA cannot read in place (fp32, or a pitch that is no multiple of 16 bytes):
 // copied to a 16-byte pitch; fp32 as three bf16 terms in planes of `rows` rows, each the
-// leading 8 bits of what the ones before leave. Rows past M are zero.
+// leading 8 bits of what the ones before leave. Rows past M are zero. Four columns a thread.
 template <typename T>
 __global__ void __launch_bounds__(256) k_stage_dy(const T* __restrict__ dy, int64_t lddy, int64_t M, int64_t N,
-                                                  int64_t rows, void* out, int64_t ld) {
-  const int64_t m = blockIdx.x, n = (int64_t)blockIdx.y * 256 + threadIdx.x;
+                                                  int64_t rows, void* out, int64_t ld, int vec) {
+  const int64_t m = blockIdx.x, n = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
   if (n >= N) return;
   if constexpr (sizeof(T) == 4) {
-    float x = m < M ? dy[m * lddy + n] : 0.0f;
-    uint16_t* o = (uint16_t*)out + m * ld + n;
+    float x[4] = {};
+    if (m < M) {
+      const float* p = dy + m * lddy + n;
+      if (vec && n + 4 <= N) {
+        const float4 v = *(const float4*)p;
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < N) x[e] = p[e];
+      }
+    }
+    // the pitch is a multiple of 8 columns: four are always there
+    uint2* o = (uint2*)((uint16_t*)out + m * ld + n);
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-      const uint32_t hi = __float_as_uint(x) & 0xffff0000u;
-      const bool fin = fabsf(x) < INFINITY;
-      // a NaN whose set bits lie in the low half must not become an infinity
-      o[i * rows * ld] = (uint16_t)((fin || x == x ? hi : 0x7fc00000u) >> 16);
-      x = fin ? x - __uint_as_float(hi) : 0.0f;
+      uint32_t t[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t hi = __float_as_uint(x[e]) & 0xffff0000u;
+        const bool fin = fabsf(x[e]) < INFINITY;
+        // a NaN whose set bits lie in the low half must not become an infinity
+        t[e] = fin || x[e] == x[e] ? hi : 0x7fc00000u;
+        x[e] = fin ? x[e] - __uint_as_float(hi) : 0.0f;
+      }
+      *(uint2*)((uint16_t*)o + i * rows * ld) = make_uint2(t[0] >> 16 | t[1], t[2] >> 16 | t[3]);
     }
   } else {
-    if (m < M) ((T*)out)[m * ld + n] = dy[m * lddy + n];
+    if (m < M) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < N) ((T*)out)[m * ld + n + e] = dy[m * lddy + n + e];
+    }
   }
 }
 __global__ void __launch_bounds__(256) k_stage_q(const uint8_t* __restrict__ q, int64_t ldq, int64_t K, uint8_t* out,
@@ -683,12 +704,13 @@ cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int
     dy = ws + pl.off_dy;
     lddy = (int64_t)round_up((size_t)a.N, 8);
     const int64_t plane = (int64_t)pl.mstep * BK;
-    const dim3 grid((unsigned)(dt == FLCE_F32 ? plane : a.M), (unsigned)cdiv64(a.N, 256));
+    const dim3 grid((unsigned)(dt == FLCE_F32 ? plane : a.M), (unsigned)cdiv64(a.N, 1024));
     if (dt == FLCE_F32) {
-      k_stage_dy<float><<<grid, 256, 0, s>>>((const float*)a.dy, a.lddy, a.M, a.N, plane, (void*)dy, lddy);
+      k_stage_dy<float><<<grid, 256, 0, s>>>((const float*)a.dy, a.lddy, a.M, a.N, plane, (void*)dy, lddy,
+                                             rows16(a.dy, a.lddy, 4));
       rows = 3 * plane;
     } else {
-      k_stage_dy<__half><<<grid, 256, 0, s>>>((const __half*)a.dy, a.lddy, a.M, a.N, plane, (void*)dy, lddy);
+      k_stage_dy<__half><<<grid, 256, 0, s>>>((const __half*)a.dy, a.lddy, a.M, a.N, plane, (void*)dy, lddy, 0);
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }

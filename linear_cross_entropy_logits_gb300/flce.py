@@ -497,18 +497,19 @@ def _workspace(ws, nbytes, dev, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
-def _launch(fn, where, args, dev, stream, used):
+def _launch(fn, where, args, dev, stream, *used):
     """Enqueue on `stream` (None: the current one); returns the stream's handle. Tensors used on
-    a stream other than the current one are recorded on it, so that the allocator does not hand
-    their memory out before the kernels are done."""
+    a given stream (`used`, and the values of dicts in it) are recorded on it, so that the
+    allocator does not hand their memory out before the kernels are done."""
     index = dev.index
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
     else:
         handle = stream.cuda_stream
-        for t in used:
-            if t is not None:
-                t.record_stream(stream)
+        for u in used:
+            for t in u.values() if isinstance(u, dict) else (u,):
+                if t is not None:
+                    t.record_stream(stream)
     if index == torch._C._cuda_getDevice():
         rc = fn(args, handle)
     else:
@@ -553,7 +554,7 @@ def embed_fwd(tokens, E, *, scale=1.0, ignore_index=-100, out=None, status=None,
     po, ldo = _matrix("out", out, N, H, E.dtype, dev)
     a = FlceEmbedArgs(N, H, V, dt, 0, _dense("tokens", tokens, (N,), torch.int64, dev), ignore_index, scale, 0,
                       pE, ldE, po, ldo, None, 0, None, 0, None, 0, _status(o, status, check, dev))
-    h = _launch(lib.flce_embed_fwd, "flce_embed_fwd", a, dev, stream, (tokens, E, out, o.get("status")))
+    h = _launch(lib.flce_embed_fwd, "flce_embed_fwd", a, dev, stream, tokens, E, o)
     return _finish(o, lib, check, h)
 
 
@@ -580,7 +581,7 @@ def embed_bwd(tokens, dout, *, V=None, dE=None, scale=1.0, ignore_index=-100, wo
     a = FlceEmbedArgs(N, H, V, dt, _grad_dtype("dE", dE), _dense("tokens", tokens, (N,), torch.int64, dev),
                       ignore_index, scale, flags, None, 0, None, 0, pd, ldd, pE, ldE, workspace.data_ptr(),
                       workspace.numel(), _status(o, status, check, dev))
-    h = _launch(lib.flce_embed_bwd, "flce_embed_bwd", a, dev, stream, (tokens, dout, dE, workspace, o.get("status")))
+    h = _launch(lib.flce_embed_bwd, "flce_embed_bwd", a, dev, stream, tokens, dout, o)
     return _finish(o, lib, check, h)
 
 
@@ -606,23 +607,23 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, weight_offset=0.0, want_y
         prstd = rstd.data_ptr()
     else:
         prstd = _dense("rstd", rstd, (N,), torch.float32, dev)
-    (py, ldy) = _row_output(o, "y", N, H, dtype, dev) if want_y else (None, 0)
+    (py, ldy) = _row_output(o, "y", x, N, H, dtype, dev) if want_y else (None, 0)
     if want_h is None:
         want_h = residual is not None
-    (ph, ldh) = _row_output(o, "h", N, H, dtype, dev) if want_h else (None, 0)
+    (ph, ldh) = _row_output(o, "h", x, N, H, dtype, dev) if want_h else (None, 0)
     (py8, ldy8, psy) = _rows8(o, "y8", "y8_scale", N, H, dev) if want_y8 else (None, 0, None)
     (ph8, ldh8, psh) = _rows8(o, "h8", "h8_scale", N, H, dev) if want_h8 else (None, 0, None)
     a = FlceRmsnormArgs(N, H, dt, eps, weight_offset, 0, px, ldx, pr, ldr, _dense("weight", weight, (H,), dtype, dev),
                         ph, ldh, py, ldy, prstd, py8, ldy8, psy, ph8, ldh8, psh)
-    _launch(lib.flce_rmsnorm_fwd, "flce_rmsnorm_fwd", a, dev, stream, (x, residual, weight, *o.values()))
+    _launch(lib.flce_rmsnorm_fwd, "flce_rmsnorm_fwd", a, dev, stream, x, residual, weight, o)
     return o
 
 
-def _row_output(o, key, N, H, dtype, dev):
-    """Pointer and pitch of the output matrix o[key], made if absent."""
+def _row_output(o, key, like, N, H, dtype, dev):
+    """Pointer and pitch of the output matrix o[key], made as `like` if absent."""
     t = o.get(key)
     if t is None:
-        t = o[key] = torch.empty((N, H), dtype=dtype, device=dev)
+        t = o[key] = torch.empty_like(like, memory_format=torch.contiguous_format)
         return t.data_ptr(), H
     return _matrix(key, t, N, H, dtype, dev)
 
@@ -654,7 +655,7 @@ def rmsnorm_bwd(dy, weight, rstd, h=None, *, h8=None, h8_scale=None, dh=None, we
     if (h is None) == (h8 is None) or (h8 is not None and h8_scale is None):
         raise ValueError("rmsnorm_bwd takes h, or h8 with h8_scale")
     o = dict(outputs) if outputs else {}
-    (pdx, lddx) = _row_output(o, "dx", N, H, dtype, dev) if want_dx else (None, 0)
+    (pdx, lddx) = _row_output(o, "dx", dy, N, H, dtype, dev) if want_dx else (None, 0)
     pw = pws = None
     wbytes, wdt = 0, 0
     if want_dweight:
@@ -677,8 +678,7 @@ def rmsnorm_bwd(dy, weight, rstd, h=None, *, h8=None, h8_scale=None, dh=None, we
     a = FlceRmsnormBwdArgs(N, H, dt, wdt, weight_offset, flags, pdy, lddy, ph, ldh, p8, ld8, ps8,
                            _dense("rstd", rstd, (N,), torch.float32, dev),
                            _dense("weight", weight, (H,), dtype, dev), pdh, lddh, pdx, lddx, pw, pws, wbytes)
-    _launch(lib.flce_rmsnorm_bwd, "flce_rmsnorm_bwd", a, dev, stream,
-            (dy, weight, rstd, h, h8, h8_scale, dh, *o.values()))
+    _launch(lib.flce_rmsnorm_bwd, "flce_rmsnorm_bwd", a, dev, stream, dy, weight, rstd, h, h8, h8_scale, dh, o)
     return o
 
 
@@ -691,7 +691,7 @@ def ckpt8_pack(x, *, outputs=None, stream=None):
     px, ldx = _matrix("x", x, N, H, x.dtype, dev)
     pq, ldq, ps = _rows8(o, "q", "scale", N, H, dev)
     _launch(lib.flce_ckpt8_pack, "flce_ckpt8_pack", FlceCkpt8Args(N, H, dt, 0, px, ldx, pq, ldq, ps), dev, stream,
-            (x, *o.values()))
+            x, o)
     return o
 
 
@@ -720,5 +720,5 @@ def ckpt8_dw(dy, q, scale, *, dW=None, workspace=None, flags=0, wait_timeout_ms=
                         None, 0, _status(o, status, check, dev))
     workspace = o["workspace"] = _workspace(workspace, lib.flce_ckpt8_dw_workspace_size(a), dev, stream)
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    h = _launch(lib.flce_ckpt8_dw, "flce_ckpt8_dw", a, dev, stream, (dy, q, scale, dW, workspace, o.get("status")))
+    h = _launch(lib.flce_ckpt8_dw, "flce_ckpt8_dw", a, dev, stream, dy, q, scale, o)
     return _finish(o, lib, check, h)
