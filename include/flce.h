@@ -94,9 +94,10 @@ typedef enum flce_dtype { FLCE_F32 = 0, FLCE_BF16 = 1, FLCE_F16 = 2 } flce_dtype
 #define FLCE_FLAG_SEPARATE_BWD 0x8u /* run the dX and dW GEMMs as two launches instead of
                                      one launch sharing a work queue (the results are the
                                      same bits either way)                                 */
-#define FLCE_FLAG_DEBUG_STALL 0x100u /* testing only: the tensor-core forward GEMM leaves
-                                     one pipeline stage unfilled so that its bounded waits
-                                     run out; the call must then report FLCE_ERR_TIMEOUT */
+#define FLCE_FLAG_DEBUG_STALL 0x100u /* testing only: the tensor-core forward GEMM (and that of
+                                     flce_ckpt8_dw) leaves one pipeline stage unfilled so
+                                     that its bounded waits run out; the call must then
+                                     report FLCE_ERR_TIMEOUT                             */
 #define FLCE_FLAG_DEBUG_STALL_BWD 0x200u /* testing only: the same in the merged dX + dW
                                      launch (its first work item)                          */
 
@@ -416,7 +417,7 @@ typedef struct flce_ckpt8_dw_args {
   int64_t K;                /* input features: columns of q and dW                       */
   int32_t dtype;            /* flce_dtype of dy                                          */
   int32_t dW_dtype;         /* FLCE_F32, or dtype itself; others FLCE_ERR_UNSUPPORTED    */
-  uint32_t flags;           /* FLCE_FLAG_DW_OVERWRITE, FLCE_FLAG_FORCE_SIMT              */
+  uint32_t flags;           /* FLCE_FLAG_DW_OVERWRITE, _FORCE_SIMT, _DEBUG_STALL         */
   uint32_t wait_timeout_ms; /* limit of every pipeline wait; 0 means 4000 ms             */
   const void* dy;           /* [M,N]                                                     */
   int64_t lddy;

@@ -139,7 +139,7 @@ extern "C" size_t flce_ckpt8_dw_workspace_size(const flce_ckpt8_dw_args* x) {
 
 extern "C" int32_t flce_ckpt8_dw(const flce_ckpt8_dw_args* x, void* stream) {
   if (x == nullptr || !sizes_ok(x->M, x->N, x->K) || !valid_dtype(x->dtype)) return FLCE_ERR_INVALID_ARG;
-  if ((x->flags & ~(FLCE_FLAG_DW_OVERWRITE | FLCE_FLAG_FORCE_SIMT)) != 0) return FLCE_ERR_INVALID_ARG;
+  if ((x->flags & ~(FLCE_FLAG_DW_OVERWRITE | FLCE_FLAG_FORCE_SIMT | FLCE_FLAG_DEBUG_STALL)) != 0) return FLCE_ERR_INVALID_ARG;
   if (x->dW_dtype != FLCE_F32 && x->dW_dtype != x->dtype) return FLCE_ERR_UNSUPPORTED;
   const int esz = dtype_size(x->dtype), wsz = dtype_size(x->dW_dtype);
   if (!x->dW || !aligned_to(x->dW, wsz) || x->lddW < x->K) return FLCE_ERR_INVALID_ARG;
@@ -166,7 +166,8 @@ extern "C" int32_t flce_ckpt8_dw(const flce_ckpt8_dw_args* x, void* stream) {
   if (!simt) {
     const uint32_t ms = x->wait_timeout_ms ? x->wait_timeout_ms : DEFAULT_TIMEOUT_MS;
     return cuda_status(
-        launch_dw_tc8(a, x->dtype, x->dW_dtype, x->workspace, status, (uint64_t)ms * 1000000ull, s));
+        launch_dw_tc8(a, x->dtype, x->dW_dtype, x->workspace, status, (uint64_t)ms * 1000000ull,
+                                     (x->flags & FLCE_FLAG_DEBUG_STALL) != 0, s));
   }
   const bool f32 = x->dW_dtype == FLCE_F32;
   switch (x->dtype) {

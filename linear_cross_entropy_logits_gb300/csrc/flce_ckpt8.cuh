@@ -22,6 +22,6 @@ struct DwArgs {
 size_t dw_tc_workspace(const DwArgs& a, int dt);
 bool dw_tc_supported();
 cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int* status, uint64_t timeout_ns,
-                          cudaStream_t s);
+                          bool stall, cudaStream_t s);
 
 }  // namespace flce

@@ -78,6 +78,7 @@ struct Params {
   int* status;
   uint64_t timeout_ns;
   int vec;             // dW rows allow 16-byte accesses
+  int stall;           // testing: the first step of the launch is never filled
 };
 
 // Work item i: whole tile i, or part (i - whole) % S of tile whole + (i - whole) / S.
@@ -291,9 +292,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           bar_expect(full(s), A_BYTES + Q_BYTES);
           const uint32_t a = smem_u32(smem + s * STAGE_BYTES);
-          tma_load(a + A_BYTES, &tm_q, full(s), k0, row * BK);
-          tma_load(a, &tm_dy, full(s), n0, st * BK);
-          tma_load(a + BOX, &tm_dy, full(s), n0 + 64, st * BK);
+          if (!(p.stall && leader && i == 0 && st == it.s0)) {
+            tma_load(a + A_BYTES, &tm_q, full(s), k0, row * BK);
+            tma_load(a, &tm_dy, full(s), n0, st * BK);
+            tma_load(a + BOX, &tm_dy, full(s), n0 + 64, st * BK);
+          }
           if (++row == p.mstep) row = 0;
           copies[s] += 1;
           if (++s == STAGES) {
@@ -679,7 +682,7 @@ bool dw_tc_supported() { return ptx::encode_fn() != nullptr; }
 size_t dw_tc_workspace(const DwArgs& a, int dt) { return plan(a, dt).total; }
 
 cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int* status, uint64_t timeout_ns,
-                          cudaStream_t s) {
+                          bool stall, cudaStream_t s) {
   const Plan8 pl = plan(a, dt);
   char* ws = (char*)workspace;
   Params p = {};
@@ -694,6 +697,7 @@ cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int
   p.part = (float*)(ws + pl.off_part);
   p.status = status;
   p.timeout_ns = timeout_ns;
+  p.stall = stall;
   const int wsz = dtype_size(wdt);
   p.vec = rows16(a.dW, a.lddW, wsz);
   cudaError_t e = cudaSuccess;

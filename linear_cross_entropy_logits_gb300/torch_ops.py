@@ -15,6 +15,11 @@ applies the upstream gradient:
 The custom op has a fake (meta) implementation, so torch.compile traces it as one opaque op
 (no graph break) and compiled results equal eager ones. Marshalling only: every step of the
 computation runs in libflce.so.
+
+Around the head, each with its gradient: embedding (lookup with scaling), add_rms_norm (the
+residual's addition and the RMS norm, optionally keeping an 8-bit checkpoint of its input for
+the backward) and linear_ckpt8 (a projection that keeps its input in 8 bits for the weight
+gradient; the two products with W itself are plain library GEMMs).
 """
 
 from __future__ import annotations
@@ -164,3 +169,188 @@ def fused_linear_cross_entropy(X, W, targets, bias=None, *, ignore_index=-100, r
     if return_extras:
         return (loss,) + tuple(outs[1:])
     return loss
+
+
+# ---------------------------------------------------------------------------------------
+# Around the head: embedding, residual RMS norm, a projection with an 8-bit checkpoint
+# ---------------------------------------------------------------------------------------
+
+@torch.library.custom_op("flce_gb300::embedding", mutates_args=())
+def embedding_op(tokens: torch.Tensor, E: torch.Tensor, scale: float, ignore_index: int) -> torch.Tensor:
+    return flce.embed_fwd(tokens.contiguous(), E, scale=scale, ignore_index=ignore_index, check=False)["out"]
+
+
+@embedding_op.register_fake
+def _(tokens, E, scale, ignore_index):
+    return E.new_empty(tokens.shape[0], E.shape[1])
+
+
+@torch.library.custom_op("flce_gb300::embedding_bwd", mutates_args=())
+def embedding_bwd_op(tokens: torch.Tensor, dout: torch.Tensor, V: int, scale: float, ignore_index: int) -> torch.Tensor:
+    dE = torch.empty(V, dout.shape[1], dtype=dout.dtype, device=dout.device)
+    flce.embed_bwd(tokens.contiguous(), dout.contiguous(), dE=dE, scale=scale, ignore_index=ignore_index,
+                   flags=flce.FLAG_DW_OVERWRITE, check=False)
+    return dE
+
+
+@embedding_bwd_op.register_fake
+def _(tokens, dout, V, scale, ignore_index):
+    return dout.new_empty(V, dout.shape[1])
+
+
+def _embedding_setup(ctx, inputs, output):
+    tokens, E, scale, ignore_index = inputs
+    ctx.save_for_backward(tokens)
+    ctx.args = (E.shape[0], scale, ignore_index)
+
+
+def _embedding_backward(ctx, g):
+    tokens, = ctx.saved_tensors
+    V, scale, ignore_index = ctx.args
+    return None, embedding_bwd_op(tokens, g, V, scale, ignore_index), None, None
+
+
+embedding_op.register_autograd(_embedding_backward, setup_context=_embedding_setup)
+
+
+def embedding(tokens, E, *, scale=1.0, ignore_index=-100):
+    """scale * E[tokens], a zero row where tokens == ignore_index; differentiable in E (a dense
+    gradient in E's dtype, each row summed in fp32 in a fixed order). tokens: int64 of any
+    shape; E [V, H]."""
+    return embedding_op(tokens.reshape(-1), E, float(scale), ignore_index).reshape(*tokens.shape, E.shape[1])
+
+
+def _rows(x):
+    """x as [rows, width] with unit column stride, without a copy where it has one."""
+    return x if x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= x.shape[1] else x.reshape(-1, x.shape[-1]).contiguous()
+
+
+@torch.library.custom_op("flce_gb300::add_rms_norm", mutates_args=())
+def add_rms_norm_op(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor], eps: float,
+                    weight_offset: float, checkpoint8: bool
+                    ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(y, h, rstd, h8, h8_scale); h is empty without a residual, h8 and h8_scale without checkpoint8."""
+    o = flce.rmsnorm_fwd(_rows(x), weight, None if residual is None else _rows(residual), eps=eps,
+                         weight_offset=weight_offset, want_h8=checkpoint8)
+    e = x.new_empty(0)
+    return (o["y"], o["h"] if residual is not None else e, o["rstd"],
+            o["h8"] if checkpoint8 else e.to(torch.float8_e4m3fn), o["h8_scale"] if checkpoint8 else e.float())
+
+
+@add_rms_norm_op.register_fake
+def _(x, weight, residual, eps, weight_offset, checkpoint8):
+    N, H = x.shape
+    f32 = dict(dtype=torch.float32, device=x.device)
+    f8 = dict(dtype=torch.float8_e4m3fn, device=x.device)
+    return (x.new_empty(N, H), x.new_empty(N, H) if residual is not None else x.new_empty(0), torch.empty(N, **f32),
+            torch.empty_strided((N, H), ((H + 15) // 16 * 16, 1), **f8) if checkpoint8 else torch.empty(0, **f8),
+            torch.empty(N, (H + 127) // 128, **f32) if checkpoint8 else torch.empty(0, **f32))
+
+
+@torch.library.custom_op("flce_gb300::add_rms_norm_bwd", mutates_args=())
+def add_rms_norm_bwd_op(dy: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, h: Optional[torch.Tensor],
+                        h8: Optional[torch.Tensor], h8_scale: Optional[torch.Tensor], dh: Optional[torch.Tensor],
+                        weight_offset: float) -> tuple[torch.Tensor, torch.Tensor]:
+    """(dx, dweight)"""
+    dw = torch.empty_like(weight)
+    o = flce.rmsnorm_bwd(_rows(dy), weight, rstd, None if h is None else _rows(h), h8=h8, h8_scale=h8_scale,
+                         dh=None if dh is None else _rows(dh), weight_offset=weight_offset, dweight=dw,
+                         flags=flce.FLAG_DW_OVERWRITE)
+    return o["dx"], dw
+
+
+@add_rms_norm_bwd_op.register_fake
+def _(dy, weight, rstd, h, h8, h8_scale, dh, weight_offset):
+    return dy.new_empty(dy.shape), torch.empty_like(weight)
+
+
+def _add_rms_norm_setup(ctx, inputs, output):
+    x, weight, residual, eps, weight_offset, checkpoint8 = inputs
+    y, h, rstd, h8, h8_scale = output
+    ctx.mark_non_differentiable(rstd, h8, h8_scale)
+    ctx.set_materialize_grads(False)
+    if checkpoint8:
+        ctx.save_for_backward(weight, rstd, h8, h8_scale)
+    else:
+        ctx.save_for_backward(weight, rstd, x if residual is None else h)
+    ctx.args = (residual is not None, weight_offset, checkpoint8, x.shape, x.dtype)
+
+
+def _add_rms_norm_backward(ctx, dy, dh, *unused):
+    has_residual, weight_offset, checkpoint8, shape, dtype = ctx.args
+    if dy is None and dh is None:
+        return (None,) * 6
+    weight, rstd = ctx.saved_tensors[:2]
+    if dy is None:
+        dy = torch.zeros(shape, dtype=dtype, device=weight.device)
+    if not has_residual:
+        dh = None
+    kept = ctx.saved_tensors[2:]
+    h, h8, h8_scale = (None, *kept) if checkpoint8 else (kept[0], None, None)
+    dx, dw = add_rms_norm_bwd_op(dy, weight, rstd, h, h8, h8_scale, dh, weight_offset)
+    return dx, dw, dx if has_residual else None, None, None, None
+
+
+add_rms_norm_op.register_autograd(_add_rms_norm_backward, setup_context=_add_rms_norm_setup)
+
+
+def add_rms_norm(x, weight, residual=None, *, eps=1e-6, weight_offset=0.0, checkpoint8=False):
+    """y = h / rms(h) * (weight + weight_offset) with h = x + residual; returns (y, h) with a
+    residual, y without. Differentiable in x, residual and weight. With ``checkpoint8`` the
+    backward uses an 8-bit checkpoint of h (e4m3, a scale per 128 columns) instead of keeping
+    h itself. x and residual [..., H], weight [H], one dtype."""
+    shape = x.shape
+    y, h, _, _, _ = add_rms_norm_op(x.reshape(-1, shape[-1]), weight,
+                                    None if residual is None else residual.reshape(-1, shape[-1]), float(eps),
+                                    float(weight_offset), bool(checkpoint8))
+    return y.reshape(shape) if residual is None else (y.reshape(shape), h.reshape(shape))
+
+
+@torch.library.custom_op("flce_gb300::ckpt8_pack", mutates_args=())
+def ckpt8_pack_op(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    o = flce.ckpt8_pack(_rows(x))
+    return o["q"], o["scale"]
+
+
+@ckpt8_pack_op.register_fake
+def _(x):
+    N, H = x.shape
+    return (torch.empty_strided((N, H), ((H + 15) // 16 * 16, 1), dtype=torch.float8_e4m3fn, device=x.device),
+            torch.empty(N, (H + 127) // 128, dtype=torch.float32, device=x.device))
+
+
+@torch.library.custom_op("flce_gb300::ckpt8_dw", mutates_args=())
+def ckpt8_dw_op(dy: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, dW_fp32: bool) -> torch.Tensor:
+    dW = torch.empty(dy.shape[1], q.shape[1], dtype=torch.float32 if dW_fp32 else dy.dtype, device=dy.device)
+    flce.ckpt8_dw(_rows(dy), q, scale, dW=dW, flags=flce.FLAG_DW_OVERWRITE, check=False)
+    return dW
+
+
+@ckpt8_dw_op.register_fake
+def _(dy, q, scale, dW_fp32):
+    return torch.empty(dy.shape[1], q.shape[1], dtype=torch.float32 if dW_fp32 else dy.dtype, device=dy.device)
+
+
+class LinearCkpt8(torch.autograd.Function):
+    """y = x W^T that keeps x in 8 bits for the weight gradient."""
+
+    @staticmethod
+    def forward(ctx, x, W):
+        need = ctx.needs_input_grad[1]
+        q, scale = ckpt8_pack_op(x) if need else (None, None)
+        ctx.save_for_backward(W, q, scale)
+        return torch.mm(x, W.t())
+
+    @staticmethod
+    def backward(ctx, dy):
+        W, q, scale = ctx.saved_tensors
+        dx = torch.mm(dy, W) if ctx.needs_input_grad[0] else None
+        dW = ckpt8_dw_op(dy, q, scale, W.dtype == torch.float32) if ctx.needs_input_grad[1] else None
+        return dx, dW
+
+
+def linear_ckpt8(x, W):
+    """x W^T for x [..., K] and W [N, K] of one dtype; the backward's dW = dy^T x reads an 8-bit
+    checkpoint of x (its rounding, half of 2^-3 of a value, is the only approximation; dx is
+    exact). x itself is not kept."""
+    return LinearCkpt8.apply(x.reshape(-1, x.shape[-1]), W).reshape(*x.shape[:-1], W.shape[0])

@@ -195,3 +195,49 @@ def test_dw_same_bits_and_side_stream():
     b = flce.ckpt8_dw(dy, p["q"], p["scale"], stream=s)
     torch.cuda.current_stream().wait_stream(s)
     assert b["status_code"] == flce.FLCE_OK and torch.equal(a, b["dW"])
+
+
+def test_dw_wait_limit():
+    """A pipeline stage that is never filled: the bounded waits run out, the call reports it, and
+    the next call is normal."""
+    g = torch.Generator().manual_seed(9)
+    p = flce.ckpt8_pack(torch.randn(1000, 512, generator=g).bfloat16().cuda())
+    dy = torch.randn(1000, 300, generator=g).bfloat16().cuda()
+    a = flce.ckpt8_dw(dy, p["q"], p["scale"])["dW"]
+    o = flce.ckpt8_dw(dy, p["q"], p["scale"], flags=flce.FLAG_DEBUG_STALL, wait_timeout_ms=50)
+    assert o["status_code"] == flce.FLCE_ERR_TIMEOUT
+    b = flce.ckpt8_dw(dy, p["q"], p["scale"])
+    assert b["status_code"] == flce.FLCE_OK and torch.equal(a, b["dW"])
+
+
+def test_calls_in_a_graph():
+    """The operators enqueue kernels and memsets only: captured once, replayed on new inputs."""
+    g = torch.Generator().manual_seed(10)
+    x = torch.randn(700, 520, generator=g).bfloat16().cuda()
+    dy = torch.randn(700, 264, generator=g).bfloat16().cuda()
+    t = torch.randint(0, 90, (700,), generator=g).cuda()
+    w = torch.ones(520).bfloat16().cuda()
+    dE, dW = torch.zeros(90, 520, device="cuda"), torch.zeros(264, 520, device="cuda")
+
+    def call():
+        o = flce.rmsnorm_fwd(x, w, want_h8=True)
+        b = flce.rmsnorm_bwd(o["y"], w, o["rstd"], h8=o["h8"], h8_scale=o["h8_scale"])
+        flce.embed_bwd(t, b["dx"], dE=dE, flags=flce.FLAG_DW_OVERWRITE, check=False)
+        p = flce.ckpt8_pack(o["y"])
+        flce.ckpt8_dw(dy, p["q"], p["scale"], dW=dW, flags=flce.FLAG_DW_OVERWRITE, check=False)
+        return flce.embed_fwd(t, dE, check=False)["out"], b["dweight"]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, dweight = call()
+    x.copy_(torch.randn(700, 520, generator=g).bfloat16())
+    graph.replay()
+    got = [v.clone() for v in (out, dweight, dE, dW)]
+    want = call()
+    for a, b in zip(got, (*want, dE, dW)):
+        assert torch.equal(a, b)
