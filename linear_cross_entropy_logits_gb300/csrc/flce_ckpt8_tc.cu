@@ -112,16 +112,13 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 
 // Four e4m3 values times a scale, as two pairs of 16-bit values (packed fp32 products).
 template <typename T>
-__device__ __forceinline__ uint2 expand4(uint32_t u, uint64_t sc2) {
+__device__ __forceinline__ uint2 expand4(uint32_t u, f2 sc2) {
   uint32_t o[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const float2 x = q_unpack2(i ? u >> 16 : u);
-    uint64_t a;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(x.x), "f"(x.y));
-    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(sc2));
     float lo, hi;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a));
+    f2_get(f2_mul(f2_make(x.x, x.y), sc2), lo, hi);
     o[i] = pack16<T>(lo, hi);
   }
   return make_uint2(o[0], o[1]);
@@ -355,8 +352,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mma_commit_local(drain);
       bar_wait(drain, 0u, ab, false);
     } else if (warp == 2) {
-      // ---------------- scales of a step's 64 rows, that of row 8 j + r at 8 r + j
-      const uint32_t dst = smem_u32(smem + OFF_S) + (uint32_t)((lane & 7) * 8 + (lane >> 3)) * 4;
+      // ---------------- scales of a step's 64 rows, that of row 16 j + r at 4 r + j
+      const uint32_t dst = smem_u32(smem + OFF_S) + (uint32_t)((lane & 15) * 4 + (lane >> 4)) * 4;
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -372,7 +369,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int h = 0; h < 2; ++h) {
             const int64_t m = (int64_t)row * BK + h * 32 + lane;
             const bool in = blk < p.d.nblk && m < p.d.M;
-            cp_async4(dst + (uint32_t)(s * S_BYTES + h * 16), sp + (in ? m * p.d.nblk : 0), in);
+            cp_async4(dst + (uint32_t)(s * S_BYTES + h * 8), sp + (in ? m * p.d.nblk : 0), in);
           }
           bar_arrive_cp_async(full_s(s));
           if (++row == p.mstep) row = 0;
@@ -387,11 +384,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp < 4 + CONV_WARPS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     // ---------------- expand q: groups of four warps take the steps in turn, so a step's
-    // expansion may last as many steps; thread (r, c) takes bytes 8c .. 8c + 7 of rows r + 8 j
+    // expansion may last as many steps; thread (r, c) takes bytes 16c .. 16c + 15 of rows r + 16 j.
+    // Threads of columns 64.. take the neighbouring row, so that eight threads' reads (64 bytes of
+    // each of two rows) and writes (every other 16-byte chunk of two rows) hit distinct banks
     const int group = (warp - 4) >> 2;
     const int t = threadIdx.x & 127;
-    const int c = t & 15, r = t >> 4;
-    const uint32_t out = (uint32_t)(c >> 3) * BOX + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ r) << 4);
+    const int c = t & 7, r = (t >> 3) ^ (c >> 2);
+    const uint32_t out = (uint32_t)(c >> 2) * BOX + (uint32_t)r * 128;
+    const uint32_t chunk = (uint32_t)((2 * (c & 3)) ^ (r & 7)) << 4;  // of bytes 16c ..; its neighbour's: ^ 16
     int s = 0, b = 0, turn = 0, whose = 0;
     uint32_t ph = 0;
     bool ok = true;
@@ -408,23 +408,20 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const uint8_t* q = smem + s * STAGE_BYTES + A_BYTES + r * 128 + c * 8;
+          const uint8_t* q = smem + s * STAGE_BYTES + A_BYTES + r * 128 + c * 16;
           uint8_t* o = smem + OFF_B + b * B_BYTES + out;
-          const float4* sc4 = (const float4*)(smem + OFF_S + s * S_BYTES + r * 32);
+          const float4 f = *(const float4*)(smem + OFF_S + s * S_BYTES + r * 16);
+          const float sc[4] = {f.x, f.y, f.z, f.w};
+          uint4 u[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 f = sc4[h];
-            const float sc[4] = {f.x, f.y, f.z, f.w};
-            uint2 u[4];
+          for (int j = 0; j < 4; ++j) u[j] = *(const uint4*)(q + j * 2048);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) u[j] = *(const uint2*)(q + (4 * h + j) * 1024);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint64_t sc2;
-              asm("mov.b64 %0, {%1, %1};" : "=l"(sc2) : "f"(sc[j]));
-              const uint2 x = expand4<T>(u[j].x, sc2), y = expand4<T>(u[j].y, sc2);
-              *(uint4*)(o + (4 * h + j) * 1024) = make_uint4(x.x, x.y, y.x, y.y);
-            }
+          for (int j = 0; j < 4; ++j) {
+            const f2 sc2 = f2_make(sc[j], sc[j]);
+            const uint2 x0 = expand4<T>(u[j].x, sc2), x1 = expand4<T>(u[j].y, sc2);
+            const uint2 x2 = expand4<T>(u[j].z, sc2), x3 = expand4<T>(u[j].w, sc2);
+            *(uint4*)(o + j * 2048 + chunk) = make_uint4(x0.x, x0.y, x1.x, x1.y);
+            *(uint4*)(o + j * 2048 + (chunk ^ 16)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
           }
           fence_async();
           __syncwarp();
