@@ -241,3 +241,35 @@ def test_calls_in_a_graph():
     want = call()
     for a, b in zip(got, (*want, dE, dW)):
         assert torch.equal(a, b)
+
+
+def test_dw_status_word_in_the_workspace():
+    """Without a status word of the caller's, flce_get_status reads the workspace's."""
+    p = flce.ckpt8_pack(torch.randn(200, 128, device="cuda"))
+    o = flce.ckpt8_dw(torch.randn(200, 64, device="cuda"), p["q"], p["scale"], check=False)
+    lib, s = flce.load(), torch.cuda.current_stream().cuda_stream
+    assert lib.flce_get_status(None, o["workspace"].data_ptr(), s) == flce.FLCE_OK
+    o = flce.ckpt8_dw(torch.randn(200, 64, device="cuda"), p["q"], p["scale"], check=False, wait_timeout_ms=50,
+                      flags=flce.FLAG_DEBUG_STALL)
+    assert lib.flce_get_status(None, o["workspace"].data_ptr(), s) == flce.FLCE_ERR_TIMEOUT
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows go through packing, the norm and its gradient."""
+    N, H = 530_000, 4096
+    x = torch.zeros(N, H, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(7, H, generator=torch.Generator().manual_seed(11)).bfloat16().cuda()
+    x[-7:] = tail
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    p, q = flce.ckpt8_pack(x), flce.ckpt8_pack(tail)
+    assert torch.equal(p["q"][-7:].float(), q["q"].float()) and torch.equal(p["scale"][-7:], q["scale"])
+    o, s = flce.rmsnorm_fwd(x, w, eps=1e-5), flce.rmsnorm_fwd(tail, w, eps=1e-5)
+    assert torch.equal(o["y"][-7:], s["y"]) and torch.equal(o["rstd"][-7:], s["rstd"])
+    b = flce.rmsnorm_bwd(x, w, o["rstd"], h8=p["q"], h8_scale=p["scale"])
+    c = flce.rmsnorm_bwd(tail, w, s["rstd"], h8=q["q"], h8_scale=q["scale"])
+    assert torch.equal(b["dx"][-7:], c["dx"])
+    assert torch.all(b["dx"][:-7] == 0)
+    dy = torch.zeros(N, 64, dtype=torch.bfloat16, device="cuda")
+    dy[-7:] = 1
+    a = flce.ckpt8_dw(dy, p["q"], p["scale"])["dW"]
+    assert torch.equal(a, flce.ckpt8_dw(dy[-7:], q["q"], q["scale"])["dW"])
