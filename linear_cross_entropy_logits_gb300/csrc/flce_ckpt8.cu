@@ -22,15 +22,20 @@ __global__ void __launch_bounds__(256) k_pack(const T* __restrict__ x, int64_t l
   const int64_t g = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
   const int64_t row = g / wpr, w = g - row * wpr;
   if (row >= N) return;
+  constexpr int SPAN = NV * 32 * EPV;  // the warp's columns: whole blocks
+  static_assert(SPAN % Q_BLOCK == 0, "a block belongs to one warp");
+  const int64_t c0 = w * SPAN;
+  const int left = (int)(H - c0 < SPAN ? H - c0 : SPAN);
+  x += row * ldx + c0;
   float v[NV][EPV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t c = ((w * NV + j) * 32 + lane) * EPV;
+    const int c = (j * 32 + lane) * EPV;
 #pragma unroll
     for (int e = 0; e < EPV; ++e) v[j][e] = 0.0f;
-    if (c < H) Vec<T, EPV>::load(x + row * ldx + c, v[j]);
+    if (c < left) Vec<T, EPV>::load(x + c, v[j]);
   }
-  q_row_piece<EPV, NV>(v, (int)w, lane, H, q + row * ldq, scale + row * nblk, 1.0f);
+  q_row_piece<EPV, NV>(v, 0, lane, left, q + row * ldq + c0, scale + row * nblk + c0 / Q_BLOCK, 1.0f);
 }
 
 template <typename T, int EPV, int NV>

@@ -67,22 +67,25 @@ __device__ __forceinline__ float group_sum(float v, float* red, int wpr, int war
 }
 
 template <typename T, int EPV, int NV>
-__global__ void __launch_bounds__(512) k_rms_fwd(const __grid_constant__ FwdArgs a, int wpr) {
+__global__ void __launch_bounds__(EPV == 1 ? 1024 : 512) k_rms_fwd(const __grid_constant__ FwdArgs a, int wpr) {
   __shared__ float red[MAX_WARPS];
   const int lane = threadIdx.x & 31, wb = threadIdx.x >> 5;
   const int group = wb / wpr, w = wb - group * wpr;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / 32 / wpr) + group;
   const bool live = row < a.N;
+  const int c0 = (w * NV * 32 + lane) * EPV, H = (int)a.H;
+  const T* xp = (const T*)a.x + row * a.ldx;
+  const T* resp = (const T*)a.res + row * a.ldres;
   float v[NV][EPV];
   Raw<T, EPV> x[NV], r[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
+    const int c = c0 + j * 32 * EPV;
     x[j].zero();
     r[j].zero();
-    if (live && c < a.H) {
-      x[j].load((const T*)a.x + row * a.ldx + c);
-      if (a.res != nullptr) r[j].load((const T*)a.res + row * a.ldres + c);
+    if (live && c < H) {
+      x[j].load(xp + c);
+      if (a.res != nullptr) r[j].load(resp + c);
     }
   }
   float ss = 0.0f;
@@ -102,16 +105,16 @@ __global__ void __launch_bounds__(512) k_rms_fwd(const __grid_constant__ FwdArgs
   if (a.h != nullptr) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
-      if (c < a.H) Vec<T, EPV>::store((T*)a.h + row * a.ldh + c, v[j]);
+      const int c = c0 + j * 32 * EPV;
+      if (c < H) Vec<T, EPV>::store((T*)a.h + row * a.ldh + c, v[j]);
     }
   }
-  if (a.h8 != nullptr) q_row_piece<EPV, NV>(v, w, lane, a.H, a.h8 + row * a.ldh8, a.h8s + row * a.nblk, 1.0f);
+  if (a.h8 != nullptr) q_row_piece<EPV, NV>(v, w, lane, H, a.h8 + row * a.ldh8, a.h8s + row * a.nblk, 1.0f);
   if (a.y == nullptr && a.y8 == nullptr) return;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
-    if (c < a.H) {
+    const int c = c0 + j * 32 * EPV;
+    if (c < H) {
       float wt[EPV], o[EPV];
       Vec<T, EPV>::load((const T*)a.w + c, wt);
 #pragma unroll
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(512) k_rms_fwd(const __grid_constant__ FwdArgs
       if (a.y != nullptr) Vec<T, EPV>::store((T*)a.y + row * a.ldy + c, o);
     }
   }
-  if (a.y8 != nullptr) q_row_piece<EPV, NV>(v, w, lane, a.H, a.y8 + row * a.ldy8, a.y8s + row * a.nblk, rstd);
+  if (a.y8 != nullptr) q_row_piece<EPV, NV>(v, w, lane, H, a.y8 + row * a.ldy8, a.y8s + row * a.nblk, rstd);
 }
 
 // Rows of any length: a block per row, two passes over it in pieces of 4 x 128 columns per
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(512) k_rms_fwd_long(const __grid_constant__ Fw
   for (int64_t p = w; p * Q_BLOCK < a.H; p += nw) {  // one 128-column block per warp and turn
     float v[4][1];
     const int64_t c0 = p * Q_BLOCK;
-    const int64_t left = a.H - c0;
+    const int left = (int)(a.H - c0 < Q_BLOCK ? a.H - c0 : Q_BLOCK);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t c = c0 + j * 32 + lane;
@@ -224,14 +227,15 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
 // group + groups, .... Each thread copies its own pieces of the next RING - 1 rows to shared
 // memory (cp.async) and reads back only those: no registers and no barriers for what is in
 // flight. g and xhat stay in registers over the row's sum, and the arithmetic is done two
-// elements at a time (packed fp32). The columns' dweight sums stay in registers throughout. One
-// block of 512 threads an SM: with 768 threads (80 registers) it took 15 us longer, with the next
+// elements at a time (packed fp32). The columns' dweight sums stay in registers throughout.
+// RING is 4; fp32 rows over 4096 columns, of which four do not fit shared memory, take 2 (4096 x
+// 8192 from the checkpoint 69 us, 107 with the row in registers as in k_rms_bwd). One block of 512
+// threads an SM: with 768 threads (80 registers) it took 15 us longer, with the next
 // row in registers instead of shared memory 2 to 10 us. What bounds it now is the row's chain of
 // loads, sum and barrier at four warps a scheduler.
-constexpr int RING = 4;
-template <typename T>
-constexpr int RING_WARPS = sizeof(T) == 4 ? 8 : 16;  // a block's, for its ring to fit
-template <typename T, int NV, bool Q8>
+template <typename T, int RING>
+constexpr int RING_WARPS = 32 * RING * sizeof(T) > 256 ? 8 : 16;  // a block's, for its ring to fit
+template <typename T, int NV, bool Q8, int RING>
 __global__ void __launch_bounds__(512, 1) k_rms_bwd_ring(const __grid_constant__ BwdArgs a, int wpr) {
   constexpr int EPV = 16 / sizeof(T);
   constexpr int NP = EPV / 2;        // pairs per vector
@@ -394,13 +398,15 @@ __global__ void __launch_bounds__(512, 1) k_rms_bwd_ring(const __grid_constant__
   put_partials<EPV, NV>(a, dws, (float*)ring, rpb, group, w, lane);
 }
 
-// Backward of other rows: a row group walks the rows group, group + groups, ...; its threads keep their
-// columns' dweight sums in registers. All of a row is loaded before its sum is taken and kept as
-// it lies in memory (unpacked again after the sum), so that two blocks of 512 threads fit an SM
-// and enough loads are in flight. At the end the block's groups add their sums in group order
-// and write one row of a.part.
+// Backward of other rows (longer, or without 16-byte accesses): a row group walks the rows group,
+// group + groups, ...; its threads keep their columns' dweight sums in registers. All of a row is
+// loaded before its sum is taken. At the end the block's groups add their sums in group order and
+// write one row of a.part. Single elements are bound by the instructions they take: eight a
+// thread, 64 registers and all 32 warps' worth an SM (20762 x 1167 bf16 65 us; 4097 x 5121 67 us,
+// 127 with sixteen a thread).
 template <typename T, int EPV, int NV, bool Q8>
-__global__ void __launch_bounds__(512, NV * EPV <= 16 ? 2 : 1) k_rms_bwd(const __grid_constant__ BwdArgs a, int wpr) {
+__global__ void __launch_bounds__(EPV == 1 ? 1024 : 512, 1) k_rms_bwd(const __grid_constant__ BwdArgs a, int wpr) {
+  constexpr int JB = EPV == 1 ? 4 : 1;  // a thread's vectors that share an 8-bit row's scale
   __shared__ float red[2][MAX_WARPS];
   extern __shared__ float sums[];  // [H] where the block has several groups
   let_next_start();
@@ -408,13 +414,14 @@ __global__ void __launch_bounds__(512, NV * EPV <= 16 ? 2 : 1) k_rms_bwd(const _
   const int rpb = blockDim.x / 32 / wpr;
   const int group = wb / wpr, w = wb - group * wpr;
   const int64_t g0 = (int64_t)blockIdx.x * rpb + group, step = (int64_t)gridDim.x * rpb;
+  const int c0 = (w * NV * 32 + lane) * EPV, H = (int)a.H;
   Raw<T, EPV> wt[NV];
   float dw[NV][EPV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
+    const int c = c0 + j * 32 * EPV;
     wt[j].zero();
-    if (c < a.H) wt[j].load((const T*)a.w + c);
+    if (c < H) wt[j].load((const T*)a.w + c);
 #pragma unroll
     for (int e = 0; e < EPV; ++e) dw[j][e] = 0.0f;
   }
@@ -426,51 +433,53 @@ __global__ void __launch_bounds__(512, NV * EPV <= 16 ? 2 : 1) k_rms_bwd(const _
     const bool live = row < a.N;
     Raw<T, EPV> dy[NV], dh[NV];
     typename std::conditional<Q8, RawQ<EPV>, Raw<T, EPV>>::type h[NV];
-    float f[NV];  // what h is multiplied by to give xhat
+    float f[NV / JB];  // what h is multiplied by to give xhat
     const float rstd = live ? a.rstd[row] : 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
-      f[j] = rstd;
+      const int c = c0 + j * 32 * EPV;
+      if (j % JB == 0) f[j / JB] = rstd;
       dy[j].zero();
       dh[j].zero();
 #pragma unroll
       for (int i = 0; i < h[j].W; ++i) h[j].w[i] = 0u;
-      if (live && c < a.H) {
+      if (live && c < H) {
         dy[j].load((const T*)a.dy + row * a.lddy + c);
         if constexpr (Q8) {
           h[j].load(a.h8 + row * a.ldh8 + c);
-          f[j] = a.h8s[row * a.nblk + c / Q_BLOCK];
+          if (j % JB == 0) f[j / JB] = a.h8s[row * a.nblk + c / Q_BLOCK];
         } else {
           h[j].load((const T*)a.h + row * a.ldh + c);
         }
         if (a.dh != nullptr) dh[j].load((const T*)a.dh + row * a.lddh + c);
       }
     }
-    float dot = 0.0f;
+    float dot = 0.0f, keep[NV];  // single elements: xhat
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if constexpr (Q8) f[j] *= rstd;
+      if (Q8 && j % JB == 0) f[j / JB] *= rstd;
       float xh[EPV];
       h[j].unpack(xh);
 #pragma unroll
       for (int e = 0; e < EPV; ++e) {
-        const float d = dy[j].get(e), x = xh[e] * f[j];
+        const float d = dy[j].get(e), x = xh[e] * f[j / JB];
         dot = fmaf(d * (wt[j].get(e) + a.off), x, dot);
         dw[j][e] = fmaf(d, x, dw[j][e]);
+        keep[j] = x;
       }
     }
     const float m = group_sum(dot, red[buf], wpr, wb, group) * a.inv_h;
     if (!live || a.dx == nullptr) continue;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = ((int64_t)(w * NV + j) * 32 + lane) * EPV;
-      if (c < a.H) {
+      const int c = c0 + j * 32 * EPV;
+      if (c < H) {
         float xh[EPV], o[EPV];
-        h[j].unpack(xh);
+        if constexpr (EPV > 1) h[j].unpack(xh);
 #pragma unroll
         for (int e = 0; e < EPV; ++e) {
-          o[e] = rstd * (dy[j].get(e) * (wt[j].get(e) + a.off) - xh[e] * f[j] * m);
+          const float x = EPV > 1 ? xh[e] * f[j / JB] : keep[j];
+          o[e] = rstd * (dy[j].get(e) * (wt[j].get(e) + a.off) - x * m);
           if (a.dh != nullptr) o[e] += dh[j].get(e);
         }
         Vec<T, EPV>::store((T*)a.dx + row * a.lddx + c, o);
@@ -549,14 +558,15 @@ constexpr int LONG_DW_ROWS = 64;  // row groups of k_rms_dw_long
 enum Width { W32, W16, W1 };
 
 // Warps per row and vectors per thread of a row of H elements in vectors of EPV: the fewest
-// warps with 16 elements a thread (8 as single elements), else 16 warps with 32 (16) elements;
-// 0 when none holds it.
+// warps with 16 elements a thread, else 16 warps with 32 (single elements: up to 32 warps with
+// 8); 0 when none holds it.
 struct Shape {
   int wpr, nv;
 };
 Shape row_shape(int64_t H, int epv) {
   const int64_t nvec = cdiv64(H, epv);
-  const int small = epv == 1 ? 8 : 16 / epv, large = 2 * small;
+  if (epv == 1) return {nvec <= 32 * 32 * 8 ? (int)cdiv64(nvec, 32 * 8) : 0, 8};
+  const int small = 16 / epv, large = 2 * small;
   if (cdiv64(nvec, 32 * small) <= 16) return {(int)cdiv64(nvec, 32 * small), small};
   if (cdiv64(nvec, 32 * large) <= 16) return {16, large};
   return {0, 0};
@@ -579,7 +589,7 @@ cudaError_t fwd_w(const FwdArgs& a, cudaStream_t s) {
     const unsigned blocks = (unsigned)cdiv64(a.N, rpb);
     const int threads = (int)rpb * p.wpr * 32;
     if (p.nv == NV) k_rms_fwd<T, EPV, NV><<<blocks, threads, 0, s>>>(a, p.wpr);
-    else k_rms_fwd<T, EPV, 2 * NV><<<blocks, threads, 0, s>>>(a, p.wpr);
+    else if constexpr (EPV > 1) k_rms_fwd<T, EPV, 2 * NV><<<blocks, threads, 0, s>>>(a, p.wpr);
   }
   return cudaGetLastError();
 }
@@ -591,10 +601,10 @@ cudaError_t fwd(const FwdArgs& a, Width w, cudaStream_t s) {
 
 template <typename T, int EPV, int NV>
 int64_t launch_bwd(const BwdArgs& a, int wpr, cudaStream_t s) {
-  const int64_t rpb = 16 / wpr;
+  const int64_t rpb = wpr > 16 ? 1 : 16 / wpr;
   const int threads = (int)rpb * wpr * 32;
   const size_t smem = rpb > 1 ? (size_t)a.H * 4 : 0;
-  int64_t blocks = (int64_t)num_sms() * BWD_BLOCKS_PER_SM;
+  int64_t blocks = (int64_t)num_sms() * (EPV == 1 && wpr <= 16 ? BWD_BLOCKS_PER_SM : 1);
   if (blocks > cdiv64(a.N, rpb)) blocks = cdiv64(a.N, rpb);
   if (a.h8 != nullptr) k_rms_bwd<T, EPV, NV, true><<<(unsigned)blocks, threads, smem, s>>>(a, wpr);
   else k_rms_bwd<T, EPV, NV, false><<<(unsigned)blocks, threads, smem, s>>>(a, wpr);
@@ -611,19 +621,20 @@ cudaError_t bwd_w(const BwdArgs& a, int64_t& part_rows, cudaStream_t s) {
       k_rms_dw_long<T><<<dim3((unsigned)cdiv64(a.H, 256), LONG_DW_ROWS), 256, 0, s>>>(a);
     }
   } else {
-    part_rows = p.nv == NV ? launch_bwd<T, EPV, NV>(a, p.wpr, s) : launch_bwd<T, EPV, 2 * NV>(a, p.wpr, s);
+    // (rows in wider accesses come here with 32 elements a thread only)
+    part_rows = launch_bwd<T, EPV, EPV == 1 ? NV : 2 * NV>(a, p.wpr, s);
   }
   return cudaGetLastError();
 }
-template <typename T, int NV, bool Q8>
+template <typename T, int NV, bool Q8, int RING>
 cudaError_t launch_ring(const BwdArgs& a, int wpr, int64_t& part_rows, cudaStream_t s) {
   constexpr int EPV = 16 / sizeof(T);
   const int64_t sms = num_sms();
   // as many groups a block as there are rows for
   int64_t rpb = cdiv64(a.N, sms);
-  if (rpb > RING_WARPS<T> / wpr) rpb = RING_WARPS<T> / wpr;
+  if (rpb > RING_WARPS<T, RING> / wpr) rpb = RING_WARPS<T, RING> / wpr;
   const int threads = (int)rpb * wpr * 32;
-  constexpr int most = RING * 32 * RING_WARPS<T> * NV * (32 + (Q8 ? EPV : 16));
+  constexpr int most = RING * 32 * RING_WARPS<T, RING> * NV * (32 + (Q8 ? EPV : 16));
   static_assert(most <= 232448 - 1024, "shared memory per block");
   const size_t smem = (size_t)RING * threads * NV * (32 + (Q8 ? EPV : 16));
   static std::atomic<bool> raised[64];
@@ -632,12 +643,12 @@ cudaError_t launch_ring(const BwdArgs& a, int wpr, int64_t& part_rows, cudaStrea
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!raised[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(k_rms_bwd_ring<T, NV, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    e = cudaFuncSetAttribute(k_rms_bwd_ring<T, NV, Q8, RING>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     raised[dev].store(true, std::memory_order_relaxed);
   }
   part_rows = cdiv64(a.N, rpb) < sms ? cdiv64(a.N, rpb) : sms;
-  k_rms_bwd_ring<T, NV, Q8><<<(unsigned)part_rows, threads, smem, s>>>(a, wpr);
+  k_rms_bwd_ring<T, NV, Q8, RING><<<(unsigned)part_rows, threads, smem, s>>>(a, wpr);
   return cudaGetLastError();
 }
 
@@ -646,9 +657,14 @@ cudaError_t bwd(const BwdArgs& a, Width w, int64_t& part_rows, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
   if (w == W1) return bwd_w<T, 1>(a, part_rows, s);
   const int64_t wpr = cdiv64(a.H, 512);  // 16 elements a thread
-  if (wpr <= RING_WARPS<T>)
-    return a.h8 ? launch_ring<T, 16 / E, true>(a, (int)wpr, part_rows, s)
-                : launch_ring<T, 16 / E, false>(a, (int)wpr, part_rows, s);
+  if (wpr <= RING_WARPS<T, 4>)
+    return a.h8 ? launch_ring<T, 16 / E, true, 4>(a, (int)wpr, part_rows, s)
+                : launch_ring<T, 16 / E, false, 4>(a, (int)wpr, part_rows, s);
+  if constexpr (RING_WARPS<T, 4> < RING_WARPS<T, 2>) {
+    if (wpr <= RING_WARPS<T, 2>)
+      return a.h8 ? launch_ring<T, 16 / E, true, 2>(a, (int)wpr, part_rows, s)
+                  : launch_ring<T, 16 / E, false, 2>(a, (int)wpr, part_rows, s);
+  }
   return bwd_w<T, E>(a, part_rows, s);
 }
 

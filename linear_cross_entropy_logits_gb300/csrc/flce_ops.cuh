@@ -249,7 +249,7 @@ __device__ __forceinline__ void q_store(uint8_t* p, const float (&v)[EPV]) {
 // (fmaxf) and is stored as NaN; a warp that meets an infinity makes the maxima again without
 // it and stores NaN for it (e4m3 has no infinity).
 template <int EPV, int NV>
-__device__ __forceinline__ void q_row_piece(const float (&v)[NV][EPV], int warp, int lane, int64_t H, uint8_t* q,
+__device__ __forceinline__ void q_row_piece(const float (&v)[NV][EPV], int warp, int lane, int H, uint8_t* q,
                                             float* s, float factor) {
   static_assert(EPV != 1 || NV % 4 == 0, "a block of single elements spans four vectors");
   constexpr int JB = EPV == 1 ? 4 : 1;                // vectors per block
@@ -279,10 +279,10 @@ __device__ __forceinline__ void q_row_piece(const float (&v)[NV][EPV], int warp,
     }
     const int e2 = q_exponent(m);
     const float inv = exp2_int(-e2);
-    const int64_t c0 = ((int64_t)(warp * NV + j0) * 32 + lane) * EPV;
+    const int c0 = ((warp * NV + j0) * 32 + lane) * EPV;
 #pragma unroll
     for (int j = j0; j < j0 + JB; ++j) {
-      const int64_t c = c0 + (int64_t)(j - j0) * 32 * EPV;
+      const int c = c0 + (j - j0) * 32 * EPV;
       if (c < H) {
         float o[EPV];
 #pragma unroll

@@ -41,7 +41,8 @@ def _sum32(x, r):
 
 SHAPES = [(1, 1, "f32"), (1, 4096, "bf16"), (3, 128, "bf16"), (5, 130, "f16"), (4, 127, "f32"), (33, 256, "bf16"),
           (9, 2048, "f16"), (7, 1337, "f32"), (6, 5376, "bf16"), (2, 8192, "f32"), (3, 16384, "bf16"), (5, 4099, "bf16"),
-          (2, 20000, "f16"), (2, 9001, "bf16"), (70, 64, "f32"), (1000, 520, "bf16")]
+          (2, 20000, "f16"), (2, 9001, "bf16"), (70, 64, "f32"), (1000, 520, "bf16"), (3, 8191, "f16"), (2, 8193, "f32"),
+          (4, 5121, "f32")]
 
 
 @pytest.mark.parametrize("N,H,dt", SHAPES)
@@ -125,7 +126,8 @@ def test_no_rows():
 
 
 BWD = [(1, 1, "f32"), (1, 4096, "bf16"), (3, 130, "f16"), (65, 256, "bf16"), (200, 1337, "f32"), (17, 5376, "bf16"),
-       (5, 16384, "f16"), (9, 9001, "bf16"), (4, 20000, "bf16"), (3000, 72, "bf16"), (2, 8192, "f32"), (12000, 136, "f16")]
+       (5, 16384, "f16"), (9, 9001, "bf16"), (4, 20000, "bf16"), (3000, 72, "bf16"), (2, 8192, "f32"), (12000, 136, "f16"),
+       (700, 8192, "f32"), (310, 6112, "f32"), (700, 5121, "bf16"), (3, 8191, "f16"), (1000, 1167, "bf16")]
 
 
 @pytest.mark.parametrize("N,H,dt", BWD)
