@@ -129,42 +129,20 @@ __device__ __forceinline__ uint2 expand4(uint32_t u, f2 sc2) {
 }
 
 // A warp's 32 rows x 128 columns of sums (lane = row) to a matrix: dst, its element (0, 0) of them,
-// of which `rows` x `cols` exist, (+)= acc. fp32 is added by L2 (one add an element: nothing to wait
-// for, and the same bits on every run); 16-bit values are read, so that they are rounded once. 16 columns at a time pass through shared memory
-// (16-byte chunk c of row r at c ^ (r / 2 % 4): free of bank conflicts both ways), so that a
-// store covers 64 bytes of each of 8 rows: stored a row per lane, 16 bytes of 32 rows at a time,
-// the rows' pitch puts most of a warp's accesses on few L2 slices (28 tiles of 256 x 256 at a
-// pitch of 16 KB took 77 us).
-template <typename D>
-__device__ __forceinline__ void emit(D* dst, int64_t ld, int rows, int cols, bool vec, bool ovw, const float (&acc)[128],
+// of which `rows` x `cols` exist, = acc (ovw) or += acc. fp32 is added by L2 (one add an element:
+// nothing to wait for, and the same bits on every run); 16-bit values are read, so that they are
+// rounded once, each block of 16 columns while the one before is written (500 x 4096 x 4096 bf16:
+// 53 us, 64 without). 16 columns at a time pass through shared memory (16-byte chunk c of row r at
+// c ^ (r / 2 % 4): free of bank conflicts both ways), so that a store covers 64 bytes of each of 8
+// rows: stored a row per lane, 16 bytes of 32 rows at a time, the rows' pitch puts most of a warp's
+// accesses on few L2 slices (28 tiles of 256 x 256 at a pitch of 16 KB took 77 us). vec: rows allow
+// accesses of four elements.
+template <typename D, bool ovw>
+__device__ __forceinline__ void emit(D* dst, int64_t ld, int rows, int cols, bool vec, const float (&acc)[128],
                                      uint32_t stage, int lane) {
   const uint32_t wr = stage + (uint32_t)lane * 64;
   const int sw = (lane >> 1) & 3;
-  const int c4 = (lane & 3) * 4;  // this lane's columns of a block, and its first row
-  const int r0 = lane >> 2;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (16 * j >= cols) break;
-    float old[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) old[i][e] = 0.0f;
-      const int r = r0 + 8 * i, c = 16 * j + c4;
-      if (sizeof(D) == 2 && !ovw && r < rows) {
-        const D* p = dst + r * ld + c;
-        if (vec && c + 4 <= cols) {
-          const uint2 v = *(const uint2*)p;
-          const D* h = (const D*)&v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) old[i][e] = to_f<D>(h[e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c + e < cols) old[i][e] = to_f<D>(p[e]);
-        }
-      }
-    }
+  auto put = [&](int j) {
     __syncwarp();  // the block before has been read
 #pragma unroll
     for (int c = 0; c < 4; ++c)
@@ -172,6 +150,80 @@ __device__ __forceinline__ void emit(D* dst, int64_t ld, int rows, int cols, boo
                    "f"(acc[16 * j + 4 * c + 1]), "f"(acc[16 * j + 4 * c + 2]), "f"(acc[16 * j + 4 * c + 3])
                    : "memory");
     __syncwarp();
+  };
+  if (!vec) {
+    // a lane has one column of every second row, so that a store covers 16 columns of two rows
+    // (four columns a lane as below: 70 -> 42 us at 500 x 4096 x 4097)
+    constexpr int B = ovw ? 4 : 8;  // rows at a time
+    const int c = lane & 15, r0 = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (16 * j >= cols) break;
+      const int left = 16 * j + c < cols ? rows - r0 : 0;  // rows from r0 on
+      D* o = dst + r0 * ld + 16 * j + c;
+      put(j);
+#pragma unroll 1
+      for (int i = 0; i < 16; i += B) {
+        float v[B];
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+          const int r = r0 + 2 * (i + u);
+          asm volatile("ld.shared.f32 %0, [%1];"
+                       : "=f"(v[u])
+                       : "r"(stage + (uint32_t)(r * 64 + (((c >> 2) ^ ((r >> 1) & 3)) << 4) + (c & 3) * 4)));
+        }
+        if constexpr (sizeof(D) == 2) {
+          if (!ovw) {
+#pragma unroll
+            for (int u = 0; u < B; ++u)
+              if (2 * (i + u) < left) v[u] += to_f<D>(o[2 * u * ld]);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < B; ++u)
+          if (2 * (i + u) < left) {
+            if constexpr (sizeof(D) == 2) o[2 * u * ld] = from_f<D>(v[u]);
+            else if (ovw) o[2 * u * ld] = v[u];
+            else atomicAdd(o + 2 * u * ld, v[u]);
+          }
+        o += 2 * B * ld;
+      }
+    }
+    return;
+  }
+  const int c4 = (lane & 3) * 4;  // this lane's columns of a block, and its first row
+  const int r0 = lane >> 2;
+  // 16-bit values of a block, read while the block before is written
+  auto read = [&](int j, uint2 (&o)[4]) {
+    if constexpr (sizeof(D) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 8 * i, c = 16 * j + c4;
+        o[i] = make_uint2(0u, 0u);
+        if (!ovw && r < rows) {
+          const D* p = dst + r * ld + c;
+          if (c + 4 <= cols) {
+            o[i] = *(const uint2*)p;
+          } else {
+            const uint16_t* u = (const uint16_t*)p;
+            if (c < cols) o[i].x = u[0];
+            if (c + 1 < cols) o[i].x |= (uint32_t)u[1] << 16;
+            if (c + 2 < cols) o[i].y = u[2];
+          }
+        }
+      }
+    }
+  };
+  uint2 next[4];
+  read(0, next);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (16 * j >= cols) break;
+    uint2 old[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) old[i] = next[i];
+    if (j < 7) read(j + 1, next);
+    put(j);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = r0 + 8 * i, c = 16 * j + c4;
@@ -182,7 +234,7 @@ __device__ __forceinline__ void emit(D* dst, int64_t ld, int rows, int cols, boo
       if (r < rows) {
         D* p = dst + r * ld + c;
         if constexpr (sizeof(D) == 4) {
-          if (vec && c + 4 <= cols) {
+          if (c + 4 <= cols) {
             if (ovw)
               *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
             else
@@ -198,9 +250,10 @@ __device__ __forceinline__ void emit(D* dst, int64_t ld, int rows, int cols, boo
               }
           }
         } else {
+          const D* h0 = (const D*)&old[i];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] += old[i][e];
-          if (vec && c + 4 <= cols) {
+          for (int e = 0; e < 4; ++e) v[e] += to_f<D>(h0[e]);
+          if (c + 4 <= cols) {
             uint2 u;
             D* h = (D*)&u;
 #pragma unroll
@@ -473,11 +526,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int row = (int)rank * 128 + quad * 32, col = h * 128;  // within the tile
       if (it.part >= 0) {
         const int64_t slot = (int64_t)(it.tile - p.whole) * p.S + it.part;
-        emit<float>(p.part + slot * TILE * TILE + row * TILE + col, TILE, 32, 128, true, true, acc, stage, lane);
+        emit<float, true>(p.part + slot * TILE * TILE + row * TILE + col, TILE, 32, 128, true, acc, stage, lane);
       } else {
         const int64_t n = (int64_t)(it.tile / p.tk) * TILE + row, k = (int64_t)(it.tile % p.tk) * TILE + col;
-        emit<D>((D*)p.d.dW + n * p.d.lddW + k, p.d.lddW, (int)min(p.d.N - n, (int64_t)32), (int)min(p.d.K - k, (int64_t)128),
-                p.vec, p.d.ovw, acc, stage, lane);
+        D* dst = (D*)p.d.dW + n * p.d.lddW + k;
+        const int rows = (int)min(p.d.N - n, (int64_t)32), cols = (int)min(p.d.K - k, (int64_t)128);
+        if (p.d.ovw) emit<D, true>(dst, p.d.lddW, rows, cols, p.vec, acc, stage, lane);
+        else emit<D, false>(dst, p.d.lddW, rows, cols, p.vec, acc, stage, lane);
       }
     }
   }
@@ -700,7 +755,7 @@ cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int
   p.timeout_ns = timeout_ns;
   p.stall = stall;
   const int wsz = dtype_size(wdt);
-  p.vec = rows16(a.dW, a.lddW, wsz);
+  p.vec = rows_by(a.dW, a.lddW, wsz, 4 * (size_t)wsz);
   cudaError_t e = cudaSuccess;
 
   const void* dy = a.dy;

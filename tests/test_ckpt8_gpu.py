@@ -81,7 +81,8 @@ DW = [(1, 1, 1, "f32", "f32"), (1, 8, 16, "bf16", "f32"), (1, 300, 520, "bf16", 
       (64, 256, 256, "bf16", "f32"), (65, 264, 272, "bf16", "f32"), (200, 257, 133, "bf16", "f32"),
       (130, 520, 1336, "f16", "f16"), (1000, 136, 400, "f32", "f32"), (777, 72, 2000, "bf16", "bf16"),
       (2049, 512, 640, "bf16", "f32"), (5000, 256, 384, "bf16", "f32"), (4100, 264, 300, "f16", "f32"),
-      (300, 1030, 90, "f32", "f32"), (129, 2000, 31, "f16", "f32")]
+      (300, 1030, 90, "f32", "f32"), (129, 2000, 31, "f16", "f32"),
+      (40, 300, 261, "bf16", "bf16"), (40, 300, 260, "f16", "f16"), (33, 270, 262, "bf16", "bf16"), (2, 257, 519, "f16", "f32")]
 
 
 @pytest.mark.parametrize("M,N,K,dt,wdt", DW)
@@ -131,6 +132,29 @@ def test_dw_strides(dt, extra, offset):
     ref = np64(dy).T @ x
     close(dW, ref, _dw_bound(np64(dy), x, M, dt, "f32", ref, 0 * ref, False))
     close(want, ref, _dw_bound(np64(dy), x, M, dt, "f32", ref, 0 * ref, False))
+
+
+@pytest.mark.parametrize("M", [20, 3000])
+@pytest.mark.parametrize("K,extra,offset", [(134, 2, 0), (133, 3, 4), (135, 1, 1), (390, 0, 0)])
+@pytest.mark.parametrize("wdt", ["bf16", "f32"])
+@pytest.mark.parametrize("accumulate", [True, False])
+def test_dw_last_columns(M, K, extra, offset, wdt, accumulate):
+    """Rows whose pitch allows wide accesses and whose last columns do not, and the reverse; the
+    elements between the rows stay as they were."""
+    N = 270
+    g = torch.Generator().manual_seed(M + K)
+    dy = (torch.randn(M, N, generator=g) * 0.3).to(DT["bf16"])
+    p = flce.ckpt8_pack(_rows(M, K, "bf16", K, 1.0).cuda())
+    x = np64(p["q"]) * oo.spread(np64(p["scale"]), K)
+    flat = torch.randn(N * (K + extra) + offset, generator=g).to(DT[wdt]).cuda()
+    keep = flat.clone()
+    dW = flat[offset:].view(N, K + extra)[:, :K]
+    init = np64(dW) if accumulate else 0 * np64(dW)
+    flce.ckpt8_dw(dy.cuda(), p["q"], p["scale"], dW=dW, flags=0 if accumulate else flce.FLAG_DW_OVERWRITE)
+    ref = init + np64(dy).T @ x
+    close(dW, ref, _dw_bound(np64(dy), x, M, "bf16", wdt, ref, init, accumulate))
+    between = flat[offset:].view(N, K + extra)[:, K:]
+    assert torch.equal(between, keep[offset:].view(N, K + extra)[:, K:]) and torch.equal(flat[:offset], keep[:offset])
 
 
 def test_dw_scales_that_are_no_powers_of_two():
