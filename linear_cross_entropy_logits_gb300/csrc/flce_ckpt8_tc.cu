@@ -20,7 +20,7 @@
 // 8192 values takes about 230 instructions of each scheduler, and reading and writing them in
 // shared memory 24 KB beside the 56 KB of the copies and the MMAs' operands: together as much as
 // its 128 bytes a cycle carry in 640. Three groups of four warps take the steps in turn.
-// 4096 x 4096 over 8192 rows, bf16 into fp32: 204 us (1345 TFLOP/s; two groups 208, without the
+// 4096 x 4096 over 8192 rows, bf16 into fp32: 201 us (1370 TFLOP/s; two groups 208, without the
 // expansion's reads, arithmetic and writes 173, a library bf16 product of the expanded operand
 // 156). What bounds it is the expansion sharing shared memory and issue slots with the rest.
 // The tensor cores truncate when they add to an accumulator; over M rows that adds up to an
@@ -57,7 +57,8 @@ constexpr int STAGE_BYTES = A_BYTES + Q_BYTES;
 constexpr int SLOTS = 4;                  // of expanded q
 constexpr int OFF_B = STAGES * STAGE_BYTES;
 constexpr int OFF_S = OFF_B + SLOTS * B_BYTES;
-constexpr int OUT_BYTES = 32 * 16 * 4;     // 16 columns of an output warp's 32 rows
+constexpr int OUT_ROW = 64;               // bytes of a row that an output warp writes at a time
+constexpr int OUT_BYTES = 32 * OUT_ROW;
 constexpr int OFF_OUT = OFF_S + STAGES * S_BYTES;
 constexpr int OFF_BARS = OFF_OUT + 8 * OUT_BYTES;
 constexpr int BOX = 64 * 64 * 2;          // one 64 x 64 MN-major box
@@ -128,32 +129,118 @@ __device__ __forceinline__ uint2 expand4(uint32_t u, f2 sc2) {
   return make_uint2(o[0], o[1]);
 }
 
-// A warp's 32 rows x 128 columns of sums (lane = row) to a matrix: dst, its element (0, 0) of them,
-// of which `rows` x `cols` exist, = acc (ovw) or += acc. fp32 is added by L2 (one add an element:
-// nothing to wait for, and the same bits on every run); 16-bit values are read, so that they are
-// rounded once, each block of 16 columns while the one before is written (500 x 4096 x 4096 bf16:
-// 53 us, 64 without). 16 columns at a time pass through shared memory (16-byte chunk c of row r at
-// c ^ (r / 2 % 4): free of bank conflicts both ways), so that a store covers 64 bytes of each of 8
-// rows: stored a row per lane, 16 bytes of 32 rows at a time, the rows' pitch puts most of a warp's
-// accesses on few L2 slices (28 tiles of 256 x 256 at a pitch of 16 KB took 77 us). vec: rows allow
-// accesses of four elements.
-template <typename D, bool ovw>
-__device__ __forceinline__ void emit(D* dst, int64_t ld, int rows, int cols, bool vec, const float (&acc)[128],
-                                     uint32_t stage, int lane) {
-  const uint32_t wr = stage + (uint32_t)lane * 64;
-  const int sw = (lane >> 1) & 3;
-  auto put = [&](int j) {
-    __syncwarp();  // the block before has been read
+// A warp's 32 rows x 128 columns of sums (lane = row) and where they go in a matrix. fp32 is added
+// by L2 (one add an element: nothing to wait for, and the same bits on every run). 16-bit values are
+// rounded once: the sums start from them (start), so that their reads overlap the first MMAs (512 x
+// 4096 x 4096 bf16 43 us; read beside the writes 52, through shared memory 45 to 52). The sums pass
+// through shared memory, 64 bytes of each row at a time, so that a store covers 64 bytes of each of
+// 8 rows: stored a row per lane, 16 bytes of 32 rows at a time, the rows' pitch puts most of a
+// warp's accesses on few L2 slices (28 tiles of 256 x 256 at a pitch of 16 KB took 77 us). With 128
+// bytes at a time 16-bit values are 8 percent faster, fp32 the same, but the shared memory for it
+// costs a stage of the copies: 10 us of the 201 over 8192 rows.
+template <typename D>
+struct Out {
+  D* dst;        // the warp's element (0, 0)
+  int64_t ld;
+  int rows, cols;  // that exist, of 32 x 128
+  uint32_t stage;  // the warp's shared memory: 32 rows of OUT_ROW bytes, 16-byte chunks permuted
+  static constexpr int PER = 16 / sizeof(D);  // elements a chunk
+  static constexpr int CH = OUT_ROW / 16;     // chunks of a row
+  static constexpr int LR = 32 / CH;          // rows a warp covers at a time
+  static constexpr int BLOCK = CH * PER;      // columns at a time
+
+  // chunk c of row r: free of bank conflicts with a lane per row and with lanes along a row
+  __device__ __forceinline__ uint32_t chunk(int r, int c) const {
+    return stage + (uint32_t)(r * OUT_ROW + ((c ^ ((r >> 1) & 3)) << 4));
+  }
+  // acc = the 16-bit values that the sums are added to (each lane its row's), zero outside.
+  __device__ __forceinline__ void start(float (&acc)[128], int lane) const {
+    const D* p = dst + lane * ld;
+    uint4 u[16];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(wr + (uint32_t)((c ^ sw) << 4)), "f"(acc[16 * j + 4 * c]),
-                   "f"(acc[16 * j + 4 * c + 1]), "f"(acc[16 * j + 4 * c + 2]), "f"(acc[16 * j + 4 * c + 3])
-                   : "memory");
+    for (int c = 0; c < 16; ++c) {
+      u[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (lane < rows && 8 * c < cols) {
+        if (8 * c + 8 <= cols) {
+          u[c] = *(const uint4*)(p + 8 * c);
+        } else {
+          uint32_t* w = (uint32_t*)&u[c];
+#pragma unroll
+          for (int e = 0; e < 7; ++e)
+            if (8 * c + e < cols) w[e / 2] |= (uint32_t)((const uint16_t*)p)[8 * c + e] << (16 * (e & 1));
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const D* h = (const D*)&u[c];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[8 * c + e] = to_f<D>(h[e]);
+    }
+  }
+  // The matrix = acc; with !ovw and fp32, += acc.
+  template <bool ovw>
+  __device__ __forceinline__ void put(const float (&acc)[128], int lane) const {
+#pragma unroll
+    for (int j = 0; j < 128 / BLOCK; ++j) {
+      if (j * BLOCK >= cols) break;
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        uint4 u;
+        const float* v = &acc[j * BLOCK + c * PER];
+        if constexpr (sizeof(D) == 4) {
+          u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        } else {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            D* h = (D*)&o[e];
+            h[0] = from_f<D>(v[2 * e]);
+            h[1] = from_f<D>(v[2 * e + 1]);
+          }
+          u = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(lane, c)), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w)
+                     : "memory");
+      }
+      __syncwarp();
+      const int c = j * BLOCK + (lane % CH) * PER;
+      D* p = dst + lane / CH * ld + c;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int r = lane / CH + LR * i;
+        uint4 u;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(chunk(r, lane % CH)));
+        if (r < rows && c < cols) {
+          if (c + PER <= cols) {
+            if constexpr (ovw)
+              *(uint4*)p = u;
+            else
+              asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p),
+                           "f"(__uint_as_float(u.x)), "f"(__uint_as_float(u.y)), "f"(__uint_as_float(u.z)),
+                           "f"(__uint_as_float(u.w))
+                           : "memory");
+          } else {
+            const D* h = (const D*)&u;
+#pragma unroll
+            for (int e = 0; e < PER - 1; ++e)
+              if (c + e < cols) {
+                if constexpr (ovw) p[e] = h[e];
+                else atomicAdd(p + e, h[e]);
+              }
+          }
+        }
+        p += LR * ld;
+      }
+    }
     __syncwarp();
-  };
-  if (!vec) {
-    // a lane has one column of every second row, so that a store covers 16 columns of two rows
-    // (four columns a lane as below: 70 -> 42 us at 500 x 4096 x 4097)
+  }
+  // Rows without 16-byte accesses, = or += acc: 16 columns at a time, a lane one column of every
+  // second row, so that a store covers 16 columns of two rows (four columns a lane: 500 x 4096 x 4097
+  // into fp32 70 us, now 42).
+  template <bool ovw>
+  __device__ __forceinline__ void put_narrow(const float (&acc)[128], int lane) const {
     constexpr int B = ovw ? 4 : 8;  // rows at a time
     const int c = lane & 15, r0 = lane >> 4;
 #pragma unroll
@@ -161,23 +248,23 @@ __device__ __forceinline__ void emit(D* dst, int64_t ld, int rows, int cols, boo
       if (16 * j >= cols) break;
       const int left = 16 * j + c < cols ? rows - r0 : 0;  // rows from r0 on
       D* o = dst + r0 * ld + 16 * j + c;
-      put(j);
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(lane, e)), "f"(acc[16 * j + 4 * e]),
+                     "f"(acc[16 * j + 4 * e + 1]), "f"(acc[16 * j + 4 * e + 2]), "f"(acc[16 * j + 4 * e + 3])
+                     : "memory");
+      __syncwarp();
 #pragma unroll 1
       for (int i = 0; i < 16; i += B) {
         float v[B];
 #pragma unroll
-        for (int u = 0; u < B; ++u) {
-          const int r = r0 + 2 * (i + u);
-          asm volatile("ld.shared.f32 %0, [%1];"
-                       : "=f"(v[u])
-                       : "r"(stage + (uint32_t)(r * 64 + (((c >> 2) ^ ((r >> 1) & 3)) << 4) + (c & 3) * 4)));
-        }
-        if constexpr (sizeof(D) == 2) {
-          if (!ovw) {
+        for (int u = 0; u < B; ++u)
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[u]) : "r"(chunk(r0 + 2 * (i + u), c >> 2) + (c & 3) * 4));
+        if constexpr (sizeof(D) == 2 && !ovw) {
 #pragma unroll
-            for (int u = 0; u < B; ++u)
-              if (2 * (i + u) < left) v[u] += to_f<D>(o[2 * u * ld]);
-          }
+          for (int u = 0; u < B; ++u)
+            if (2 * (i + u) < left) v[u] += to_f<D>(o[2 * u * ld]);
         }
 #pragma unroll
         for (int u = 0; u < B; ++u)
@@ -189,86 +276,9 @@ __device__ __forceinline__ void emit(D* dst, int64_t ld, int rows, int cols, boo
         o += 2 * B * ld;
       }
     }
-    return;
+    __syncwarp();
   }
-  const int c4 = (lane & 3) * 4;  // this lane's columns of a block, and its first row
-  const int r0 = lane >> 2;
-  // 16-bit values of a block, read while the block before is written
-  auto read = [&](int j, uint2 (&o)[4]) {
-    if constexpr (sizeof(D) == 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 8 * i, c = 16 * j + c4;
-        o[i] = make_uint2(0u, 0u);
-        if (!ovw && r < rows) {
-          const D* p = dst + r * ld + c;
-          if (c + 4 <= cols) {
-            o[i] = *(const uint2*)p;
-          } else {
-            const uint16_t* u = (const uint16_t*)p;
-            if (c < cols) o[i].x = u[0];
-            if (c + 1 < cols) o[i].x |= (uint32_t)u[1] << 16;
-            if (c + 2 < cols) o[i].y = u[2];
-          }
-        }
-      }
-    }
-  };
-  uint2 next[4];
-  read(0, next);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (16 * j >= cols) break;
-    uint2 old[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) old[i] = next[i];
-    if (j < 7) read(j + 1, next);
-    put(j);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + 8 * i, c = 16 * j + c4;
-      float v[4];
-      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-                   : "r"(stage + (uint32_t)(r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4))));
-      if (r < rows) {
-        D* p = dst + r * ld + c;
-        if constexpr (sizeof(D) == 4) {
-          if (c + 4 <= cols) {
-            if (ovw)
-              *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
-            else
-              asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v[0]), "f"(v[1]),
-                           "f"(v[2]), "f"(v[3])
-                           : "memory");
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (c + e < cols) {
-                if (ovw) p[e] = v[e];
-                else atomicAdd(p + e, v[e]);
-              }
-          }
-        } else {
-          const D* h0 = (const D*)&old[i];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] += to_f<D>(h0[e]);
-          if (c + 4 <= cols) {
-            uint2 u;
-            D* h = (D*)&u;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = from_f<D>(v[e]);
-            *(uint2*)p = u;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (c + e < cols) p[e] = from_f<D>(v[e]);
-          }
-        }
-      }
-    }
-  }
-}
+};
 
 template <typename T, typename D>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -503,9 +513,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     Item it;
     for (int i = pair; ok && get_item(p, i, it); i += npairs) {
+      const int row = (int)rank * 128 + quad * 32, col = h * 128;  // within the tile
+      const int64_t n = (int64_t)(it.tile / p.tk) * TILE + row, k = (int64_t)(it.tile % p.tk) * TILE + col;
+      const Out<D> out{(D*)p.d.dW + n * p.d.lddW + k, p.d.lddW, (int)min(p.d.N - n, (int64_t)32),
+                       (int)min(p.d.K - k, (int64_t)128), stage};
       float acc[128];
+      if (sizeof(D) == 2 && it.part < 0 && p.vec && !p.d.ovw) {
+        out.start(acc, lane);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+        for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+      }
       for (int st = it.s0; st < it.s1; st += p.seg, ++g) {
         const int as = g & 1;
         ok = __all_sync(0xffffffffu, bar_wait(tfull(as), (uint32_t)(g >> 1) & 1u, ab, true));
@@ -523,16 +541,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) bar_arrive(mapa(tempty(as), 0));
       }
       if (!ok) break;
-      const int row = (int)rank * 128 + quad * 32, col = h * 128;  // within the tile
       if (it.part >= 0) {
         const int64_t slot = (int64_t)(it.tile - p.whole) * p.S + it.part;
-        emit<float, true>(p.part + slot * TILE * TILE + row * TILE + col, TILE, 32, 128, true, acc, stage, lane);
+        const Out<float> part{p.part + slot * TILE * TILE + row * TILE + col, TILE, 32, 128, stage};
+        part.put<true>(acc, lane);
+      } else if (p.vec) {
+        if constexpr (sizeof(D) == 4) {
+          if (p.d.ovw) out.template put<true>(acc, lane);
+          else out.template put<false>(acc, lane);
+        } else {
+          out.template put<true>(acc, lane);  // (with !ovw acc has the old values)
+        }
       } else {
-        const int64_t n = (int64_t)(it.tile / p.tk) * TILE + row, k = (int64_t)(it.tile % p.tk) * TILE + col;
-        D* dst = (D*)p.d.dW + n * p.d.lddW + k;
-        const int rows = (int)min(p.d.N - n, (int64_t)32), cols = (int)min(p.d.K - k, (int64_t)128);
-        if (p.d.ovw) emit<D, true>(dst, p.d.lddW, rows, cols, p.vec, acc, stage, lane);
-        else emit<D, false>(dst, p.d.lddW, rows, cols, p.vec, acc, stage, lane);
+        if (p.d.ovw) out.template put_narrow<true>(acc, lane);
+        else out.template put_narrow<false>(acc, lane);
       }
     }
   }
@@ -755,7 +777,7 @@ cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int
   p.timeout_ns = timeout_ns;
   p.stall = stall;
   const int wsz = dtype_size(wdt);
-  p.vec = rows_by(a.dW, a.lddW, wsz, 4 * (size_t)wsz);
+  p.vec = rows16(a.dW, a.lddW, wsz);
   cudaError_t e = cudaSuccess;
 
   const void* dy = a.dy;
