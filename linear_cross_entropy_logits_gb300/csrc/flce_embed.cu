@@ -21,29 +21,33 @@ namespace flce {
 namespace {
 
 // ------------------------------------------------------------------ forward
-// Block (x, y): row x, vectors y * U * threads ... of it; each thread moves U vectors.
-constexpr int FWD_U = 2;
+// Block (x, y): row x, vectors y * U * threads ... of it; each thread moves U vectors. Narrow
+// accesses are bound by the instructions around them: eight a thread share the row's.
+template <int EPV>
+constexpr int FWD_U = EPV <= 2 ? 8 : 2;
 template <typename T, int EPV>
 __global__ void __launch_bounds__(256) k_embed_fwd(const int64_t* __restrict__ tokens, int64_t V, int64_t H,
                                                    int64_t ignore_index, float scale, const T* __restrict__ E,
                                                    int64_t ldE, T* __restrict__ out, int64_t ldout, int* status) {
+  constexpr int U = FWD_U<EPV>;
   const int64_t row = blockIdx.x;
   const int64_t t = tokens[row];
   const bool live = t >= 0 && t < V && t != ignore_index;
   if (!live && t != ignore_index && status != nullptr && threadIdx.x == 0 && blockIdx.y == 0)
     atomicOr(status, ST_TARGET_RANGE);
-  const int64_t v0 = (int64_t)blockIdx.y * FWD_U * blockDim.x + threadIdx.x;
-  Raw<T, EPV> r[FWD_U];
+  const int64_t c0 = ((int64_t)blockIdx.y * U * blockDim.x + threadIdx.x) * EPV;
+  const int left = (int)min(H - c0, (int64_t)INT32_MAX), step = (int)blockDim.x * EPV;
+  const T* src = E + (live ? t : 0) * ldE + c0;
+  T* dst = out + row * ldout + c0;
+  Raw<T, EPV> r[U];
 #pragma unroll
-  for (int u = 0; u < FWD_U; ++u) {
-    const int64_t c = (v0 + u * blockDim.x) * EPV;
+  for (int u = 0; u < U; ++u) {
     r[u].zero();
-    if (live && c < H) r[u].load(E + t * ldE + c);
+    if (live && u * step < left) r[u].load(src + u * step);
   }
 #pragma unroll
-  for (int u = 0; u < FWD_U; ++u) {
-    const int64_t c = (v0 + u * blockDim.x) * EPV;
-    if (c >= H) continue;
+  for (int u = 0; u < U; ++u) {
+    if (u * step >= left) break;
     if (live && scale != 1.0f) {
       float v[EPV];
       r[u].unpack(v);
@@ -51,16 +55,17 @@ __global__ void __launch_bounds__(256) k_embed_fwd(const int64_t* __restrict__ t
       for (int e = 0; e < EPV; ++e) v[e] *= scale;
       r[u].pack(v);
     }
-    r[u].store(out + row * ldout + c);
+    r[u].store(dst + u * step);
   }
 }
 
 template <typename T, int EPV>
 void launch_fwd(const flce_embed_args& a, cudaStream_t s) {
-  // as many blocks a row as 256 threads of FWD_U vectors need, of as few threads as that takes
+  // as many blocks a row as 256 threads of U vectors need, of as few threads as that takes
+  constexpr int U = FWD_U<EPV>;
   const int64_t nvec = cdiv64(a.H, EPV);
-  const int64_t by = cdiv64(nvec, 256 * FWD_U);
-  const int threads = (int)(cdiv64(cdiv64(nvec, by * FWD_U), 32) * 32);
+  const int64_t by = cdiv64(nvec, 256 * U);
+  const int threads = (int)(cdiv64(cdiv64(nvec, by * U), 32) * 32);
   k_embed_fwd<T, EPV><<<dim3((unsigned)a.N, (unsigned)by), threads, 0, s>>>(
       a.tokens, a.V, a.H, a.ignore_index, a.scale, (const T*)a.E, a.ldE, (T*)a.out, a.ldout, a.status);
 }
@@ -74,6 +79,7 @@ cudaError_t fwd(const flce_embed_args& a, cudaStream_t s) {
   };
   if (fits(32)) launch_fwd<T, 2 * W>(a, s);
   else if (fits(16)) launch_fwd<T, W>(a, s);
+  else if (sizeof(T) == 2 && fits(4)) launch_fwd<T, 4 / sizeof(T)>(a, s);
   else launch_fwd<T, 1>(a, s);
   return cudaGetLastError();
 }
@@ -661,6 +667,9 @@ cudaError_t sums(SumArgs a, int epv, int threads, cudaStream_t s) {
   constexpr int W = 16 / sizeof(T);
   const unsigned blocks = (unsigned)(a.pieces * a.slices);
   if (epv == W) return launch_after(k_embed_sum<T, D, W>, blocks, threads, 0, s, a);
+  if constexpr (sizeof(T) == 2) {
+    if (epv == 2) return launch_after(k_embed_sum<T, D, 2>, blocks, threads, 0, s, a);
+  }
   return launch_after(k_embed_sum<T, D, 1>, blocks, threads, 0, s, a);
 }
 
@@ -742,9 +751,11 @@ extern "C" int32_t flce_embed_bwd(const flce_embed_args* x, void* stream) {
   a.part = (float*)(ws + l.part);
   a.count = (int*)(ws + l.count);
   const int wide = 16 / esz;
-  const bool fits = x->H % wide == 0 && rows16(x->dout, x->lddout, esz) &&
-                    rows_by(x->dE, x->lddE, dsz, (size_t)(wide * dsz > 32 ? 32 : wide * dsz));
-  const int epv = fits ? wide : 1;
+  auto fits = [&](int v) {
+    return x->H % v == 0 && rows_by(x->dout, x->lddout, esz, (size_t)(v * esz)) &&
+           rows_by(x->dE, x->lddE, dsz, (size_t)(v * dsz > 32 ? 32 : v * dsz));
+  };
+  const int epv = fits(wide) ? wide : esz == 2 && fits(2) ? 2 : 1;
   int threads;
   sum_shape(x->H, epv, threads, a.slices);
 

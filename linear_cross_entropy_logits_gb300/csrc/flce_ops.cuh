@@ -45,12 +45,13 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 // In the second: the first has finished and its writes are visible.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// EPV consecutive elements of a row as they lie in memory: 32 or 16 bytes in one access, or a
-// single element (EPV == 1).
+// EPV consecutive elements of a row as they lie in memory: 32, 16, 8 or 4 bytes in one access,
+// or a single element (EPV == 1).
 template <typename T, int EPV>
 struct Raw {
   static constexpr int BYTES = EPV * (int)sizeof(T);
-  static_assert(EPV == 1 || BYTES == 32 || BYTES == 16, "vector width");
+  static_assert(EPV == 1 || BYTES == 32 || BYTES == 16 || BYTES == 8 || BYTES == 4,
+                "vector width");
   static constexpr int W = EPV == 1 ? 1 : BYTES / 4;
   uint32_t w[W];
 
@@ -67,6 +68,12 @@ struct Raw {
                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                    : "l"(p)
                    : "memory");
+    } else if constexpr (BYTES == 4) {
+      w[0] = *(const uint32_t*)p;
+    } else if constexpr (BYTES == 8) {
+      const uint2 u = *(const uint2*)p;
+      w[0] = u.x;
+      w[1] = u.y;
     } else {
       const uint4 u = *(const uint4*)p;
       w[0] = u.x;
@@ -83,6 +90,10 @@ struct Raw {
       asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                    "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                    : "memory");
+    } else if constexpr (BYTES == 4) {
+      *(uint32_t*)p = w[0];
+    } else if constexpr (BYTES == 8) {
+      *(uint2*)p = make_uint2(w[0], w[1]);
     } else {
       *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
     }
