@@ -5,7 +5,8 @@
 //   dW[n, k] += sum_m dy[m, n] q[m, k] s[m, k / 128]
 //
 // Packing is bound by HBM: 2 bytes read and 1.03 written per 16-bit element. 16384 x 4096 bf16 in
-// 32 us (5.3 TB/s in DRAM under ncu; floor 30).
+// 32 us (5.3 TB/s in DRAM under ncu; floor 30). Rows of even length that allow no 16-byte accesses go
+// in pairs of elements (4097 x 5122 bf16 20 us, singly 28).
 #include <math.h>
 
 #include "flce_ckpt8.cuh"
@@ -54,6 +55,7 @@ cudaError_t pack(const flce_ckpt8_args& a, cudaStream_t s) {
   };
   if (fits(32)) launch_pack<T, 2 * W, 2>(a, s);
   else if (fits(16)) launch_pack<T, W, 2>(a, s);
+  else if (fits(2 * sizeof(T))) launch_pack<T, 2, 4>(a, s);
   else launch_pack<T, 1, 4>(a, s);
   return cudaGetLastError();
 }

@@ -9,8 +9,8 @@
 // columns and the outputs, so nothing is read twice. Rows too long for the registers
 // (k_rms_fwd_long / k_rms_bwd_long) are read twice, the second time mostly from L2.
 //
-// Accesses are 32 bytes a thread where every operand's rows allow it, else 16, else single
-// elements: 8192 x 4096 bf16 with residual, 16-bit and 8-bit output and 8-bit checkpoint in
+// Accesses are 32 bytes a thread where every operand's rows allow it, else 16, else two elements,
+// else one: 8192 x 4096 bf16 with residual, 16-bit and 8-bit output and 8-bit checkpoint in
 // 55 us (5.0 TB/s in DRAM under ncu; floor 50) against 68 with 16 bytes and a test for
 // infinities per element. Backward of the same shape from the checkpoint, with the residual's
 // gradient: 46 + 6 us (floor 35).
@@ -67,7 +67,7 @@ __device__ __forceinline__ float group_sum(float v, float* red, int wpr, int war
 }
 
 template <typename T, int EPV, int NV>
-__global__ void __launch_bounds__(EPV == 1 ? 1024 : 512) k_rms_fwd(const __grid_constant__ FwdArgs a, int wpr) {
+__global__ void __launch_bounds__(EPV <= 2 ? 1024 : 512) k_rms_fwd(const __grid_constant__ FwdArgs a, int wpr) {
   __shared__ float red[MAX_WARPS];
   const int lane = threadIdx.x & 31, wb = threadIdx.x >> 5;
   const int group = wb / wpr, w = wb - group * wpr;
@@ -401,12 +401,12 @@ __global__ void __launch_bounds__(512, 1) k_rms_bwd_ring(const __grid_constant__
 // Backward of other rows (longer, or without 16-byte accesses): a row group walks the rows group,
 // group + groups, ...; its threads keep their columns' dweight sums in registers. All of a row is
 // loaded before its sum is taken. At the end the block's groups add their sums in group order and
-// write one row of a.part. Single elements are bound by the instructions they take: eight a
-// thread, 64 registers and all 32 warps' worth an SM (20762 x 1167 bf16 65 us; 4097 x 5121 67 us,
-// 127 with sixteen a thread).
+// write one row of a.part. Accesses of one or two elements are bound by the instructions they take:
+// eight elements a thread, 64 registers and all 32 warps' worth an SM (4097 x 5122 bf16 in pairs
+// 60 us, singly 67, singly with sixteen a thread 127).
 template <typename T, int EPV, int NV, bool Q8>
-__global__ void __launch_bounds__(EPV == 1 ? 1024 : 512, 1) k_rms_bwd(const __grid_constant__ BwdArgs a, int wpr) {
-  constexpr int JB = EPV == 1 ? 4 : 1;  // a thread's vectors that share an 8-bit row's scale
+__global__ void __launch_bounds__(EPV <= 2 ? 1024 : 512, 1) k_rms_bwd(const __grid_constant__ BwdArgs a, int wpr) {
+  constexpr int JB = Q_VECTORS<EPV>;  // a thread's vectors that share an 8-bit row's scale
   __shared__ float red[2][MAX_WARPS];
   extern __shared__ float sums[];  // [H] where the block has several groups
   let_next_start();
@@ -554,18 +554,18 @@ __global__ void __launch_bounds__(1024) k_rms_dw_sum(const float* part, int64_t 
 constexpr int BWD_BLOCKS_PER_SM = 2;
 constexpr int LONG_DW_ROWS = 64;  // row groups of k_rms_dw_long
 
-// Rows that take 32-byte, 16-byte or single-element accesses.
-enum Width { W32, W16, W1 };
+// Rows that take accesses of 32 bytes, 16 bytes, two elements or one.
+enum Width { W32, W16, W2, W1 };
 
 // Warps per row and vectors per thread of a row of H elements in vectors of EPV: the fewest
-// warps with 16 elements a thread, else 16 warps with 32 (single elements: up to 32 warps with
-// 8); 0 when none holds it.
+// warps with 16 elements a thread, else 16 warps with 32 (one or two elements an access: up to
+// 32 warps with 8); 0 when none holds it.
 struct Shape {
   int wpr, nv;
 };
 Shape row_shape(int64_t H, int epv) {
   const int64_t nvec = cdiv64(H, epv);
-  if (epv == 1) return {nvec <= 32 * 32 * 8 ? (int)cdiv64(nvec, 32 * 8) : 0, 8};
+  if (epv <= 2) return {H <= 32 * 32 * 8 ? (int)cdiv64(H, 32 * 8) : 0, 8 / epv};
   const int small = 16 / epv, large = 2 * small;
   if (cdiv64(nvec, 32 * small) <= 16) return {(int)cdiv64(nvec, 32 * small), small};
   if (cdiv64(nvec, 32 * large) <= 16) return {16, large};
@@ -580,7 +580,7 @@ int64_t partial_rows() {
 
 template <typename T, int EPV>
 cudaError_t fwd_w(const FwdArgs& a, cudaStream_t s) {
-  constexpr int NV = EPV == 1 ? 8 : 16 / EPV;
+  constexpr int NV = (EPV <= 2 ? 8 : 16) / EPV;
   const Shape p = row_shape(a.H, EPV);
   if (p.wpr == 0) {
     k_rms_fwd_long<T><<<(unsigned)a.N, 512, 0, s>>>(a);
@@ -589,14 +589,19 @@ cudaError_t fwd_w(const FwdArgs& a, cudaStream_t s) {
     const unsigned blocks = (unsigned)cdiv64(a.N, rpb);
     const int threads = (int)rpb * p.wpr * 32;
     if (p.nv == NV) k_rms_fwd<T, EPV, NV><<<blocks, threads, 0, s>>>(a, p.wpr);
-    else if constexpr (EPV > 1) k_rms_fwd<T, EPV, 2 * NV><<<blocks, threads, 0, s>>>(a, p.wpr);
+    else if constexpr (EPV > 2) k_rms_fwd<T, EPV, 2 * NV><<<blocks, threads, 0, s>>>(a, p.wpr);
   }
   return cudaGetLastError();
 }
 template <typename T>
 cudaError_t fwd(const FwdArgs& a, Width w, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
-  return w == W32 ? fwd_w<T, 2 * E>(a, s) : w == W16 ? fwd_w<T, E>(a, s) : fwd_w<T, 1>(a, s);
+  switch (w) {
+    case W32: return fwd_w<T, 2 * E>(a, s);
+    case W16: return fwd_w<T, E>(a, s);
+    case W2: return fwd_w<T, 2>(a, s);
+    default: return fwd_w<T, 1>(a, s);
+  }
 }
 
 template <typename T, int EPV, int NV>
@@ -604,7 +609,7 @@ int64_t launch_bwd(const BwdArgs& a, int wpr, cudaStream_t s) {
   const int64_t rpb = wpr > 16 ? 1 : 16 / wpr;
   const int threads = (int)rpb * wpr * 32;
   const size_t smem = rpb > 1 ? (size_t)a.H * 4 : 0;
-  int64_t blocks = (int64_t)num_sms() * (EPV == 1 && wpr <= 16 ? BWD_BLOCKS_PER_SM : 1);
+  int64_t blocks = (int64_t)num_sms() * (EPV <= 2 && wpr <= 16 ? BWD_BLOCKS_PER_SM : 1);
   if (blocks > cdiv64(a.N, rpb)) blocks = cdiv64(a.N, rpb);
   if (a.h8 != nullptr) k_rms_bwd<T, EPV, NV, true><<<(unsigned)blocks, threads, smem, s>>>(a, wpr);
   else k_rms_bwd<T, EPV, NV, false><<<(unsigned)blocks, threads, smem, s>>>(a, wpr);
@@ -612,7 +617,7 @@ int64_t launch_bwd(const BwdArgs& a, int wpr, cudaStream_t s) {
 }
 template <typename T, int EPV>
 cudaError_t bwd_w(const BwdArgs& a, int64_t& part_rows, cudaStream_t s) {
-  constexpr int NV = EPV == 1 ? 8 : 16 / EPV;
+  constexpr int NV = (EPV <= 2 ? 8 : 16) / EPV;
   const Shape p = row_shape(a.H, EPV);
   if (p.wpr == 0) {
     if (a.dx != nullptr) k_rms_bwd_long<T><<<(unsigned)a.N, 512, 0, s>>>(a);
@@ -622,7 +627,7 @@ cudaError_t bwd_w(const BwdArgs& a, int64_t& part_rows, cudaStream_t s) {
     }
   } else {
     // (rows in wider accesses come here with 32 elements a thread only)
-    part_rows = launch_bwd<T, EPV, EPV == 1 ? NV : 2 * NV>(a, p.wpr, s);
+    part_rows = launch_bwd<T, EPV, EPV <= 2 ? NV : 2 * NV>(a, p.wpr, s);
   }
   return cudaGetLastError();
 }
@@ -656,6 +661,7 @@ template <typename T>
 cudaError_t bwd(const BwdArgs& a, Width w, int64_t& part_rows, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
   if (w == W1) return bwd_w<T, 1>(a, part_rows, s);
+  if (w == W2) return bwd_w<T, 2>(a, part_rows, s);
   const int64_t wpr = cdiv64(a.H, 512);  // 16 elements a thread
   if (wpr <= RING_WARPS<T, 4>)
     return a.h8 ? launch_ring<T, 16 / E, true, 4>(a, (int)wpr, part_rows, s)
@@ -722,7 +728,7 @@ extern "C" int32_t flce_rmsnorm_fwd(const flce_rmsnorm_args* x, void* stream) {
            (!a.y || rows_by(a.y, a.ldy, esz, bytes)) && (!a.y8 || rows_by(a.y8, a.ldy8, 1, e)) &&
            (!a.h8 || rows_by(a.h8, a.ldh8, 1, e));
   };
-  const Width w = fits(32) ? W32 : fits(16) ? W16 : W1;
+  const Width w = fits(32) ? W32 : fits(16) ? W16 : fits(2 * esz) ? W2 : W1;
   cudaStream_t s = (cudaStream_t)stream;
   switch (x->dtype) {
     case FLCE_F32: return cuda_status(fwd<float>(a, w, s));
@@ -779,11 +785,13 @@ extern "C" int32_t flce_rmsnorm_bwd(const flce_rmsnorm_bwd_args* x, void* stream
   a.dx = x->dx;
   a.lddx = x->lddx;
   a.part = x->dweight ? (float*)x->workspace : nullptr;
-  const int e16 = 16 / esz;
-  const bool wide = H % e16 == 0 && rows16(a.dy, a.lddy, esz) && (!a.h || rows16(a.h, a.ldh, esz)) &&
-                    (!a.h8 || rows_by(a.h8, a.ldh8, 1, e16)) && aligned_to(a.w, 16) &&
-                    (!a.dh || rows16(a.dh, a.lddh, esz)) && (!a.dx || rows16(a.dx, a.lddx, esz));
-  const Width w = wide ? W16 : W1;
+  auto fits = [&](int bytes) {
+    const int e = bytes / esz;
+    return H % e == 0 && rows_by(a.dy, a.lddy, esz, bytes) && (!a.h || rows_by(a.h, a.ldh, esz, bytes)) &&
+           (!a.h8 || rows_by(a.h8, a.ldh8, 1, e)) && aligned_to(a.w, bytes) &&
+           (!a.dh || rows_by(a.dh, a.lddh, esz, bytes)) && (!a.dx || rows_by(a.dx, a.lddx, esz, bytes));
+  };
+  const Width w = fits(16) ? W16 : fits(2 * esz) ? W2 : W1;
   int64_t rows = 0;
   cudaError_t e;
   switch (x->dtype) {

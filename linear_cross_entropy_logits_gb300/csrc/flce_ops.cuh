@@ -186,10 +186,11 @@ __device__ __forceinline__ int q_exponent(float amax) {
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // Two and four e4m3 values (round to nearest even; the inputs are within +-448 or NaN).
+__device__ __forceinline__ uint16_t q_pack2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
 __device__ __forceinline__ uint32_t q_pack4(float a, float b, float c, float d) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
+  return q_pack2(a, b) | ((uint32_t)q_pack2(c, d) << 16);
 }
 __device__ __forceinline__ uint8_t q_pack1(float a) {
   return (uint8_t)__nv_cvt_float_to_fp8(a, __NV_SATFINITE, __NV_E4M3);
@@ -203,7 +204,7 @@ __device__ __forceinline__ float2 q_unpack2(uint32_t u) {
 // EPV e4m3 values as they lie in memory.
 template <int EPV>
 struct RawQ {
-  static_assert(EPV == 16 || EPV == 8 || EPV == 4 || EPV == 1, "vector width");
+  static_assert(EPV == 16 || EPV == 8 || EPV == 4 || EPV == 2 || EPV == 1, "vector width");
   static constexpr int W = EPV < 4 ? 1 : EPV / 4;
   uint32_t w[W];
   __device__ __forceinline__ void load(const uint8_t* p) {
@@ -219,6 +220,8 @@ struct RawQ {
       w[1] = u.y;
     } else if constexpr (EPV == 4) {
       w[0] = *(const uint32_t*)p;
+    } else if constexpr (EPV == 2) {
+      w[0] = *(const uint16_t*)p;
     } else {
       w[0] = *p;
     }
@@ -226,6 +229,10 @@ struct RawQ {
   __device__ __forceinline__ void unpack(float (&v)[EPV]) const {
     if constexpr (EPV == 1) {
       v[0] = q_unpack2(w[0]).x;
+    } else if constexpr (EPV == 2) {
+      const float2 a = q_unpack2(w[0]);
+      v[0] = a.x;
+      v[1] = a.y;
     } else {
 #pragma unroll
       for (int i = 0; i < W; ++i) {
@@ -247,14 +254,21 @@ __device__ __forceinline__ void q_store(uint8_t* p, const float (&v)[EPV]) {
     *(uint2*)p = make_uint2(q_pack4(v[0], v[1], v[2], v[3]), q_pack4(v[4], v[5], v[6], v[7]));
   } else if constexpr (EPV == 4) {
     *(uint32_t*)p = q_pack4(v[0], v[1], v[2], v[3]);
+  } else if constexpr (EPV == 2) {
+    *(uint16_t*)p = q_pack2(v[0], v[1]);
   } else {
     *p = q_pack1(v[0]);
   }
 }
 
+// A thread's vectors in one block, where a row's vectors lie as below.
+template <int EPV>
+constexpr int Q_VECTORS = EPV >= 4 ? 1 : Q_BLOCK / (32 * EPV);
+
 // A row held by a group of warps: warp w of the group holds vectors (w * NV + j) * 32 + lane,
 // j < NV, of EPV elements each, so that every access of a warp is contiguous and a 128-column
-// block lies in 128 / EPV neighbouring lanes (EPV 16, 8, 4) or four vectors of a warp (EPV 1).
+// block lies in 128 / EPV neighbouring lanes (EPV 16, 8, 4) or two or four vectors of a warp
+// (EPV 2, 1).
 // Quantises such a row piece: block maxima of |v| by shuffles, then e4m3 values to q and one
 // scale per block (the power of two times `factor`) to s. A NaN takes no part in a maximum
 // (fmaxf) and is stored as NaN; a warp that meets an infinity makes the maxima again without
@@ -262,9 +276,9 @@ __device__ __forceinline__ void q_store(uint8_t* p, const float (&v)[EPV]) {
 template <int EPV, int NV>
 __device__ __forceinline__ void q_row_piece(const float (&v)[NV][EPV], int warp, int lane, int H, uint8_t* q,
                                             float* s, float factor) {
-  static_assert(EPV != 1 || NV % 4 == 0, "a block of single elements spans four vectors");
-  constexpr int JB = EPV == 1 ? 4 : 1;                // vectors per block
-  constexpr int LB = EPV == 1 ? 32 : Q_BLOCK / EPV;   // lanes per block
+  constexpr int JB = Q_VECTORS<EPV>;            // vectors per block
+  constexpr int LB = Q_BLOCK / (EPV * JB);      // lanes per block
+  static_assert(NV % JB == 0, "a block belongs to one warp");
 #pragma unroll
   for (int j0 = 0; j0 < NV; j0 += JB) {
     float m = 0.0f;

@@ -38,7 +38,7 @@ def _rows(N, H, dt, seed, spread=3.0):
 @pytest.mark.parametrize("N,H,dt,extra,offset", [
     (1, 1, "f32", 0, 0), (1, 128, "bf16", 0, 0), (3, 129, "f16", 0, 0), (50, 4096, "bf16", 0, 0), (7, 1336, "f16", 0, 0),
     (9, 1000, "f32", 0, 0), (5, 20001, "bf16", 0, 0), (33, 200, "bf16", 3, 1), (33, 200, "f32", 4, 4), (1000, 77, "bf16", 0, 0),
-    (16, 136, "f16", 8, 8)])
+    (16, 136, "f16", 8, 8), (65, 1166, "bf16", 0, 0), (9, 130, "f32", 2, 2), (33, 200, "f16", 2, 4), (3, 2, "f32", 0, 0)])
 def test_pack(N, H, dt, extra, offset):
     x = _rows(N, H, dt, N + H)
     o = {"q": odd_rows(N, H, torch.float8_e4m3fn, extra, offset)} if extra else None

@@ -42,7 +42,7 @@ def _sum32(x, r):
 SHAPES = [(1, 1, "f32"), (1, 4096, "bf16"), (3, 128, "bf16"), (5, 130, "f16"), (4, 127, "f32"), (33, 256, "bf16"),
           (9, 2048, "f16"), (7, 1337, "f32"), (6, 5376, "bf16"), (2, 8192, "f32"), (3, 16384, "bf16"), (5, 4099, "bf16"),
           (2, 20000, "f16"), (2, 9001, "bf16"), (70, 64, "f32"), (1000, 520, "bf16"), (3, 8191, "f16"), (2, 8193, "f32"),
-          (4, 5121, "f32")]
+          (4, 5121, "f32"), (33, 1166, "bf16"), (5, 5122, "f32"), (3, 8190, "f16"), (2, 8194, "bf16"), (70, 66, "f16")]
 
 
 @pytest.mark.parametrize("N,H,dt", SHAPES)
@@ -69,7 +69,8 @@ def test_forward(N, H, dt, residual):
     close(o["y8_scale"], want, (RSTD + F32) * want)
 
 
-@pytest.mark.parametrize("dt,H,extra,offset", [("bf16", 136, 8, 8), ("bf16", 136, 1, 3), ("f32", 64, 4, 4), ("f16", 260, 3, 0)])
+@pytest.mark.parametrize("dt,H,extra,offset", [("bf16", 136, 8, 8), ("bf16", 136, 1, 3), ("f32", 64, 4, 4), ("f16", 260, 3, 0),
+                                               ("bf16", 136, 2, 2), ("f32", 66, 2, 6)])
 def test_forward_strides_and_in_place(dt, H, extra, offset):
     N = 37
     x, r, w = _rows(N, H, dt, 5)
@@ -127,7 +128,8 @@ def test_no_rows():
 
 BWD = [(1, 1, "f32"), (1, 4096, "bf16"), (3, 130, "f16"), (65, 256, "bf16"), (200, 1337, "f32"), (17, 5376, "bf16"),
        (5, 16384, "f16"), (9, 9001, "bf16"), (4, 20000, "bf16"), (3000, 72, "bf16"), (2, 8192, "f32"), (12000, 136, "f16"),
-       (700, 8192, "f32"), (310, 6112, "f32"), (700, 5121, "bf16"), (3, 8191, "f16"), (1000, 1167, "bf16")]
+       (700, 8192, "f32"), (310, 6112, "f32"), (700, 5121, "bf16"), (3, 8191, "f16"), (1000, 1167, "bf16"),
+       (1000, 1166, "bf16"), (300, 5122, "bf16"), (40, 2050, "f32"), (9, 8194, "f16")]
 
 
 @pytest.mark.parametrize("N,H,dt", BWD)
@@ -164,7 +166,8 @@ def test_gradient(N, H, dt, q8, with_dh, same):
     assert torch.equal(b["dx"], o["dx"]) and "dweight" not in b
 
 
-@pytest.mark.parametrize("dt,H,extra,offset", [("bf16", 136, 8, 8), ("bf16", 136, 1, 3), ("f32", 67, 4, 4)])
+@pytest.mark.parametrize("dt,H,extra,offset", [("bf16", 136, 8, 8), ("bf16", 136, 1, 3), ("f32", 67, 4, 4),
+                                               ("bf16", 136, 2, 2), ("f32", 66, 2, 6)])
 def test_gradient_strides_and_in_place(dt, H, extra, offset):
     N = 300
     x, d, w = _rows(N, H, dt, 8)
