@@ -234,28 +234,46 @@ __device__ __forceinline__ void sort_prepare(const SortArgs& a, int rank) {
   for (int i = rank * SORT_THREADS + (int)threadIdx.x; i < a.ncount; i += CTAS * SORT_THREADS) a.count[i] = 0;
 }
 
-// The blocks behind those that sort: zeroes, while few SMs are busy with the list. The rows that
-// tokens point to are written again by the sums; that costs less than finding out which they are.
-// Block z of nz takes every nz-th piece of 64 KB (of a row, where rows lie apart).
-__device__ __forceinline__ void zero_rows(const SortArgs& a, int z, int nz) {
-  constexpr int64_t CHUNK = 65536;
-  const int64_t per = (a.zlen + CHUNK - 1) / CHUNK, all = a.zrows * per;
-  for (int64_t i = z; i < all; i += nz) {
-    const int64_t row = i / per, o = (i - row * per) * CHUNK;
-    uint8_t* p = a.zero + row * a.zpitch + o;
-    const int64_t len = min(CHUNK, a.zlen - o);
-    // two bytes at a time up to a 16-byte boundary, 16 bytes at a time, two bytes at a time again
-    const int64_t head = min((int64_t)((16 - (uintptr_t)p % 16) % 16), len);
-    const int64_t body = (len - head) / 16, tail = head + body * 16;
-    for (int64_t t = 2 * threadIdx.x; t < head; t += 2 * SORT_THREADS) *(uint16_t*)(p + t) = 0;
-    for (int64_t t = threadIdx.x; t < body; t += SORT_THREADS) ((uint4*)(p + head))[t] = make_uint4(0u, 0u, 0u, 0u);
-    for (int64_t t = tail + 2 * threadIdx.x; t < len; t += 2 * SORT_THREADS) *(uint16_t*)(p + t) = 0;
-  }
-}
-
 // hist, tot, wsum and the pairs held in shared memory
 constexpr size_t sort_smem(int ctas, int bits, int held) {
   return ((size_t)(SORT_WARPS + ctas) << bits) * 4 + SORT_WARPS * 4 + (size_t)held * 8;
+}
+
+// The blocks behind those that sort: zeroes, while few SMs are busy with the list. The rows that
+// tokens point to are written again by the sums; that costs less than finding out which they are.
+// Block z of nz takes every nz-th piece of 64 KB (of a row, where rows lie apart), and one thread
+// copies it from zeroed shared memory (32000 x 1003 fp16, 2999 tokens: 22 us for the call, by
+// stores of all threads 24). Two blocks an SM: with one, the clusters of eight that did not fit at
+// first left SMs idle (28 us; 128256 x 4096 fp32 361 against 546).
+constexpr int64_t ZERO_CHUNK = 65536;
+__device__ __forceinline__ void zero_rows(const SortArgs& a, int z, int nz, uint4* zeros) {
+  constexpr int ZEROS = 16384;
+  static_assert(ZEROS <= sort_smem(1, 8, 0), "the smallest launch's shared memory");
+  for (int t = threadIdx.x; t < ZEROS / 16; t += SORT_THREADS) zeros[t] = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  const uint32_t src = (uint32_t)__cvta_generic_to_shared(zeros);
+  const int64_t per = (a.zlen + ZERO_CHUNK - 1) / ZERO_CHUNK, all = a.zrows * per;
+  for (int64_t i = z; i < all; i += nz) {
+    const int64_t row = i / per, o = (i - row * per) * ZERO_CHUNK;
+    uint8_t* p = a.zero + row * a.zpitch + o;
+    const int64_t len = min(ZERO_CHUNK, a.zlen - o);
+    // two bytes at a time up to a 16-byte boundary, multiples of 16 bytes, two bytes at a time again
+    const int64_t head = min((int64_t)((16 - (uintptr_t)p % 16) % 16), len);
+    const int64_t tail = head + (len - head) / 16 * 16;
+    if (threadIdx.x == 0) {
+      for (int64_t t = head; t < tail; t += ZEROS)
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(p + t), "r"(src),
+                     "r"((uint32_t)min((int64_t)ZEROS, tail - t))
+                     : "memory");
+    }
+    for (int64_t t = 2 * threadIdx.x; t < head; t += 2 * SORT_THREADS) *(uint16_t*)(p + t) = 0;
+    for (int64_t t = tail + 2 * threadIdx.x; t < len; t += 2 * SORT_THREADS) *(uint16_t*)(p + t) = 0;
+  }
+  if (threadIdx.x == 0) {
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
 }
 
 // TILES tiles of 32 pairs per warp. Pairs past N have the largest key and stay behind the others.
@@ -264,7 +282,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) k_sort_reg(const __grid_const
   constexpr int PER = SORT_WARPS * TILES * 32;  // pairs per block
   constexpr int BINS = 1 << BITS;
   constexpr uint32_t MASK = BINS - 1;
-  extern __shared__ uint2 dyn[];
+  extern __shared__ __align__(16) uint2 dyn[];
   uint2* buf = dyn;                             // [PER]
   uint32_t* hist = (uint32_t*)(dyn + PER);      // [SORT_WARPS][BINS]
   uint32_t* tot = hist + SORT_WARPS * BINS;     // [CTAS][BINS]
@@ -274,7 +292,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) k_sort_reg(const __grid_const
   uint32_t* h = hist + warp * BINS;
   let_next_start();
   if ((int)blockIdx.x >= CTAS) {
-    zero_rows(a, (int)blockIdx.x - CTAS, (int)gridDim.x - CTAS);
+    zero_rows(a, (int)blockIdx.x - CTAS, (int)gridDim.x - CTAS, (uint4*)dyn);
     return;
   }
   uint32_t key[TILES], pos[TILES], off[TILES];
@@ -338,7 +356,7 @@ __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS
     k_sort(const __grid_constant__ SortArgs a) {
   constexpr int BINS = 1 << BITS;
   constexpr uint32_t MASK = BINS - 1;
-  extern __shared__ uint2 dyn[];
+  extern __shared__ __align__(16) uint2 dyn[];
   uint32_t* hist = (uint32_t*)dyn;              // [SORT_WARPS][BINS]
   uint32_t* tot = hist + SORT_WARPS * BINS;     // [SORT_CTAS][BINS]
   uint32_t* wsum = tot + SORT_CTAS * BINS;      // [SORT_WARPS]
@@ -347,7 +365,7 @@ __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS
   uint32_t* h = hist + warp * BINS;
   let_next_start();
   if ((int)blockIdx.x >= SORT_CTAS) {
-    zero_rows(a, (int)blockIdx.x - SORT_CTAS, (int)gridDim.x - SORT_CTAS);
+    zero_rows(a, (int)blockIdx.x - SORT_CTAS, (int)gridDim.x - SORT_CTAS, (uint4*)dyn);
     return;
   }
   sort_prepare<SORT_CTAS>(a, rank);
@@ -417,7 +435,9 @@ cudaError_t launch_cluster(K kern, int ctas, size_t smem, const SortArgs& a, cud
   attr[0].val.clusterDim.x = (unsigned)ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)(a.zrows ? (num_sms() + ctas - 1) / ctas * ctas : ctas), 1, 1);
+  int64_t blocks = ctas + a.zrows * cdiv64(a.zlen, ZERO_CHUNK);
+  if (blocks > 2 * num_sms()) blocks = 2 * num_sms();
+  cfg.gridDim = dim3((unsigned)(cdiv64(blocks, ctas) * ctas), 1, 1);
   cfg.blockDim = dim3(SORT_THREADS, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
