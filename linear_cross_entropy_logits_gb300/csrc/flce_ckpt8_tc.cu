@@ -82,7 +82,7 @@ struct Params {
   float* part;         // [split tiles][S][TILE][TILE]
   int* status;
   uint64_t timeout_ns;
-  int vec;             // dW rows allow 16-byte accesses
+  int access;          // bytes of an access that dW's rows allow: 16, 4 or (16-bit values) 2
   int stall;           // testing: the first step of the launch is never filled
 };
 
@@ -178,8 +178,61 @@ struct Out {
       for (int e = 0; e < 8; ++e) acc[8 * c + e] = to_f<D>(h[e]);
     }
   }
-  // The matrix = acc; with !ovw and fp32, += acc.
-  template <bool ovw>
+  // The same by accesses of A = 4 or 2 bytes, through shared memory: a pair of rows or a row at a time
+  // (500 x 4096 x 4098 and x 4097 bf16 45 and 50 us, 80 with the values read beside the writes).
+  template <int A>
+  __device__ __forceinline__ void start_narrow(float (&acc)[128], int lane) const {
+    constexpr int LPR = OUT_ROW / A, RPI = 32 / LPR;  // lanes per row, rows per access
+    constexpr int B = LPR / 2;                        // accesses in flight
+    const int byte = lane % LPR * A;
+#pragma unroll
+    for (int j = 0; j < 128 / BLOCK; ++j) {
+      const int c = j * BLOCK + byte / (int)sizeof(D);
+      const int left = c < cols ? rows - lane / LPR : 0;  // rows from this lane's first on
+      const D* p = dst + lane / LPR * ld + c;
+      __syncwarp();  // the block before has been read
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32; i0 += B * RPI) {
+        uint32_t v[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+          // (volatile: all of a batch before the first is used)
+          const int there = i0 + i * RPI < left;
+          if constexpr (A == 2)
+            asm volatile("{.reg .pred q; setp.ne.s32 q, %2, 0; mov.b32 %0, 0; @q ld.global.u16 %0, [%1];}"
+                         : "=r"(v[i])
+                         : "l"(p), "r"(there)
+                         : "memory");
+          else
+            asm volatile("{.reg .pred q; setp.ne.s32 q, %2, 0; mov.b32 %0, 0; @q ld.global.u32 %0, [%1];}"
+                         : "=r"(v[i])
+                         : "l"(p), "r"(there)
+                         : "memory");
+          p += RPI * ld;
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+          const uint32_t at = chunk(i0 + i * RPI + lane / LPR, byte >> 4) + (byte & 15);
+          if constexpr (A == 2) asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)v[i]) : "memory");
+          else asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v[i]) : "memory");
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        uint32_t u[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                     : "r"(chunk(lane, k)));
+        const D* h = (const D*)u;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[j * BLOCK + k * PER + e] = to_f<D>(h[e]);
+      }
+    }
+    __syncwarp();
+  }
+  // The matrix = acc by accesses of A bytes; with !ovw and fp32, += acc.
+  template <bool ovw, int A>
   __device__ __forceinline__ void put(const float (&acc)[128], int lane) const {
 #pragma unroll
     for (int j = 0; j < 128 / BLOCK; ++j) {
@@ -205,6 +258,38 @@ struct Out {
                      : "memory");
       }
       __syncwarp();
+      if constexpr (A < 16) {
+        constexpr int LPR = OUT_ROW / A, RPI = 32 / LPR;
+        const int byte = lane % LPR * A, c = j * BLOCK + byte / (int)sizeof(D);
+        const int left = c < cols ? rows - lane / LPR : 0;  // rows from this lane's first on
+        D* p = dst + lane / LPR * ld + c;
+        constexpr int B = 8;
+#pragma unroll 1
+        for (int i0 = 0; i0 < LPR; i0 += B) {
+          uint32_t v[B];
+#pragma unroll
+          for (int i = 0; i < B; ++i) {
+            const uint32_t at = chunk((i0 + i) * RPI + lane / LPR, byte >> 4) + (byte & 15);
+            if constexpr (A == 2) {
+              uint16_t u;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(at));
+              v[i] = u;
+            } else {
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[i]) : "r"(at));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < B; ++i) {
+            if ((i0 + i) * RPI < left) {
+              if constexpr (A == 2) *(uint16_t*)p = (uint16_t)v[i];
+              else if constexpr (ovw) *(uint32_t*)p = v[i];
+              else atomicAdd((float*)p, __uint_as_float(v[i]));
+            }
+            p += RPI * ld;
+          }
+        }
+        continue;
+      }
       const int c = j * BLOCK + (lane % CH) * PER;
       D* p = dst + lane / CH * ld + c;
 #pragma unroll
@@ -232,48 +317,6 @@ struct Out {
           }
         }
         p += LR * ld;
-      }
-    }
-    __syncwarp();
-  }
-  // Rows without 16-byte accesses, = or += acc: 16 columns at a time, a lane one column of every
-  // second row, so that a store covers 16 columns of two rows (four columns a lane: 500 x 4096 x 4097
-  // into fp32 70 us, now 42).
-  template <bool ovw>
-  __device__ __forceinline__ void put_narrow(const float (&acc)[128], int lane) const {
-    constexpr int B = ovw ? 4 : 8;  // rows at a time
-    const int c = lane & 15, r0 = lane >> 4;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (16 * j >= cols) break;
-      const int left = 16 * j + c < cols ? rows - r0 : 0;  // rows from r0 on
-      D* o = dst + r0 * ld + 16 * j + c;
-      __syncwarp();
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(lane, e)), "f"(acc[16 * j + 4 * e]),
-                     "f"(acc[16 * j + 4 * e + 1]), "f"(acc[16 * j + 4 * e + 2]), "f"(acc[16 * j + 4 * e + 3])
-                     : "memory");
-      __syncwarp();
-#pragma unroll 1
-      for (int i = 0; i < 16; i += B) {
-        float v[B];
-#pragma unroll
-        for (int u = 0; u < B; ++u)
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[u]) : "r"(chunk(r0 + 2 * (i + u), c >> 2) + (c & 3) * 4));
-        if constexpr (sizeof(D) == 2 && !ovw) {
-#pragma unroll
-          for (int u = 0; u < B; ++u)
-            if (2 * (i + u) < left) v[u] += to_f<D>(o[2 * u * ld]);
-        }
-#pragma unroll
-        for (int u = 0; u < B; ++u)
-          if (2 * (i + u) < left) {
-            if constexpr (sizeof(D) == 2) o[2 * u * ld] = from_f<D>(v[u]);
-            else if (ovw) o[2 * u * ld] = v[u];
-            else atomicAdd(o + 2 * u * ld, v[u]);
-          }
-        o += 2 * B * ld;
       }
     }
     __syncwarp();
@@ -518,8 +561,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Out<D> out{(D*)p.d.dW + n * p.d.lddW + k, p.d.lddW, (int)min(p.d.N - n, (int64_t)32),
                        (int)min(p.d.K - k, (int64_t)128), stage};
       float acc[128];
-      if (sizeof(D) == 2 && it.part < 0 && p.vec && !p.d.ovw) {
-        out.start(acc, lane);
+      if (sizeof(D) == 2 && it.part < 0 && !p.d.ovw) {
+        if (p.access == 16) out.start(acc, lane);
+        else if (p.access == 4) out.template start_narrow<4>(acc, lane);
+        else out.template start_narrow<2>(acc, lane);
       } else {
 #pragma unroll
         for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
@@ -544,17 +589,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (it.part >= 0) {
         const int64_t slot = (int64_t)(it.tile - p.whole) * p.S + it.part;
         const Out<float> part{p.part + slot * TILE * TILE + row * TILE + col, TILE, 32, 128, stage};
-        part.put<true>(acc, lane);
-      } else if (p.vec) {
-        if constexpr (sizeof(D) == 4) {
-          if (p.d.ovw) out.template put<true>(acc, lane);
-          else out.template put<false>(acc, lane);
+        part.put<true, 16>(acc, lane);
+      } else if constexpr (sizeof(D) == 4) {
+        if (p.access == 16) {
+          if (p.d.ovw) out.template put<true, 16>(acc, lane);
+          else out.template put<false, 16>(acc, lane);
         } else {
-          out.template put<true>(acc, lane);  // (with !ovw acc has the old values)
+          if (p.d.ovw) out.template put<true, 4>(acc, lane);
+          else out.template put<false, 4>(acc, lane);
         }
-      } else {
-        if (p.d.ovw) out.template put_narrow<true>(acc, lane);
-        else out.template put_narrow<false>(acc, lane);
+      } else {  // (with !ovw acc has the old values)
+        if (p.access == 16) out.template put<true, 16>(acc, lane);
+        else if (p.access == 4) out.template put<true, 4>(acc, lane);
+        else out.template put<true, 2>(acc, lane);
       }
     }
   }
@@ -595,7 +642,7 @@ __global__ void __launch_bounds__(512) k_dw_join(const __grid_constant__ Params 
     t[3] += v.w;
   }
   D* o = (D*)p.d.dW + n * p.d.lddW + k;
-  if (p.vec && k + 4 <= p.d.K) {
+  if (p.access == 16 && k + 4 <= p.d.K) {
     if constexpr (sizeof(D) == 4) {
       float4 v = p.d.ovw ? make_float4(0.f, 0.f, 0.f, 0.f) : *(float4*)o;
       *(float4*)o = make_float4(v.x + t[0], v.y + t[1], v.z + t[2], v.w + t[3]);
@@ -777,7 +824,7 @@ cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int
   p.timeout_ns = timeout_ns;
   p.stall = stall;
   const int wsz = dtype_size(wdt);
-  p.vec = rows16(a.dW, a.lddW, wsz);
+  p.access = rows16(a.dW, a.lddW, wsz) ? 16 : wsz == 4 || (a.K % 2 == 0 && rows_by(a.dW, a.lddW, wsz, 4)) ? 4 : 2;
   cudaError_t e = cudaSuccess;
 
   const void* dy = a.dy;
