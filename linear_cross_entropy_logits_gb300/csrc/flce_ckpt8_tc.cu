@@ -132,7 +132,7 @@ __device__ __forceinline__ uint2 expand4(uint32_t u, f2 sc2) {
 // A warp's 32 rows x 128 columns of sums (lane = row) and where they go in a matrix. fp32 is added
 // by L2 (one add an element: nothing to wait for, and the same bits on every run). 16-bit values are
 // rounded once: the sums start from them (start), so that their reads overlap the first MMAs (512 x
-// 4096 x 4096 bf16 43 us; read beside the writes 52, through shared memory 45 to 52). The sums pass
+// 4096 x 4096 bf16 36 us; each lane its row's 43; read beside the writes 52). The sums pass
 // through shared memory, 64 bytes of each row at a time, so that a store covers 64 bytes of each of
 // 8 rows: stored a row per lane, 16 bytes of 32 rows at a time, the rows' pitch puts most of a
 // warp's accesses on few L2 slices (28 tiles of 256 x 256 at a pitch of 16 KB took 77 us). With 128
@@ -153,29 +153,59 @@ struct Out {
   __device__ __forceinline__ uint32_t chunk(int r, int c) const {
     return stage + (uint32_t)(r * OUT_ROW + ((c ^ ((r >> 1) & 3)) << 4));
   }
-  // acc = the 16-bit values that the sums are added to (each lane its row's), zero outside.
+  // acc = the 16-bit values that the sums are added to, zero outside: 8 rows an access, two blocks of
+  // columns in flight, through shared memory.
   __device__ __forceinline__ void start(float (&acc)[128], int lane) const {
-    const D* p = dst + lane * ld;
-    uint4 u[16];
+    constexpr int P = 2;  // (1 and 4: 2 to 8 percent slower)
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      u[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (lane < rows && 8 * c < cols) {
-        if (8 * c + 8 <= cols) {
-          u[c] = *(const uint4*)(p + 8 * c);
-        } else {
-          uint32_t* w = (uint32_t*)&u[c];
+    for (int j0 = 0; j0 < 128 / BLOCK; j0 += P) {
+      uint4 u[P][CH];
 #pragma unroll
-          for (int e = 0; e < 7; ++e)
-            if (8 * c + e < cols) w[e / 2] |= (uint32_t)((const uint16_t*)p)[8 * c + e] << (16 * (e & 1));
+      for (int j = 0; j < P; ++j) {
+        const int c = (j0 + j) * BLOCK + lane % CH * PER;
+        const D* p = dst + lane / CH * ld + c;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int there = lane / CH + LR * i < rows && c + PER <= cols;
+          asm volatile("{.reg .pred q; setp.ne.s32 q, %5, 0; mov.b32 %0, 0; mov.b32 %1, 0; mov.b32 %2, 0; mov.b32 %3, 0; "
+                       "@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];}"
+                       : "=r"(u[j][i].x), "=r"(u[j][i].y), "=r"(u[j][i].z), "=r"(u[j][i].w)
+                       : "l"(p), "r"(there)
+                       : "memory");
+          if (lane / CH + LR * i < rows && c < cols && c + PER > cols) {
+            uint32_t* w = (uint32_t*)&u[j][i];
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+              if (c + e < cols) w[e / 2] |= (uint32_t)((const uint16_t*)p)[e] << (16 * (e & 1));
+          }
+          p += LR * ld;
         }
       }
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        __syncwarp();  // the block before has been read
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(lane / CH + LR * i, lane % CH)), "r"(u[j][i].x),
+                       "r"(u[j][i].y), "r"(u[j][i].z), "r"(u[j][i].w)
+                       : "memory");
+        __syncwarp();
+        take(acc, j0 + j, lane);
+      }
     }
+    __syncwarp();
+  }
+  // This lane's row of a block in shared memory.
+  __device__ __forceinline__ void take(float (&acc)[128], int j, int lane) const {
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const D* h = (const D*)&u[c];
+    for (int k = 0; k < CH; ++k) {
+      uint32_t u[4];
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                   : "r"(chunk(lane, k)));
+      const D* h = (const D*)u;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[8 * c + e] = to_f<D>(h[e]);
+      for (int e = 0; e < PER; ++e) acc[j * BLOCK + k * PER + e] = to_f<D>(h[e]);
     }
   }
   // The same by accesses of A = 4 or 2 bytes, through shared memory: a pair of rows or a row at a time
@@ -218,16 +248,7 @@ struct Out {
         }
       }
       __syncwarp();
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        uint32_t u[4];
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
-                     : "r"(chunk(lane, k)));
-        const D* h = (const D*)u;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[j * BLOCK + k * PER + e] = to_f<D>(h[e]);
-      }
+      take(acc, j, lane);
     }
     __syncwarp();
   }
