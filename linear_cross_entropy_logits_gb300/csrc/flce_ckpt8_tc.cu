@@ -400,6 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   cluster_sync();
   tc_after();
   const uint32_t tmem = *tmem_slot;
+  after_previous();  // staged operands are there
 
   // Registers: 80 a thread at launch (6 warpgroups: 480 in all) = 32 + 3 * 48 + 2 * 152.
   if (warp < 4) {
@@ -688,6 +689,7 @@ __global__ void __launch_bounds__(512) k_dw_join(const __grid_constant__ Params 
 template <typename T>
 __global__ void __launch_bounds__(256) k_stage_dy(const T* __restrict__ dy, int64_t lddy, int64_t M, int64_t N,
                                                   int64_t rows, void* out, int64_t ld, int vec) {
+  let_next_start();
   const int64_t m = blockIdx.x, n = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
   if (n >= N) return;
   if constexpr (sizeof(T) == 4) {
@@ -719,17 +721,23 @@ __global__ void __launch_bounds__(256) k_stage_dy(const T* __restrict__ dy, int6
       *(uint2*)((uint16_t*)o + i * rows * ld) = make_uint2(t[0] >> 16 | t[1], t[2] >> 16 | t[3]);
     }
   } else {
-    if (m < M) {
+    const uint16_t* p = (const uint16_t*)dy + m * lddy + n;
+    uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n + e < N) ((T*)out)[m * ld + n + e] = dy[m * lddy + n + e];
-    }
+    for (int e = 0; e < 4; ++e) w[e] = n + e < N ? p[e] : 0u;
+    *(uint2*)((uint16_t*)out + m * ld + n) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
   }
 }
 __global__ void __launch_bounds__(256) k_stage_q(const uint8_t* __restrict__ q, int64_t ldq, int64_t K, uint8_t* out,
                                                  int64_t ld) {
-  const int64_t m = blockIdx.x, k = (int64_t)blockIdx.y * 256 + threadIdx.x;
-  if (k < K) out[m * ld + k] = q[m * ldq + k];
+  let_next_start();
+  const int64_t m = blockIdx.x, k = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
+  if (k >= K) return;
+  uint32_t w = 0;  // (the pitch is a multiple of 16)
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (k + e < K) w |= (uint32_t)q[m * ldq + k + e] << (8 * e);
+  *(uint32_t*)(out + m * ld + k) = w;
 }
 
 // ------------------------------------------------------------------ plan
@@ -785,7 +793,8 @@ Plan8 plan(const DwArgs& a, int dt) {
 }
 
 template <typename T, typename D>
-cudaError_t launch(const CUtensorMap& A, const CUtensorMap& Q, const Params& p, int64_t items, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& A, const CUtensorMap& Q, const Params& p, int64_t items, bool staged,
+                   cudaStream_t s) {
   auto kern = k_dw_tc8<T, D>;
   // per-device cache of the pairs that fit at once; concurrent first launches may both set it
   static std::atomic<int> fit[64];
@@ -794,7 +803,7 @@ cudaError_t launch(const CUtensorMap& A, const CUtensorMap& Q, const Params& p, 
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
@@ -802,6 +811,8 @@ cudaError_t launch(const CUtensorMap& A, const CUtensorMap& Q, const Params& p, 
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // it starts up while operands are staged
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = fit[dev].load(std::memory_order_relaxed);
@@ -815,6 +826,7 @@ cudaError_t launch(const CUtensorMap& A, const CUtensorMap& Q, const Params& p, 
     fit[dev].store(n, std::memory_order_relaxed);
   }
   cfg.gridDim = dim3(2 * (unsigned)(items < n ? items : n), 1, 1);
+  cfg.numAttrs = staged ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, A, Q, p);
   if (e != cudaSuccess || p.S == 1) return e;
   const int64_t split = (int64_t)p.tn * p.tk - p.whole;
@@ -869,7 +881,7 @@ cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int
   if (stage_q(a)) {
     q = (const uint8_t*)(ws + pl.off_q);
     ldq = (int64_t)round_up((size_t)a.K, 16);
-    k_stage_q<<<dim3((unsigned)a.M, (unsigned)cdiv64(a.K, 256)), 256, 0, s>>>(a.q, a.ldq, a.K, (uint8_t*)q, ldq);
+    k_stage_q<<<dim3((unsigned)a.M, (unsigned)cdiv64(a.K, 1024)), 256, 0, s>>>(a.q, a.ldq, a.K, (uint8_t*)q, ldq);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   CUtensorMap A, Q;
@@ -878,10 +890,12 @@ cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int
       !ptx::encode_2d(&Q, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, a.K, a.M, ldq, 128, BK, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   const int64_t items = p.whole + ((int64_t)p.tn * p.tk - p.whole) * p.S;
+  const bool staged = stage_dy(a, dt) || stage_q(a);
   if (dt == FLCE_F16)
-    return wdt == FLCE_F32 ? launch<__half, float>(A, Q, p, items, s) : launch<__half, __half>(A, Q, p, items, s);
-  if (wdt == FLCE_F32) return launch<__nv_bfloat16, float>(A, Q, p, items, s);
-  return launch<__nv_bfloat16, __nv_bfloat16>(A, Q, p, items, s);
+    return wdt == FLCE_F32 ? launch<__half, float>(A, Q, p, items, staged, s)
+                           : launch<__half, __half>(A, Q, p, items, staged, s);
+  if (wdt == FLCE_F32) return launch<__nv_bfloat16, float>(A, Q, p, items, staged, s);
+  return launch<__nv_bfloat16, __nv_bfloat16>(A, Q, p, items, staged, s);
 }
 
 }  // namespace flce
