@@ -100,8 +100,9 @@ __device__ __forceinline__ bool get_item(const Params& p, int i, Item& it) {
   const int s = j % p.S;
   it.tile = t;
   it.part = p.S > 1 ? s : -1;
-  it.s0 = (int)((int64_t)p.steps * s / p.S);
-  it.s1 = (int)((int64_t)p.steps * (s + 1) / p.S);
+  // (32 bits: 64-bit divisions took 0.5 us before the first copy; steps * S < 2^29)
+  it.s0 = (int)((uint32_t)p.steps * (uint32_t)s / (uint32_t)p.S);
+  it.s1 = (int)((uint32_t)p.steps * (uint32_t)(s + 1) / (uint32_t)p.S);
   return true;
 }
 
@@ -632,8 +633,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncwarp();
   tc_before();
   cluster_sync();  // no role of either CTA issues anything after this point
-  if (threadIdx.x == 0) {
-    // every copy issued lands before shared memory is released
+  if (threadIdx.x == 0 && *abort_flag) {
+    // every copy issued lands before shared memory is released; without an abort all were waited for
     for (int s = 0; s < STAGES; ++s)
       if (copies[s] > 0) bar_wait(full(s), (uint32_t)(copies[s] - 1) & 1u, ab, false);
   }
