@@ -43,7 +43,8 @@ def _tokens(kind, N, V, g):
 
 FWD = [(1, 64, 10, "bf16", 1.0, 0, 0), (5, 1, 7, "f32", 0.5, 0, 0), (33, 1003, 500, "f16", 2.0, 0, 0),
        (300, 2048, 1000, "bf16", 45.25, 0, 0), (17, 136, 40, "bf16", 1.0, 3, 1), (64, 520, 99, "f32", 1.0, 8, 4),
-       (2, 20000, 5, "f16", 1.0, 0, 0), (40, 8, 3, "bf16", 3.0, 8, 8)]
+       (2, 20000, 5, "f16", 1.0, 0, 0), (40, 8, 3, "bf16", 3.0, 8, 8),
+       (333, 40, 50, "bf16", 0.5, 0, 0), (1001, 130, 77, "f16", 1.0, 2, 2), (155, 65, 9, "f32", 1.0, 1, 1)]
 
 
 @pytest.mark.parametrize("N,H,V,dt,scale,extra,offset", FWD)
