@@ -210,7 +210,7 @@ struct Out {
     }
   }
   // The same by accesses of A = 4 or 2 bytes, through shared memory: a pair of rows or a row at a time
-  // (500 x 4096 x 4098 and x 4097 bf16 45 and 50 us, 80 with the values read beside the writes).
+  // (500 x 4096 x 4098 and x 4097 bf16 41 and 46 us, 80 with the values read beside the writes).
   template <int A>
   __device__ __forceinline__ void start_narrow(float (&acc)[128], int lane) const {
     constexpr int LPR = OUT_ROW / A, RPI = 32 / LPR;  // lanes per row, rows per access
