@@ -534,8 +534,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (whose == group) {
           ok = bar_wait(full(s), ph, ab, true) && bar_wait(full_s(s), ph, ab, true);
           if (ok && turn >= SLOTS) {
-            // the slot's last user, SLOTS steps back, was in stage s - SLOTS (this round's or,
-            // below 0, the round before's)
+            // the slot's last user, SLOTS steps back, was in stage s - SLOTS (this pass's or,
+            // below 0, the pass before's)
             const int u = s - SLOTS;
             ok = bar_wait(empty(u < 0 ? u + STAGES : u), u < 0 ? ph ^ 1u : ph, ab, true);
           }
