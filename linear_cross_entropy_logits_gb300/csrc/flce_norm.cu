@@ -620,11 +620,12 @@ cudaError_t bwd_w(const BwdArgs& a, int64_t& part_rows, cudaStream_t s) {
   constexpr int NV = (EPV <= 2 ? 8 : 16) / EPV;
   const Shape p = row_shape(a.H, EPV);
   if (p.wpr == 0) {
-    if (a.dx != nullptr) k_rms_bwd_long<T><<<(unsigned)a.N, 512, 0, s>>>(a);
+    // the sums first: dx may be dy itself
     if (a.part != nullptr) {
       part_rows = LONG_DW_ROWS;
       k_rms_dw_long<T><<<dim3((unsigned)cdiv64(a.H, 256), LONG_DW_ROWS), 256, 0, s>>>(a);
     }
+    if (a.dx != nullptr) k_rms_bwd_long<T><<<(unsigned)a.N, 512, 0, s>>>(a);
   } else {
     // (rows in wider accesses come here with 32 elements a thread only)
     part_rows = launch_bwd<T, EPV, EPV <= 2 ? NV : 2 * NV>(a, p.wpr, s);

@@ -182,6 +182,31 @@ def test_gradient_strides_and_in_place(dt, H, extra, offset):
     close(got["dweight"], np64(want["dweight"]), 2 * F32 * (N + 8) * wmag)
 
 
+@pytest.mark.parametrize("N,H,dt,extra,offset", [(3, 20000, "bf16", 0, 0), (5, 9001, "f16", 0, 0), (2, 16392, "f32", 0, 0),
+                                                 (4, 8194, "bf16", 0, 0), (3, 9216, "bf16", 1, 3), (70, 8193, "f32", 0, 0)])
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("over", ["dy", "dh"])
+def test_gradient_of_long_rows_in_place(N, H, dt, extra, offset, q8, over):
+    """Rows that two kernels read, with dx in the place of dy or of dh: dweight is that of the
+    dy that was given."""
+    x, d, w = _rows(N, H, dt, N + H)
+    rd = torch.rand(N, generator=torch.Generator().manual_seed(6)).cuda() + 0.5
+    dh = torch.randn(N, H, generator=torch.Generator().manual_seed(7)).to(DT[dt])
+    dd, hh = strided(d.cuda(), extra, offset), strided(dh.cuda(), extra, offset)
+    h = np64(x)
+    kw = dict(h=strided(x.cuda(), extra, offset))
+    if q8:
+        p = flce.ckpt8_pack(x.cuda())
+        h = np64(p["q"]) * oo.spread(np64(p["scale"]), H)
+        kw = dict(h8=p["q"], h8_scale=p["scale"])
+    into = dd if over == "dy" else hh
+    o = flce.rmsnorm_bwd(dd, w.cuda(), rd, **kw, dh=hh, outputs={"dx": into})
+    assert o["dx"].data_ptr() == into.data_ptr()
+    dx, dw, mag, wmag = oo.rmsnorm_bwd(np64(d), h, np64(rd), np64(w), 0.0, np64(dh))
+    close(into, dx, ULP[dt] * np.abs(dx) + F32 * mag + FLOOR[dt], "dx")
+    close(o["dweight"], dw, F32 * ((N + 8) * wmag + np.abs(dw)), "dweight")
+
+
 def test_gradient_is_the_derivative_of_the_forward():
     """dx and dweight of L = sum(c * y) in fp32 against central differences of the float64
     forward (step 1e-5: truncation below 1e-8 of the second derivative's scale)."""
