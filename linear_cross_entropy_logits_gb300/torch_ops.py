@@ -232,9 +232,9 @@ def add_rms_norm_op(x: torch.Tensor, weight: torch.Tensor, residual: Optional[to
     """(y, h, rstd, h8, h8_scale); h is empty without a residual, h8 and h8_scale without checkpoint8."""
     o = flce.rmsnorm_fwd(_rows(x), weight, None if residual is None else _rows(residual), eps=eps,
                          weight_offset=weight_offset, want_h8=checkpoint8)
-    e = x.new_empty(0)
-    return (o["y"], o["h"] if residual is not None else e, o["rstd"],
-            o["h8"] if checkpoint8 else e.to(torch.float8_e4m3fn), o["h8_scale"] if checkpoint8 else e.float())
+    empty = lambda dtype: torch.empty(0, dtype=dtype, device=x.device)  # noqa: E731  (outputs share no memory)
+    return (o["y"], o["h"] if residual is not None else empty(x.dtype), o["rstd"],
+            o["h8"] if checkpoint8 else empty(torch.float8_e4m3fn), o["h8_scale"] if checkpoint8 else empty(torch.float32))
 
 
 @add_rms_norm_op.register_fake

@@ -11,7 +11,7 @@ import pytest
 import torch
 
 from linear_cross_entropy_logits_gb300 import build as B
-from linear_cross_entropy_logits_gb300 import flce
+from linear_cross_entropy_logits_gb300 import flce, torch_ops
 from oracle import ops_oracle as oo
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -172,6 +172,37 @@ def test_matrix_check():
         flce._dense("v", x[:, 0], (6,), torch.float32, cpu)
     with pytest.raises(ValueError):
         flce._dense("s", x[:, :4], (6, 4), torch.float32, cpu)
+
+
+def _storages(outs):
+    return [t.untyped_storage()._cdata for t in outs]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("residual", [True, False])
+@pytest.mark.parametrize("checkpoint8", [True, False])
+def test_norm_op_outputs_are_tensors_of_their_own(monkeypatch, dtype, residual, checkpoint8):
+    """The autograd form on the CPU, with the norm's kernels replaced by plain tensors: outputs of
+    a custom op share no memory with one another, the empty ones included."""
+    def norm(x, weight, res, *, eps, weight_offset, want_h8):
+        N, H = x.shape
+        o = {"y": x.clone(), "rstd": torch.ones(N)}
+        if res is not None:
+            o["h"] = x + res
+        if want_h8:
+            o["h8"], o["h8_scale"] = x.to(torch.float8_e4m3fn), torch.ones(N, (H + 127) // 128)
+        return o
+
+    monkeypatch.setattr(flce, "rmsnorm_fwd", norm)
+    x, w = torch.randn(6, 40).to(dtype).requires_grad_(), torch.ones(40, dtype=dtype, requires_grad=True)
+    r = torch.randn(6, 40).to(dtype) if residual else None
+    out = torch_ops.add_rms_norm(x, w, r, checkpoint8=checkpoint8)
+    y, h = out if residual else (out, None)
+    assert y.requires_grad and y.dtype is dtype and (h is None or h.requires_grad)
+    outs = torch_ops.add_rms_norm_op(x, w, r, 1e-6, 0.0, checkpoint8)
+    assert len(set(_storages(outs))) == 5
+    fake = [dtype, dtype, torch.float32, torch.float8_e4m3fn, torch.float32]
+    assert [t.dtype for t in outs] == fake and [t.numel() == 0 for t in outs[1:]] == [not residual, False] + 2 * [not checkpoint8]
 
 
 # ---- the oracles
