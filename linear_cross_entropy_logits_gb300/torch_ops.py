@@ -51,10 +51,10 @@ def fused_linear_cross_entropy_op(X: torch.Tensor, W: torch.Tensor, targets: tor
                        reduction=reduction, z_loss_scale=z_loss_scale, grad_out=grad_out,
                        want_dX=want_dX, want_dW=want_dW, dW=dW, dbias=db, check=False,
                        flags=flce.FLAG_DW_OVERWRITE)
-    empty = X.new_empty(0)
+    empty = lambda dtype: torch.empty(0, dtype=dtype, device=X.device)  # noqa: E731  (outputs share no memory)
     return (out["loss"], out["z_loss"], out["acc"], out["lse"], out["pred"],
-            out["dX"] if want_dX else empty, dW if want_dW else empty.float(),
-            db if db is not None else empty.float())
+            out["dX"] if want_dX else empty(X.dtype), dW if want_dW else empty(torch.float32),
+            db if db is not None else empty(torch.float32))
 
 
 @fused_linear_cross_entropy_op.register_fake

@@ -205,6 +205,28 @@ def test_norm_op_outputs_are_tensors_of_their_own(monkeypatch, dtype, residual, 
     assert [t.dtype for t in outs] == fake and [t.numel() == 0 for t in outs[1:]] == [not residual, False] + 2 * [not checkpoint8]
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("need_x", [True, False])
+@pytest.mark.parametrize("need_w", [True, False])
+@pytest.mark.parametrize("with_bias", [True, False])
+def test_head_op_outputs_are_tensors_of_their_own(monkeypatch, dtype, need_x, need_w, with_bias):
+    """The same of the head's op, in evaluation and with either gradient."""
+    def head(X, W, targets, bias, *, want_dX, **kw):
+        f = lambda n: torch.zeros(n)  # noqa: E731
+        o = {"loss": f(1), "z_loss": f(1), "acc": f(1), "lse": f(len(X)), "pred": torch.zeros(len(X), dtype=torch.int64)}
+        if want_dX:
+            o["dX"] = torch.zeros_like(X)
+        return o
+
+    monkeypatch.setattr(flce, "fwd_bwd", head)
+    X, W = torch.randn(5, 8, dtype=dtype, requires_grad=need_x), torch.randn(7, 8, dtype=dtype, requires_grad=need_w)
+    b = torch.zeros(7, dtype=dtype, requires_grad=need_w) if with_bias else None
+    t = torch.zeros(5, dtype=torch.int64)
+    assert torch_ops.fused_linear_cross_entropy(X, W, t, b).requires_grad == (need_x or need_w)
+    outs = torch_ops.fused_linear_cross_entropy_op(X, W, t, b, None, -100, "mean", 0.0, need_x, need_w, True)
+    assert len(set(_storages(outs))) == 8
+
+
 # ---- the oracles
 
 def test_e4m3_rounding_against_torch():
