@@ -3,6 +3,10 @@
 Argument marshalling only: torch tensors supply device memory and the current CUDA stream;
 every step of the computation runs in the library's kernels. If the library has not been
 built the first call raises, there is no fallback.
+
+Calls run on the current stream, or on the one given as ``stream``. It must already wait for
+what made the inputs, and a stream that reads the results waits for it. The operators around
+the head make their tensors in that stream's memory.
 """
 
 from __future__ import annotations
@@ -269,6 +273,28 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _on(stream, fn, kw):
+    """fn(**kw) with `stream` as the current one: what the call allocates and fills comes from that
+    stream's memory and is ordered with its kernels. Tensors of the caller's are recorded on
+    `stream`, those that the call makes on the stream that was current, so that neither is handed
+    out again before the other stream is done with it."""
+    given = [t for v in kw.values() for t in (v.values() if isinstance(v, dict) else (v,)) if torch.is_tensor(t)]
+    if any(t.device != stream.device for t in given):
+        raise ValueError(f"stream is on {stream.device}, not every tensor is")
+    kw["stream"] = None
+    caller = torch.cuda.current_stream(stream.device)
+    if caller == stream:
+        return fn(**kw)
+    with torch.cuda.stream(stream):
+        o = fn(**kw)
+    for t in given:
+        t.record_stream(stream)
+    for t in o.values():
+        if torch.is_tensor(t) and not any(t is g for g in given):
+            t.record_stream(caller)
+    return o
+
+
 def fwd_bwd(X, W, targets, bias=None, *, ignore_index=-100, reduction="mean",
             z_loss_scale=0.0, grad_out=None, want_dX=True, want_dW=True, dW=None, dbias=None,
             workspace=None, workspace_bytes=None, budget_bytes=0, outputs=None, flags=0,
@@ -485,31 +511,19 @@ def empty_rows8(N, H, device):
     return torch.empty_strided((N, H), ((H + 15) & ~15, 1), dtype=torch.float8_e4m3fn, device=device)
 
 
-def _workspace(ws, nbytes, dev, stream):
-    """The caller's byte workspace, or a new one owned by the stream that uses it."""
+def _workspace(ws, nbytes, dev):
+    """The caller's byte workspace, or a new one."""
     if ws is not None:
         if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev:
             raise ValueError(f"workspace must be a dense uint8 tensor on {dev}")
         return ws
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
-def _launch(fn, where, args, dev, stream, *used):
-    """Enqueue on `stream` (None: the current one); returns the stream's handle. Tensors used on
-    a given stream (`used`, and the values of dicts in it) are recorded on it, so that the
-    allocator does not hand their memory out before the kernels are done."""
+def _launch(fn, where, args, dev):
+    """Enqueue on the current stream; returns its handle."""
     index = dev.index
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        handle = stream.cuda_stream
-        for u in used:
-            for t in u.values() if isinstance(u, dict) else (u,):
-                if t is not None:
-                    t.record_stream(stream)
+    handle = torch._C._cuda_getCurrentRawStream(index)
     if index == torch._C._cuda_getDevice():
         rc = fn(args, handle)
     else:
@@ -544,6 +558,8 @@ def embed_fwd(tokens, E, *, scale=1.0, ignore_index=-100, out=None, status=None,
     outside [0, V) gives a zero row and FLCE_ERR_TARGET_RANGE. ``status`` (int32 [1]) receives
     the device status word without a check.
     """
+    if stream is not None:
+        return _on(stream, embed_fwd, locals())
     lib = _lib or load()
     dev, (V, H), dt = _cuda_2d("E", E)
     N = tokens.shape[0]
@@ -554,7 +570,7 @@ def embed_fwd(tokens, E, *, scale=1.0, ignore_index=-100, out=None, status=None,
     po, ldo = _matrix("out", out, N, H, E.dtype, dev)
     a = FlceEmbedArgs(N, H, V, dt, 0, _dense("tokens", tokens, (N,), torch.int64, dev), ignore_index, scale, 0,
                       pE, ldE, po, ldo, None, 0, None, 0, None, 0, _status(o, status, check, dev))
-    h = _launch(lib.flce_embed_fwd, "flce_embed_fwd", a, dev, stream, tokens, E, o)
+    h = _launch(lib.flce_embed_fwd, "flce_embed_fwd", a, dev)
     return _finish(o, lib, check, h)
 
 
@@ -566,6 +582,8 @@ def embed_bwd(tokens, dout, *, V=None, dE=None, scale=1.0, ignore_index=-100, wo
     it is written), for instance the head's own dW of a tied embedding. Without dE a new fp32
     one of ``V`` rows is written. Returns a dict with dE (and status_code when ``check``).
     """
+    if stream is not None:
+        return _on(stream, embed_bwd, locals())
     lib = _lib or load()
     dev, (N, H), dt = _cuda_2d("dout", dout)
     if dE is None:
@@ -574,14 +592,14 @@ def embed_bwd(tokens, dout, *, V=None, dE=None, scale=1.0, ignore_index=-100, wo
         dE = torch.empty((V, H), dtype=torch.float32, device=dev)
         flags |= FLAG_DW_OVERWRITE
     V = dE.shape[0]
-    workspace = _workspace(workspace, lib.flce_embed_workspace_size(N, H, V), dev, stream)
+    workspace = _workspace(workspace, lib.flce_embed_workspace_size(N, H, V), dev)
     o = {"dE": dE, "workspace": workspace}
     pd, ldd = _matrix("dout", dout, N, H, dout.dtype, dev)
     pE, ldE = _matrix("dE", dE, V, H, dE.dtype, dev)
     a = FlceEmbedArgs(N, H, V, dt, _grad_dtype("dE", dE), _dense("tokens", tokens, (N,), torch.int64, dev),
                       ignore_index, scale, flags, None, 0, None, 0, pd, ldd, pE, ldE, workspace.data_ptr(),
                       workspace.numel(), _status(o, status, check, dev))
-    h = _launch(lib.flce_embed_bwd, "flce_embed_bwd", a, dev, stream, tokens, dout, o)
+    h = _launch(lib.flce_embed_bwd, "flce_embed_bwd", a, dev)
     return _finish(o, lib, check, h)
 
 
@@ -594,6 +612,8 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, weight_offset=0.0, want_y
     h8, h8_scale (8-bit checkpoint of h for ``rmsnorm_bwd``). ``outputs`` may carry preallocated
     tensors under the same keys; h may be x or residual itself.
     """
+    if stream is not None:
+        return _on(stream, rmsnorm_fwd, locals())
     lib = _lib or load()
     dev, (N, H), dt = _cuda_2d("x", x)
     dtype = x.dtype
@@ -615,7 +635,7 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, weight_offset=0.0, want_y
     (ph8, ldh8, psh) = _rows8(o, "h8", "h8_scale", N, H, dev) if want_h8 else (None, 0, None)
     a = FlceRmsnormArgs(N, H, dt, eps, weight_offset, 0, px, ldx, pr, ldr, _dense("weight", weight, (H,), dtype, dev),
                         ph, ldh, py, ldy, prstd, py8, ldy8, psy, ph8, ldh8, psh)
-    _launch(lib.flce_rmsnorm_fwd, "flce_rmsnorm_fwd", a, dev, stream, x, residual, weight, o)
+    _launch(lib.flce_rmsnorm_fwd, "flce_rmsnorm_fwd", a, dev)
     return o
 
 
@@ -649,6 +669,8 @@ def rmsnorm_bwd(dy, weight, rstd, h=None, *, h8=None, h8_scale=None, dh=None, we
     stream's own gradient, added) and dweight, accumulated into when given (fp32 or dy's dtype;
     FLAG_DW_OVERWRITE: written), else a new fp32 vector. The norm's input is ``h`` or its 8-bit
     checkpoint ``h8, h8_scale``. Returns a dict with dx and dweight."""
+    if stream is not None:
+        return _on(stream, rmsnorm_bwd, locals())
     lib = _lib or load()
     dev, (N, H), dt = _cuda_2d("dy", dy)
     dtype = dy.dtype
@@ -664,7 +686,7 @@ def rmsnorm_bwd(dy, weight, rstd, h=None, *, h8=None, h8_scale=None, dh=None, we
             flags |= FLAG_DW_OVERWRITE
         wdt = _grad_dtype("dweight", dweight)
         pw = _dense("dweight", dweight, (H,), dweight.dtype, dev)
-        workspace = _workspace(workspace, lib.flce_rmsnorm_workspace_size(N, H), dev, stream)
+        workspace = _workspace(workspace, lib.flce_rmsnorm_workspace_size(N, H), dev)
         pws, wbytes = workspace.data_ptr(), workspace.numel()
         o["dweight"], o["workspace"] = dweight, workspace
     (ph, ldh) = (None, 0) if h is None else _matrix("h", h, N, H, dtype, dev)
@@ -678,20 +700,21 @@ def rmsnorm_bwd(dy, weight, rstd, h=None, *, h8=None, h8_scale=None, dh=None, we
     a = FlceRmsnormBwdArgs(N, H, dt, wdt, weight_offset, flags, pdy, lddy, ph, ldh, p8, ld8, ps8,
                            _dense("rstd", rstd, (N,), torch.float32, dev),
                            _dense("weight", weight, (H,), dtype, dev), pdh, lddh, pdx, lddx, pw, pws, wbytes)
-    _launch(lib.flce_rmsnorm_bwd, "flce_rmsnorm_bwd", a, dev, stream, dy, weight, rstd, h, h8, h8_scale, dh, o)
+    _launch(lib.flce_rmsnorm_bwd, "flce_rmsnorm_bwd", a, dev)
     return o
 
 
 def ckpt8_pack(x, *, outputs=None, stream=None):
     """8-bit checkpoint of x [N, H]: a dict with q (e4m3 [N, H], rows at multiples of 16 bytes)
     and scale (fp32 [N, ceil(H/128)], powers of two); the value kept is q * scale."""
+    if stream is not None:
+        return _on(stream, ckpt8_pack, locals())
     lib = _lib or load()
     dev, (N, H), dt = _cuda_2d("x", x)
     o = dict(outputs) if outputs else {}
     px, ldx = _matrix("x", x, N, H, x.dtype, dev)
     pq, ldq, ps = _rows8(o, "q", "scale", N, H, dev)
-    _launch(lib.flce_ckpt8_pack, "flce_ckpt8_pack", FlceCkpt8Args(N, H, dt, 0, px, ldx, pq, ldq, ps), dev, stream,
-            x, o)
+    _launch(lib.flce_ckpt8_pack, "flce_ckpt8_pack", FlceCkpt8Args(N, H, dt, 0, px, ldx, pq, ldq, ps), dev)
     return o
 
 
@@ -703,6 +726,8 @@ def ckpt8_dw(dy, q, scale, *, dW=None, workspace=None, flags=0, wait_timeout_ms=
     fp32 or dy's dtype, accumulated into (FLAG_DW_OVERWRITE: written), else a new fp32 one.
     Returns a dict with dW (and status_code when ``check``, which synchronises the stream).
     """
+    if stream is not None:
+        return _on(stream, ckpt8_dw, locals())
     lib = _lib or load()
     dev, (M, N), dt = _cuda_2d("dy", dy)
     if q.dim() != 2:
@@ -718,7 +743,7 @@ def ckpt8_dw(dy, q, scale, *, dW=None, workspace=None, flags=0, wait_timeout_ms=
     a = FlceCkpt8DwArgs(M, N, K, dt, _grad_dtype("dW", dW), flags, wait_timeout_ms, pdy, lddy, pq, ldq,
                         _dense("scale", scale, (M, (K + Q_BLOCK - 1) // Q_BLOCK), torch.float32, dev), pW, ldW,
                         None, 0, _status(o, status, check, dev))
-    workspace = o["workspace"] = _workspace(workspace, lib.flce_ckpt8_dw_workspace_size(a), dev, stream)
+    workspace = o["workspace"] = _workspace(workspace, lib.flce_ckpt8_dw_workspace_size(a), dev)
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    h = _launch(lib.flce_ckpt8_dw, "flce_ckpt8_dw", a, dev, stream, dy, q, scale, o)
+    h = _launch(lib.flce_ckpt8_dw, "flce_ckpt8_dw", a, dev)
     return _finish(o, lib, check, h)

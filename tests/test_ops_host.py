@@ -174,6 +174,89 @@ def test_matrix_check():
         flce._dense("s", x[:, :4], (6, 4), torch.float32, cpu)
 
 
+class _Stream:
+    device = torch.device("cpu")
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """The binding on the CPU with stand-ins for streams and kernels: a log of (event, current
+    stream, tensor) for allocations, launches and records."""
+    log, cur = [], [_Stream()]
+
+    class use:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            cur.append(self.s)
+
+        def __exit__(self, *a):
+            cur.pop()
+
+    def logged(make):
+        def f(*a, **kw):
+            t = make(*a, **kw)
+            log.append(("new", cur[-1], t))
+            return t
+        return f
+
+    for name in ("empty", "zeros", "empty_strided", "empty_like"):
+        monkeypatch.setattr(torch, name, logged(getattr(torch, name)))
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: cur[-1])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: log.append(("record", s, t)))
+    monkeypatch.setattr(flce, "_cuda_2d", lambda name, t: (t.device, t.shape, flce.DTYPES[t.dtype]))
+    monkeypatch.setattr(flce, "_launch", lambda fn, where, args, dev: log.append(("launch", cur[-1], None)))
+    return log, cur
+
+
+def _call(name, x, status, stream):
+    t, kw = torch.zeros(6, dtype=torch.int64), dict(check=False, status=status, stream=stream)
+    if name == "embed_fwd":
+        return flce.embed_fwd(t, x, **kw)
+    if name == "embed_bwd":
+        return flce.embed_bwd(t, x, V=3, **kw)
+    if name == "rmsnorm_fwd":
+        return flce.rmsnorm_fwd(x, x[0].clone(), x.clone(), want_y8=True, want_h8=True, stream=stream)
+    if name == "rmsnorm_bwd":
+        return flce.rmsnorm_bwd(x, x[0].clone(), torch.ones(6), x.clone(), stream=stream)
+    if name == "ckpt8_pack":
+        return flce.ckpt8_pack(x, stream=stream)
+    return flce.ckpt8_dw(x, x.to(torch.float8_e4m3fn), torch.ones(6, 1), **kw)
+
+
+@pytest.mark.parametrize("name", ["embed_fwd", "embed_bwd", "rmsnorm_fwd", "rmsnorm_bwd", "ckpt8_pack", "ckpt8_dw"])
+def test_a_given_stream_owns_what_the_call_makes(lib, streams, name):
+    """Outputs and workspaces come from the given stream's memory: another's block may still be in
+    use by kernels that the given stream does not wait for. And memory is not handed out again
+    before the caller's stream is done with the outputs, and the given one with the inputs."""
+    log, cur = streams
+    x, s, status = torch.randn(6, 8), _Stream(), torch.zeros(1, dtype=torch.int32)
+    log.clear()
+    o = _call(name, x, status, s)
+    mine = [t for t in o.values() if torch.is_tensor(t) and t is not status]
+    new = [(st, t) for ev, st, t in log if ev == "new"]
+    for t in mine:
+        assert any(t is u and st is s for st, u in new)
+    assert [st for ev, st, _ in log if ev == "launch"] == [s]
+    rec = [(st, t) for ev, st, t in log if ev == "record"]
+    for t in mine:
+        assert any(t is u and st is cur[-1] for st, u in rec)
+    assert any(x is u and st is s for st, u in rec)
+    # the stream that is current anyway: nothing to record
+    log.clear()
+    _call(name, x, status, cur[-1])
+    assert not [e for e in log if e[0] == "record"]
+
+
+def test_a_stream_of_another_device_is_refused(streams):
+    s = _Stream()
+    s.device = torch.device("meta")
+    with pytest.raises(ValueError, match="stream"):
+        flce.ckpt8_pack(torch.randn(2, 8), stream=s)
+
+
 def _storages(outs):
     return [t.untyped_storage()._cdata for t in outs]
 
