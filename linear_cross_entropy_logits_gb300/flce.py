@@ -4,9 +4,9 @@ Argument marshalling only: torch tensors supply device memory and the current CU
 every step of the computation runs in the library's kernels. If the library has not been
 built the first call raises, there is no fallback.
 
-Calls run on the current stream, or on the one given as ``stream``. It must already wait for
-what made the inputs, and a stream that reads the results waits for it. The operators around
-the head make their tensors in that stream's memory.
+Calls run on the current stream, or on the one given as ``stream``: then it also owns the
+tensors that the call makes, and it must already wait for what made the inputs; a stream that
+reads the results waits for it.
 """
 
 from __future__ import annotations
@@ -308,6 +308,8 @@ def fwd_bwd(X, W, targets, bias=None, *, ignore_index=-100, reduction="mean",
     dbias, and the status code when ``check`` is set (which synchronises the stream).
     ``outputs`` may carry preallocated output tensors under the same keys.
     """
+    if stream is not None:
+        return _on(stream, fwd_bwd, locals())
     lib = load()
     if X.device.type != "cuda":
         raise ValueError("X must be a CUDA tensor")
@@ -368,7 +370,7 @@ def fwd_bwd(X, W, targets, bias=None, *, ignore_index=-100, reduction="mean",
     a.status = _ptr(o["status"])
     a.wait_timeout_ms = wait_timeout_ms
     a.profile = profiler.handle if profiler is not None else None
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    s = torch.cuda.current_stream(dev)
     rc = lib.flce_fwd_bwd(ctypes.byref(a), ctypes.c_void_p(s.cuda_stream))
     if rc != FLCE_OK:
         raise FlceError(rc, "flce_fwd_bwd")
@@ -390,6 +392,8 @@ def fused_linear_jsd(Xs, Ws, Xt, Wt, labels=None, *, beta=0.5, temperature=1.0, 
                      outputs=None):
     """Fused linear JSD / KL distillation forward + backward (student gradients only).
     Returns a dict with loss, n_labelled, dX, dW (and status_code when ``check``)."""
+    if stream is not None:
+        return _on(stream, fused_linear_jsd, locals())
     lib = load()
     BT, Hs = Xs.shape
     Ht = Xt.shape[1]
@@ -432,7 +436,7 @@ def fused_linear_jsd(Xs, Ws, Xt, Wt, labels=None, *, beta=0.5, temperature=1.0, 
     a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
     a.status = _ptr(o["status"])
     a.profile = profiler.handle if profiler is not None else None
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    s = torch.cuda.current_stream(dev)
     rc = lib.flce_fused_linear_jsd(ctypes.byref(a), ctypes.c_void_p(s.cuda_stream))
     if rc != FLCE_OK:
         raise FlceError(rc, "flce_fused_linear_jsd")
@@ -446,7 +450,11 @@ def fused_linear_jsd(Xs, Ws, Xt, Wt, labels=None, *, beta=0.5, temperature=1.0, 
 def scale_by(x, g, stream=None):
     """x *= g in place (x: contiguous CUDA tensor, fp32/bf16/fp16; g: one-element fp32 CUDA
     tensor), skipped on the device when g == 1."""
-    s = stream if stream is not None else torch.cuda.current_stream(x.device)
+    s = torch.cuda.current_stream(x.device)
+    if stream is not None and stream != s:
+        x.record_stream(stream)
+        g.record_stream(stream)
+        s = stream
     rc = load().flce_scale_by(ctypes.c_void_p(x.data_ptr()), x.numel(), DTYPES[x.dtype],
                               ctypes.c_void_p(g.data_ptr()), ctypes.c_void_p(s.cuda_stream))
     if rc != FLCE_OK:

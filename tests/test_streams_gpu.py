@@ -34,6 +34,9 @@ def _calls():
     t = torch.randint(0, 900, (300,), generator=g).cuda()
     p = flce.ckpt8_pack(x)
     rstd = torch.ones(300, device="cuda")
+    X, V = r(256, 128), r(1024, 128)
+    y = torch.randint(0, 1024, (256,), generator=g).cuda()
+    Xt, Vt = r(256, 192), r(1024, 192)
     return {
         "embed_fwd": lambda **k: flce.embed_fwd(t, W, check=False, **k),
         "embed_bwd": lambda **k: flce.embed_bwd(t, x, V=900, **k),
@@ -41,10 +44,13 @@ def _calls():
         "rmsnorm_bwd": lambda **k: flce.rmsnorm_bwd(x, w, rstd, res, **k),
         "ckpt8_pack": lambda **k: flce.ckpt8_pack(x, **k),
         "ckpt8_dw": lambda **k: flce.ckpt8_dw(res, p["q"], p["scale"], **k),
+        "fwd_bwd": lambda **k: flce.fwd_bwd(X, V, y, **k),
+        "fused_linear_jsd": lambda **k: flce.fused_linear_jsd(X, V, Xt, Vt, y, **k),
     }
 
 
-@pytest.mark.parametrize("name", ["embed_fwd", "embed_bwd", "rmsnorm_fwd", "rmsnorm_bwd", "ckpt8_pack", "ckpt8_dw"])
+@pytest.mark.parametrize("name", ["embed_fwd", "embed_bwd", "rmsnorm_fwd", "rmsnorm_bwd", "ckpt8_pack", "ckpt8_dw", "fwd_bwd",
+                                  "fused_linear_jsd"])
 def test_what_a_call_makes_belongs_to_its_stream(name):
     call = _calls()[name]
     want = call()
