@@ -500,7 +500,8 @@ struct SumArgs {
 // A run whose rows lie in several pieces: each piece leaves a partial row, and the block that
 // leaves the last one adds them up in piece order. x: this piece, whose first key is k when the
 // run began before it (head). Returns whether this block is the last; x0: the piece where the
-// run begins, np: the number of pieces. The piece borders are looked at 32 at a time.
+// run begins, np: the number of pieces. The piece borders are looked at 32 at a time (not by the
+// read-only path: the sort may still write the keys when this kernel starts).
 __device__ __forceinline__ bool last_of_run(const SumArgs& a, int x, bool head, uint32_t k, int slice, int& x0, int& np) {
   __shared__ int sh[3];
   __threadfence();
@@ -511,7 +512,7 @@ __device__ __forceinline__ bool last_of_run(const SumArgs& a, int x, bool head, 
     if (head) {
       for (b0 = x - 1;; b0 -= 32) {  // back over the pieces that it runs into from the one before
         const int p = b0 - lane;
-        const bool in = p > 0 && __ldg(a.keys + (int64_t)p * PIECE - 1) == k;
+        const bool in = p > 0 && __ldcg(a.keys + (int64_t)p * PIECE - 1) == k;
         const unsigned m = __ballot_sync(0xffffffffu, in);
         if (m != 0xffffffffu) {
           b0 -= __ffs(~m) - 1;
@@ -522,7 +523,7 @@ __device__ __forceinline__ bool last_of_run(const SumArgs& a, int x, bool head, 
     int n = x - b0 + 1;
     for (;;) {  // and on over those that begin with it
       const int p = b0 + n + lane;
-      const bool in = p < a.pieces && __ldg(a.keys + (int64_t)p * PIECE) == k;
+      const bool in = p < a.pieces && __ldcg(a.keys + (int64_t)p * PIECE) == k;
       const unsigned m = __ballot_sync(0xffffffffu, in);
       n += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
       if (m != 0xffffffffu) break;

@@ -257,6 +257,24 @@ def test_a_stream_of_another_device_is_refused(streams):
         flce.ckpt8_pack(torch.randn(2, 8), stream=s)
 
 
+def test_kernels_that_start_early_do_not_read_by_the_read_only_path():
+    """A kernel that may start before the one it follows has finished (after_previous) reads memory
+    that is written during its life: neither it nor its helpers may use loads for constant data."""
+    seen = 0
+    for name in os.listdir(B.CSRC):
+        with open(os.path.join(B.CSRC, name)) as f:
+            src = f.read()
+        if "after_previous();" not in src:
+            continue
+        assert "__ldg(" not in src and "ld.global.nc" not in src, name
+        for kernel in src.split("__global__")[1:]:
+            head, body = kernel.split("{", 1)
+            if "after_previous();" in body.split("\n}\n")[0]:
+                seen += 1
+                assert "__restrict__" not in head, head
+    assert seen >= 4
+
+
 def _storages(outs):
     return [t.untyped_storage()._cdata for t in outs]
 
