@@ -409,8 +409,9 @@ FLCE_API int32_t flce_ckpt8_pack(const flce_ckpt8_args* args, void* stream);
  * in memory. q * scale is rounded to dy's 16-bit dtype on the way into the tensor cores:
  * exact for bf16 with power-of-two scales. For fp16, and for other scales, it is one more
  * rounding of a value that has 4 significant bits (fp16: saturated at 65504). fp32 dy is split
- * into three bf16 terms (exact). FLCE_FLAG_FORCE_SIMT takes fp32 FMA kernels instead, without
- * any rounding of the operands. The sum is held in fp32 and added to dW with one rounding. */
+ * into three bf16 terms (exact); where a scale is no power of two, so is q * scale, to 2^-22,
+ * at twice the work. FLCE_FLAG_FORCE_SIMT takes fp32 FMA kernels instead, without any rounding
+ * of the operands. The sum is held in fp32 and added to dW with one rounding. */
 typedef struct flce_ckpt8_dw_args {
   int64_t M;                /* rows (tokens), 0 .. 2^29                                  */
   int64_t N;                /* output features: columns of dy, rows of dW                */

@@ -166,7 +166,8 @@ extern "C" int32_t flce_ckpt8_dw(const flce_ckpt8_dw_args* x, void* stream) {
   // without a status word of the caller's: the one flce_get_status reads in a workspace
   int* status = x->status ? (int*)x->status : x->M > 0 ? &((Ctrl*)x->workspace)->status : nullptr;
   cudaError_t e = cudaSuccess;
-  if (status) e = cudaMemsetAsync(status, 0, sizeof(int), s);
+  // (the tensor-core path zeroes it itself)
+  if (status && (x->M == 0 || simt)) e = cudaMemsetAsync(status, 0, sizeof(int), s);
   if (e == cudaSuccess && x->M == 0 && ovw)
     e = cudaMemset2DAsync(x->dW, (size_t)x->lddW * wsz, 0, (size_t)x->K * wsz, (size_t)x->N, s);
   if (e != cudaSuccess || x->M == 0) return cuda_status(e);

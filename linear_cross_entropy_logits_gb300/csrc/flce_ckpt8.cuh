@@ -18,7 +18,8 @@ struct DwArgs {
   int ovw;
 };
 
-// Workspace bytes of the tensor-core path, and its launch. `dt`: dtype of dy; `wdt`: of dW.
+// Workspace bytes of the tensor-core path, and its launch, which zeroes the status word first.
+// `dt`: dtype of dy; `wdt`: of dW.
 size_t dw_tc_workspace(const DwArgs& a, int dt);
 bool dw_tc_supported();
 cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int* status, uint64_t timeout_ns,

@@ -170,6 +170,32 @@ def test_dw_scales_that_are_no_powers_of_two():
     close(got, want, _dw_bound(np64(dy), xs, M, "bf16", "f32", want, 0 * want, True))
 
 
+def _odd_scales(M, nblk, seed):
+    """Scales as the norm's 8-bit output has them: powers of two times any fp32 factor."""
+    g = torch.Generator().manual_seed(seed)
+    return torch.exp2(torch.randint(-6, 7, (M, nblk), generator=g).float()) * (0.5 + torch.rand(M, nblk, generator=g))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 8, 16), (63, 72, 130), (500, 128, 384), (1000, 257, 133), (3000, 520, 300),
+                                   (130, 2000, 1336), (9000, 64, 128)])
+@pytest.mark.parametrize("accumulate", [True, False])
+def test_dw_fp32_gradient_with_any_scales(M, N, K, accumulate):
+    """fp32 dy, whose 24 bits count, times checkpoint values that have as many."""
+    p = flce.ckpt8_pack(_rows(M, K, "f32", M + K, 0.5).cuda())
+    s = _odd_scales(M, (K + 127) // 128, M).cuda()
+    g = torch.Generator().manual_seed(4)
+    dy = torch.randn(M, N, generator=g)
+    init = torch.randn(N, K, generator=g) if accumulate else torch.full((N, K), float("nan"))
+    dW = init.clone().cuda()
+    o = flce.ckpt8_dw(dy.cuda(), p["q"], s, dW=dW, flags=0 if accumulate else flce.FLAG_DW_OVERWRITE)
+    assert o["status_code"] == flce.FLCE_OK
+    x = np64(p["q"]) * oo.spread(np64(s), K)
+    base = np64(init) if accumulate else np.zeros((N, K))
+    want = np64(dy).T @ x + base
+    close(dW, want, _dw_bound(np64(dy), x, M, "f32", "f32", want, base, True))
+    assert rel_fro(np64(dW), want) <= 1e-5
+
+
 def test_dw_non_finite_rows_stay_in_their_columns():
     M, N, K = 70, 64, 256
     x = torch.randn(M, K)
