@@ -38,7 +38,7 @@
 // has up to 24 bits too: it is split in the same way (x0 + x1 + x2, rounded to nearest) as it is
 // expanded, and the products down to 2^-16 of the largest make six passes (those left out: 2^-22).
 // The smallest go first, so that what their additions lose is small too. A kernel in front looks at
-// the scales; the host does not wait. 8192 x 4096 x 4096: 621 us, with six passes 1265.
+// the scales; the host does not wait. 8192 x 4096 x 4096: 615 us, with six passes 1262.
 #include <atomic>
 #include <type_traits>
 
@@ -77,10 +77,9 @@ constexpr int SEG32 = 16;                 // for fp32 dy (1024 rows of a term): 
 constexpr int MAX_SPLIT = 16;
 constexpr int SCAN_BLOCKS = 128;          // of k_scan_scales
 
-// Terms of fp32 dy and of q * scale in pass p, four bits a pass: d0 x2, d1 x1, d0 x1, d2 x0, d1 x0,
-// d0 x0. Scales that are powers of two take the last three.
+// The passes of fp32 dy: d0 x2, d1 x1, d0 x1, d2 x0, d1 x0, d0 x0; where scales are powers of two the
+// last three. The term of dy in pass p, four bits each:
 __device__ __forceinline__ int dy_term(int p) { return 0x012010 >> (4 * p) & 3; }
-__device__ __forceinline__ int q_term(int p) { return 0x000112 >> (4 * p) & 3; }
 
 struct Params {
   DwArgs d;
@@ -590,6 +589,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Threads of columns 64.. take the neighbouring row, so that eight threads' reads (64 bytes of
     // each of two rows) and writes (every other 16-byte chunk of two rows) hit distinct banks
     const int group = (warp - 4) >> 2;
+    const int terms_end = pass0 == 0 ? 3 * p.mstep : 0;  // steps before it take x2 (one pass) or x1 (two)
     const int t = threadIdx.x & 127;
     const int c = t & 7, r = (t >> 3) ^ (c >> 2);
     const uint32_t out = (uint32_t)(c >> 2) * BOX + (uint32_t)r * 128;
@@ -599,7 +599,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     Item it;
     for (int i = pair; ok && get_item(p, steps, i, it); i += npairs) {
-      int row = it.s0 % p.mstep, pass = pass0 + it.s0 / p.mstep;
       for (int st = it.s0; st < it.s1; ++st, ++turn) {
         if (whose == group) {
           ok = bar_wait(full(s), ph, ab, true) && bar_wait(full_s(s), ph, ab, true);
@@ -629,17 +628,12 @@ __global__ void __launch_bounds__(THREADS, 1)
               *(uint4*)(o + j * 2048 + (chunk ^ 16)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
             }
           };
-          const int term = F32 ? q_term(pass) : 0;
-          if (term == 0) expand(std::integral_constant<int, 0>());
-          else if (term == 1) expand(std::integral_constant<int, 1>());
+          if (!F32 || st >= terms_end) expand(std::integral_constant<int, 0>());
+          else if (st >= p.mstep) expand(std::integral_constant<int, 1>());
           else expand(std::integral_constant<int, 2>());
           fence_async();
           __syncwarp();
           if (lane == 0) bar_arrive(mapa(conv(b), 0));
-        }
-        if (F32 && ++row == p.mstep) {
-          row = 0;
-          ++pass;
         }
         if (++s == STAGES) {
           s = 0;
