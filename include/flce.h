@@ -407,8 +407,10 @@ FLCE_API int32_t flce_ckpt8_pack(const flce_ckpt8_args* args, void* stream);
 /* Weight gradient of a projection y = x W^T from the 8-bit checkpoint of its input:
  * dW[n,k] += sum_m dy[m,n] * q[m,k] * scale[m, k / 128], without expanding the checkpoint
  * in memory. q * scale is rounded to dy's 16-bit dtype on the way into the tensor cores:
- * exact for bf16 with power-of-two scales. For fp16, and for other scales, it is one more
- * rounding of a value that has 4 significant bits (fp16: saturated at 65504). fp32 dy is split
+ * exact for bf16 with power-of-two scales; for other scales it is one more rounding of a value
+ * that has 4 significant bits. fp16 counts from the largest scale (of a block that is not all
+ * zeros): values of scales down to 2^-22 of it are exact in the same way, below that they are
+ * off by up to 2^-40 of the largest value that the largest scale allows. fp32 dy is split
  * into three bf16 terms (exact); where a scale is no power of two, so is q * scale, to 2^-22,
  * at twice the work. FLCE_FLAG_FORCE_SIMT takes fp32 FMA kernels instead, without any rounding
  * of the operands. The sum is held in fp32 and added to dW with one rounding. */

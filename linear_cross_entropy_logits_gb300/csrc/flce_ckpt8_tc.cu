@@ -5,7 +5,9 @@
 // The scale varies along m, the axis that is summed over, so it cannot be applied to the
 // product afterwards, and dy keeps its 16 bits, so the 8-bit tensor-core formats do not apply:
 // the checkpoint is expanded to dy's type on the way to the tensor cores, in shared memory,
-// and never in HBM. (bf16: exact where the scales are powers of two.)
+// and never in HBM. (bf16: exact where the scales are powers of two. fp16 has fewer exponents than
+// a checkpoint: a kernel in front finds the largest scale, a power of two brings that to 2^7, and
+// the sums are multiplied back. Exact, then, down to 2^-22 of the largest scale.)
 //
 // Shape: persistent pairs of CTAs (tcgen05 cta_group::2), a pair tile of 256 (n) x 256 (k), 64
 // rows m per step. Each CTA stages its 128 columns of dy (TMA, 16 KB) and its 128 columns of
@@ -76,6 +78,7 @@ constexpr int SEG16 = 32;                 // steps per accumulator for 16-bit dy
 constexpr int SEG32 = 16;                 // for fp32 dy (1024 rows of a term): half that error
 constexpr int MAX_SPLIT = 16;
 constexpr int SCAN_BLOCKS = 128;          // of k_scan_scales
+constexpr int SCAN_LOADS = 8;             // its threads' loads in flight
 
 // The passes of fp32 dy: d0 x2, d1 x1, d0 x1, d2 x0, d1 x0, d0 x0; where scales are powers of two the
 // last three. The term of dy in pass p, four bits each:
@@ -117,19 +120,49 @@ __device__ __forceinline__ bool get_item(const Params& p, int steps, int i, Item
   return true;
 }
 
-// Looks at n scales: each block leaves the exponent 2^(e - 127) that its largest finite magnitude
-// does not pass (0 for none), and 256 where one is no power of two. Zeroes the status word.
-__global__ void __launch_bounds__(256) k_scan_scales(const float* scale, int64_t n, uint32_t* out, int* status) {
+// Whether block blk of q's row m holds a value other than zero.
+__device__ __forceinline__ bool any_value(const DwArgs& d, int64_t m, int64_t blk, bool wide) {
+  const uint8_t* q = d.q + m * d.ldq + blk * Q_BLOCK;
+  const int n = (int)min((int64_t)Q_BLOCK, d.K - blk * Q_BLOCK);
+  if (wide && n == Q_BLOCK) {
+    for (int i = 0; i < Q_BLOCK; i += 16) {
+      const uint4 u = *(const uint4*)(q + i);
+      if (((u.x | u.y | u.z | u.w) & 0x7f7f7f7fu) != 0) return true;
+    }
+  } else {
+    for (int i = 0; i < n; ++i)
+      if ((q[i] & 0x7f) != 0) return true;
+  }
+  return false;
+}
+
+// Looks at the scales: each block leaves the exponent 2^(e - 127) that its largest finite magnitude
+// does not pass (0 for none), and 256 where one is no power of two. A block of zeros has scale 1,
+// which says nothing about the others: with `look`, those are left out. Zeroes the status word.
+__global__ void __launch_bounds__(256) k_scan_scales(const __grid_constant__ DwArgs d, bool look, bool wide, uint32_t* out,
+                                                     int* status) {
   __shared__ uint32_t red[8];
   let_next_start();
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
   uint32_t e = 0, odd = 0;
-#pragma unroll 8
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const uint32_t b = __float_as_uint(scale[i]) & 0x7fffffffu;
-    if (b < 0x7f800000u) {
-      e = max(e, (b + 0x7fffffu) >> 23);
-      odd |= b & 0x7fffffu;
+  constexpr int U = SCAN_LOADS;
+  const int64_t n = d.M * d.nblk, step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += U * step) {
+    uint32_t b[U], ones = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) b[u] = i + u * step < n ? __float_as_uint(d.scale[i + u * step]) & 0x7fffffffu : 0u;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool one = look && b[u] == 0x3f800000u;
+      ones |= (uint32_t)one << u;
+      if (b[u] < 0x7f800000u && !one) {
+        e = max(e, (b[u] + 0x7fffffu) >> 23);
+        odd |= b[u] & 0x7fffffu;
+      }
+    }
+    for (; ones != 0 && e < 127u; ones &= ones - 1) {
+      const int64_t k = i + (__ffs(ones) - 1) * step;
+      if (any_value(d, k / d.nblk, k % d.nblk, wide)) e = 127u;
     }
   }
   e = __reduce_max_sync(0xffffffffu, e);
@@ -155,6 +188,9 @@ __device__ __forceinline__ uint32_t scan_result(const Params& p, int lane) {
   }
   return __reduce_max_sync(0xffffffffu, e) | __reduce_or_sync(0xffffffffu, odd);
 }
+// c of the power of two 2^c that fp16 values are expanded without: the largest scale becomes at
+// most 2^7, its largest value 448 * 2^7 = 57344. e: what the scan found (2^-110 at least).
+__device__ __forceinline__ int fp16_shift(uint32_t e) { return max((int)(e & 255u) - 127, -110) - 7; }
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -162,7 +198,7 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   if constexpr (std::is_same<T, __nv_bfloat16>::value)
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   else
-    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
@@ -408,6 +444,7 @@ template <typename T, typename D, bool F32>
 __global__ void __launch_bounds__(THREADS, 1)
     k_dw_tc8(const __grid_constant__ CUtensorMap tm_dy, const __grid_constant__ CUtensorMap tm_q,
              const __grid_constant__ Params p) {
+  constexpr bool F16 = std::is_same<T, __half>::value;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint64_t* bars = (uint64_t*)(smem + OFF_BARS);
@@ -589,6 +626,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Threads of columns 64.. take the neighbouring row, so that eight threads' reads (64 bytes of
     // each of two rows) and writes (every other 16-byte chunk of two rows) hit distinct banks
     const int group = (warp - 4) >> 2;
+    const float unit = F16 ? exp2_int(-fp16_shift(scan_result(p, lane))) : 1.0f;
     const int terms_end = pass0 == 0 ? 3 * p.mstep : 0;  // steps before it take x2 (one pass) or x1 (two)
     const int t = threadIdx.x & 127;
     const int c = t & 7, r = (t >> 3) ^ (c >> 2);
@@ -612,8 +650,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (!ok) break;
           const uint8_t* q = smem + s * STAGE_BYTES + A_BYTES + r * 128 + c * 16;
           uint8_t* o = smem + OFF_B + b * B_BYTES + out;
-          const float4 f = *(const float4*)(smem + OFF_S + s * S_BYTES + r * 16);
-          const float sc[4] = {f.x, f.y, f.z, f.w};
+          const float4 sc4 = *(const float4*)(smem + OFF_S + s * S_BYTES + r * 16);
+          const float sc[4] = {sc4.x, sc4.y, sc4.z, sc4.w};
           uint4 u[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) u[j] = *(const uint4*)(q + j * 2048);
@@ -621,7 +659,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             constexpr int TERM = decltype(term)::value;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const f2 sc2 = f2_make(sc[j], sc[j]);
+              const float f = F16 ? sc[j] * unit : sc[j];
+              const f2 sc2 = f2_make(f, f);
               const uint2 x0 = expand4<T, TERM>(u[j].x, sc2), x1 = expand4<T, TERM>(u[j].y, sc2);
               const uint2 x2 = expand4<T, TERM>(u[j].z, sc2), x3 = expand4<T, TERM>(u[j].w, sc2);
               *(uint4*)(o + j * 2048 + chunk) = make_uint4(x0.x, x0.y, x1.x, x1.y);
@@ -650,6 +689,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int w = warp - 4 - CONV_WARPS, quad = warp & 3, h = w >> 2;
     const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(h * 128);
     const uint32_t stage = smem_u32(smem + OFF_OUT + w * OUT_BYTES);
+    const float unit = F16 ? exp2_int(fp16_shift(scan_result(p, lane))) : 1.0f;
     int g = 0;
     bool ok = true;
     Item it;
@@ -677,7 +717,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t r[16];
           tmem_ld16(taddr + (uint32_t)(as * TILE + j * 16), r);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) acc[j * 16 + e] += __uint_as_float(r[e]);
+          for (int e = 0; e < 16; ++e) {
+            const float v = __uint_as_float(r[e]);
+            acc[j * 16 + e] = F16 ? fmaf(v, unit, acc[j * 16 + e]) : acc[j * 16 + e] + v;
+          }
         }
         tc_before();
         __syncwarp();
@@ -826,7 +869,7 @@ struct Plan8 {
 // Rows that TMA cannot read in place.
 bool stage_dy(const DwArgs& a, int dt) { return dt == FLCE_F32 || !rows16(a.dy, a.lddy, 2); }
 // Whether the kernel needs to know the scales' range.
-bool dw_tc_scans(int dt) { return dt == FLCE_F32; }
+bool dw_tc_scans(int dt) { return dt != FLCE_BF16; }
 bool stage_q(const DwArgs& a) { return !rows16(a.q, a.ldq, 1); }
 
 // Whole tiles fill whole waves of pairs; the rest are split S ways, S minimising the steps of
@@ -873,7 +916,7 @@ Plan8 plan(const DwArgs& a, int dt) {
 }
 
 template <typename T, typename D, bool F32>
-cudaError_t launch(const CUtensorMap& A, const CUtensorMap& Q, const Params& p, int64_t items, bool staged,
+cudaError_t launch(const CUtensorMap& A, const CUtensorMap& Q, const Params& p, int64_t items, bool behind,
                    cudaStream_t s) {
   auto kern = k_dw_tc8<T, D, F32>;
   // per-device cache of the pairs that fit at once; concurrent first launches may both set it
@@ -891,7 +934,7 @@ cudaError_t launch(const CUtensorMap& A, const CUtensorMap& Q, const Params& p, 
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // it starts up while operands are staged
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // it starts up beside the kernel in front
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -906,7 +949,7 @@ cudaError_t launch(const CUtensorMap& A, const CUtensorMap& Q, const Params& p, 
     fit[dev].store(n, std::memory_order_relaxed);
   }
   cfg.gridDim = dim3(2 * (unsigned)(items < n ? items : n), 1, 1);
-  cfg.numAttrs = staged ? 2 : 1;
+  cfg.numAttrs = behind ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, A, Q, p);
   if (e != cudaSuccess || p.S == 1) return e;
   const int64_t split = (int64_t)p.tn * p.tk - p.whole;
@@ -941,9 +984,10 @@ cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int
   p.access = rows16(a.dW, a.lddW, wsz) ? 16 : wsz == 4 || (a.K % 2 == 0 && rows_by(a.dW, a.lddW, wsz, 4)) ? 4 : 2;
   cudaError_t e;
   if (dw_tc_scans(dt)) {
-    const int64_t n = a.M * a.nblk, most = cdiv64(n, 2048);  // eight scales a thread
+    const int64_t n = a.M * a.nblk, most = cdiv64(n, 256 * SCAN_LOADS);
     p.nscan = (int)(most < SCAN_BLOCKS ? most : SCAN_BLOCKS);
-    k_scan_scales<<<(unsigned)p.nscan, 256, 0, s>>>(a.scale, n, (uint32_t*)(ws + pl.off_scan), status);
+    k_scan_scales<<<(unsigned)p.nscan, 256, 0, s>>>(a, dt == FLCE_F16, rows16(a.q, a.ldq, 1),
+                                                    (uint32_t*)(ws + pl.off_scan), status);
     e = cudaGetLastError();
   } else {
     e = cudaMemsetAsync(status, 0, sizeof(int), s);
@@ -982,13 +1026,13 @@ cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int
       !ptx::encode_2d(&Q, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, a.K, a.M, ldq, 128, BK, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   const int64_t items = p.whole + ((int64_t)p.tn * p.tk - p.whole) * p.S;
-  const bool staged = stage_dy(a, dt) || stage_q(a);
+  const bool behind = dw_tc_scans(dt) || stage_dy(a, dt) || stage_q(a);  // another kernel of this call
   if (dt == FLCE_F16)
-    return wdt == FLCE_F32 ? launch<__half, float, false>(A, Q, p, items, staged, s)
-                           : launch<__half, __half, false>(A, Q, p, items, staged, s);
-  if (dt == FLCE_F32) return launch<__nv_bfloat16, float, true>(A, Q, p, items, staged, s);
-  if (wdt == FLCE_F32) return launch<__nv_bfloat16, float, false>(A, Q, p, items, staged, s);
-  return launch<__nv_bfloat16, __nv_bfloat16, false>(A, Q, p, items, staged, s);
+    return wdt == FLCE_F32 ? launch<__half, float, false>(A, Q, p, items, behind, s)
+                           : launch<__half, __half, false>(A, Q, p, items, behind, s);
+  if (dt == FLCE_F32) return launch<__nv_bfloat16, float, true>(A, Q, p, items, behind, s);
+  if (wdt == FLCE_F32) return launch<__nv_bfloat16, float, false>(A, Q, p, items, behind, s);
+  return launch<__nv_bfloat16, __nv_bfloat16, false>(A, Q, p, items, behind, s);
 }
 
 }  // namespace flce

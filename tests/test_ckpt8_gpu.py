@@ -196,6 +196,102 @@ def test_dw_fp32_gradient_with_any_scales(M, N, K, accumulate):
     assert rel_fro(np64(dW), want) <= 1e-5
 
 
+def _fp16_rows(kind, M, K, g):
+    x = torch.randn(M, K, generator=g)
+    if kind == "large":                       # past fp16's largest value
+        return x * 3e6
+    if kind == "small":                       # below its smallest
+        return x * 1e-10
+    if kind == "rows":                        # rows 2^-20 ... 1 of the largest
+        return x * torch.exp2(16 - torch.randint(0, 21, (M, 1), generator=g).float())
+    e = torch.randint(0, 61, (M, (K + 127) // 128), generator=g).float().repeat_interleave(128, dim=1)[:, :K]
+    return x * torch.exp2(30 - e)             # "far": blocks 2^-60 ... 1 of the largest
+
+
+@pytest.mark.parametrize("kind", ["large", "small", "rows", "far"])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 16), (65, 264, 272), (1531, 136, 390), (4100, 520, 133)])
+@pytest.mark.parametrize("wdt,accumulate", [("f32", True), ("f32", False), ("f16", False)])
+def test_dw_fp16_gradient_of_checkpoints_of_any_size(kind, M, N, K, wdt, accumulate):
+    """The checkpoint need not fit fp16. With e the exponent of the largest scale, its values are
+    exact down to 2^(e - 31) and off by 2^(e - 32) below; the largest value is over 224 * 2^e."""
+    g = torch.Generator().manual_seed(M + N)
+    p = flce.ckpt8_pack(_fp16_rows(kind, M, K, g).cuda())
+    x = np64(p["q"]) * oo.spread(np64(p["scale"]), K)
+    # (fp16 results stay in range)
+    unit = 1.0 if wdt == "f32" else 2.0 ** -np.ceil(np.log2(np.abs(x).max() * M))
+    x = x * unit
+    s = p["scale"] * unit
+    dy = (torch.randn(M, N, generator=g) * 0.3).half()
+    base = torch.randn(N, K, generator=g).float() * np.abs(x).max() if accumulate else torch.zeros(N, K)
+    dW = base.to(DT[wdt]).cuda()
+    flce.ckpt8_dw(dy.cuda(), p["q"], s, dW=dW, flags=0 if accumulate else flce.FLAG_DW_OVERWRITE)
+    base = np64(base)
+    want = np64(dy).T @ x + base
+    bound = _dw_bound(np64(dy), x, M, "f16", wdt, want, base, False)
+    bound += 2.0 ** -39 * np.abs(x).max() * np.abs(np64(dy)).sum(axis=0)[:, None]
+    close(dW, want, bound)
+    if wdt == "f32" and kind != "far":
+        assert rel_fro(np64(dW), want) <= 1e-5
+
+
+def test_dw_fp16_gradient_of_the_norms_checkpoint():
+    """h = x + r of fp16 values can pass fp16's range; its checkpoint holds it."""
+    M, N, K = 300, 64, 256
+    g = torch.Generator().manual_seed(12)
+    x = (50000 + 10000 * torch.rand(M, K, generator=g)).half().cuda()
+    o = flce.rmsnorm_fwd(x, torch.ones(K, dtype=torch.float16, device="cuda"), x, want_h=False, want_h8=True)
+    h = np64(o["h8"]) * oo.spread(np64(o["h8_scale"]), K)
+    assert h.max() > 65504
+    dy = (torch.randn(M, N, generator=g) * 0.01).half()
+    got = flce.ckpt8_dw(dy.cuda(), o["h8"], o["h8_scale"])["dW"]
+    assert rel_fro(np64(got), np64(dy).T @ h) <= 1e-5
+
+
+@pytest.mark.parametrize("K,extra,offset", [(272, 0, 0), (256, 16, 0), (390, 3, 1), (130, 0, 0)])
+@pytest.mark.parametrize("one", [False, True])
+def test_dw_fp16_gradient_beside_blocks_of_zeros(K, extra, offset, one):
+    """A block of zeros has scale 1 whatever the others have, and a block whose scale is 1 may
+    hold a single value, its last."""
+    M, N = 700, 72
+    g = torch.Generator().manual_seed(K)
+    x = torch.randn(M, K, generator=g) * 1e-9
+    x[::3] = 0
+    x[1::3, :128] = 0
+    x[2::3, K // 128 * 128 - 128:] = 0
+    if one:
+        x[0, 127] = 400.0
+        x[3, K - 1] = -300.0
+    p = flce.ckpt8_pack(x.cuda())
+    assert (p["scale"] == 1).any()
+    q = strided(p["q"], extra, offset)
+    dy = (torch.randn(M, N, generator=g) * 0.3).half()
+    xs = np64(p["q"]) * oo.spread(np64(p["scale"]), K)
+    want = np64(dy).T @ xs
+    got = flce.ckpt8_dw(dy.cuda(), q, p["scale"])["dW"]
+    bound = _dw_bound(np64(dy), xs, M, "f16", "f32", want, 0 * want, False)
+    close(got, want, bound + 2.0 ** -39 * np.abs(xs).max() * np.abs(np64(dy)).sum(axis=0)[:, None])
+    assert rel_fro(np64(got), want) <= 1e-5
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_dw_scales_that_are_not_finite(dt, bad):
+    """They spoil their block's columns and no others."""
+    M, N, K = 200, 72, 300
+    g = torch.Generator().manual_seed(13)
+    x = 1 + torch.rand(M, K, generator=g)
+    p = flce.ckpt8_pack(x.cuda())
+    s = p["scale"].clone()
+    s[77, 1] = bad
+    dy = (1 + torch.rand(M, N, generator=g)).to(DT[dt])
+    dW = np64(flce.ckpt8_dw(dy.cuda(), p["q"], s)["dW"])
+    assert not np.isfinite(dW[:, 128:256]).any()
+    xs = np64(p["q"]) * oo.spread(np64(p["scale"]), K)
+    want = np64(dy).T @ xs
+    keep = np.r_[0:128, 256:300]
+    assert rel_fro(dW[:, keep], want[:, keep]) <= 1e-5
+
+
 def test_dw_non_finite_rows_stay_in_their_columns():
     M, N, K = 70, 64, 256
     x = torch.randn(M, K)
