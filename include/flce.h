@@ -413,7 +413,8 @@ FLCE_API int32_t flce_ckpt8_pack(const flce_ckpt8_args* args, void* stream);
  * off by up to 2^-40 of the largest value that the largest scale allows. fp32 dy is split
  * into three bf16 terms (exact); where a scale is no power of two, so is q * scale, to 2^-22,
  * at twice the work. FLCE_FLAG_FORCE_SIMT takes fp32 FMA kernels instead, without any rounding
- * of the operands. The sum is held in fp32 and added to dW with one rounding. */
+ * of the operands. The sum is held in fp32 and added to dW with one rounding. If a wait runs
+ * out (FLCE_ERR_TIMEOUT), the tiles of dW that were not finished are NaN. */
 typedef struct flce_ckpt8_dw_args {
   int64_t M;                /* rows (tokens), 0 .. 2^29                                  */
   int64_t N;                /* output features: columns of dy, rows of dW                */

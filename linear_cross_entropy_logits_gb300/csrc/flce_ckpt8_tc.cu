@@ -693,13 +693,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     int g = 0;
     bool ok = true;
     Item it;
-    for (int i = pair; ok && get_item(p, steps, i, it); i += npairs) {
+    // (a pair that gave up writes NaN to the tiles that it has not finished: nobody may look at the
+    // status word)
+    for (int i = pair; get_item(p, steps, i, it); i += npairs) {
       const int row = (int)rank * 128 + quad * 32, col = h * 128;  // within the tile
       const int64_t n = (int64_t)(it.tile / p.tk) * TILE + row, k = (int64_t)(it.tile % p.tk) * TILE + col;
       const Out<D> out{(D*)p.d.dW + n * p.d.lddW + k, p.d.lddW, (int)min(p.d.N - n, (int64_t)32),
                        (int)min(p.d.K - k, (int64_t)128), stage};
       float acc[128];
-      if (sizeof(D) == 2 && it.part < 0 && !p.d.ovw) {
+      if (sizeof(D) == 2 && it.part < 0 && !p.d.ovw && ok) {
         if (p.access == 16) out.start(acc, lane);
         else if (p.access == 4) out.template start_narrow<4>(acc, lane);
         else out.template start_narrow<2>(acc, lane);
@@ -707,7 +709,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
       }
-      for (int st = it.s0; st < it.s1; st += p.seg, ++g) {
+      for (int st = it.s0; ok && st < it.s1; st += p.seg, ++g) {
         const int as = g & 1;
         ok = __all_sync(0xffffffffu, bar_wait(tfull(as), (uint32_t)(g >> 1) & 1u, ab, true));
         if (!ok) break;
@@ -726,7 +728,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) bar_arrive(mapa(tempty(as), 0));
       }
-      if (!ok) break;
+      if (!ok) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) acc[j] = NAN;
+      }
       if (it.part >= 0) {
         const int64_t slot = (int64_t)(it.tile - p.whole) * p.S + it.part;
         const Out<float> part{p.part + slot * TILE * TILE + row * TILE + col, TILE, 32, 128, stage};

@@ -356,6 +356,27 @@ def test_dw_wait_limit():
     assert b["status_code"] == flce.FLCE_OK and torch.equal(a, b["dW"])
 
 
+@pytest.mark.parametrize("dt,wdt", [("bf16", "f32"), ("bf16", "bf16"), ("f16", "f16"), ("f32", "f32")])
+@pytest.mark.parametrize("M", [60, 5000])
+@pytest.mark.parametrize("accumulate", [True, False])
+def test_dw_wait_limit_leaves_nan(dt, wdt, M, accumulate):
+    """A caller who does not look at the status sees it in dW: the tile that a pair gave up on is
+    NaN (60 rows: whole, 5000: the sum of parts), the others are right."""
+    N, K = 300, 520
+    g = torch.Generator().manual_seed(M)
+    p = flce.ckpt8_pack(torch.randn(M, K, generator=g).cuda())
+    dy = torch.randn(M, N, generator=g).to(DT[dt]).cuda()
+    init = torch.randn(N, K, generator=g).to(DT[wdt]).cuda()
+    flags = 0 if accumulate else flce.FLAG_DW_OVERWRITE
+    a, b = init.clone(), init.clone()
+    flce.ckpt8_dw(dy, p["q"], p["scale"], dW=a, flags=flags)
+    o = flce.ckpt8_dw(dy, p["q"], p["scale"], dW=b, flags=flags | flce.FLAG_DEBUG_STALL, wait_timeout_ms=50)
+    assert o["status_code"] == flce.FLCE_ERR_TIMEOUT
+    assert torch.isnan(b[:256, :256]).all()
+    a[:256, :256] = b[:256, :256] = 0
+    assert torch.equal(a, b)
+
+
 def test_calls_in_a_graph():
     """The operators enqueue kernels and memsets only: captured once, replayed on new inputs."""
     g = torch.Generator().manual_seed(10)
