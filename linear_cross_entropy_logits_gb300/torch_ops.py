@@ -176,12 +176,16 @@ def fused_linear_cross_entropy(X, W, targets, bias=None, *, ignore_index=-100, r
 # ---------------------------------------------------------------------------------------
 
 @torch.library.custom_op("flce_gb300::embedding", mutates_args=())
-def embedding_op(tokens: torch.Tensor, E: torch.Tensor, scale: float, ignore_index: int) -> torch.Tensor:
-    return flce.embed_fwd(tokens.contiguous(), E, scale=scale, ignore_index=ignore_index, check=False)["out"]
+def embedding_op(tokens: torch.Tensor, E: torch.Tensor, scale: float, ignore_index: int,
+                 check: bool = False) -> torch.Tensor:
+    o = flce.embed_fwd(tokens.contiguous(), E, scale=scale, ignore_index=ignore_index, check=check)
+    if check and o["status_code"] != flce.FLCE_OK:
+        raise flce.FlceError(o["status_code"], "embedding")
+    return o["out"]
 
 
 @embedding_op.register_fake
-def _(tokens, E, scale, ignore_index):
+def _(tokens, E, scale, ignore_index, check=False):
     return E.new_empty(tokens.shape[0], E.shape[1])
 
 
@@ -199,7 +203,7 @@ def _(tokens, dout, V, scale, ignore_index):
 
 
 def _embedding_setup(ctx, inputs, output):
-    tokens, E, scale, ignore_index = inputs
+    tokens, E, scale, ignore_index, check = inputs
     ctx.save_for_backward(tokens)
     ctx.args = (E.shape[0], scale, ignore_index)
 
@@ -207,17 +211,18 @@ def _embedding_setup(ctx, inputs, output):
 def _embedding_backward(ctx, g):
     tokens, = ctx.saved_tensors
     V, scale, ignore_index = ctx.args
-    return None, embedding_bwd_op(tokens, g, V, scale, ignore_index), None, None
+    return None, embedding_bwd_op(tokens, g, V, scale, ignore_index), None, None, None
 
 
 embedding_op.register_autograd(_embedding_backward, setup_context=_embedding_setup)
 
 
-def embedding(tokens, E, *, scale=1.0, ignore_index=-100):
+def embedding(tokens, E, *, scale=1.0, ignore_index=-100, check=False):
     """scale * E[tokens], a zero row where tokens == ignore_index; differentiable in E (a dense
     gradient in E's dtype, each row summed in fp32 in a fixed order). tokens: int64 of any
-    shape; E [V, H]."""
-    return embedding_op(tokens.reshape(-1), E, float(scale), ignore_index).reshape(*tokens.shape, E.shape[1])
+    shape; E [V, H]. A token outside [0, V) gives a zero row and no gradient; ``check`` raises
+    FlceError for it instead, which waits for the stream."""
+    return embedding_op(tokens.reshape(-1), E, float(scale), ignore_index, check).reshape(*tokens.shape, E.shape[1])
 
 
 def _rows(x):

@@ -58,6 +58,20 @@ def test_embedding():
     assert a.grad.dtype == E.dtype
 
 
+def test_embedding_of_tokens_out_of_range():
+    E = _leaf(torch.randn(5, 16, device="cuda"))
+    t = torch.tensor([[1, 5], [-3, -100]], device="cuda")
+    out = torch_ops.embedding(t, E)
+    assert torch.equal(out[0, 0], E[1]) and torch.all(out[0, 1] == 0) and torch.all(out[1] == 0)
+    out.sum().backward()
+    assert E.grad.sum(dim=1).tolist() == [0, 16, 0, 0, 0]
+    for bad in (t, t[:1], t[1:]):
+        with pytest.raises(flce.FlceError) as e:
+            torch_ops.embedding(bad, E, check=True)
+        assert e.value.code == flce.FLCE_ERR_TARGET_RANGE
+    assert torch.equal(torch_ops.embedding(t[1:, 1:], E, check=True), torch.zeros(1, 1, 16, device="cuda"))
+
+
 @pytest.mark.parametrize("residual", [True, False])
 @pytest.mark.parametrize("checkpoint8,tol", [(False, 1e-5), (True, 0.036)])
 def test_add_rms_norm(residual, checkpoint8, tol):
