@@ -341,21 +341,21 @@ class LinearCkpt8(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, W):
-        need = ctx.needs_input_grad[1]
-        q, scale = ckpt8_pack_op(x) if need else (None, None)
-        ctx.save_for_backward(W, q, scale)
+        ctx.save_for_backward(W, *ckpt8_pack_op(x))
         return torch.mm(x, W.t())
 
     @staticmethod
     def backward(ctx, dy):
         W, q, scale = ctx.saved_tensors
         dx = torch.mm(dy, W) if ctx.needs_input_grad[0] else None
-        dW = ckpt8_dw_op(dy, q, scale, W.dtype == torch.float32) if ctx.needs_input_grad[1] else None
-        return dx, dW
+        return dx, ckpt8_dw_op(dy, q, scale, W.dtype == torch.float32)
 
 
 def linear_ckpt8(x, W):
     """x W^T for x [..., K] and W [N, K] of one dtype; the backward's dW = dy^T x reads an 8-bit
     checkpoint of x (its rounding, half of 2^-3 of a value, is the only approximation; dx is
-    exact). x itself is not kept."""
-    return LinearCkpt8.apply(x.reshape(-1, x.shape[-1]), W).reshape(*x.shape[:-1], W.shape[0])
+    exact). x itself is not kept. Without a gradient of W to come (frozen, or in evaluation) it is
+    a plain product."""
+    rows = x.reshape(-1, x.shape[-1])
+    y = LinearCkpt8.apply(rows, W) if torch.is_grad_enabled() and W.requires_grad else torch.mm(rows, W.t())
+    return y.reshape(*x.shape[:-1], W.shape[0])

@@ -275,6 +275,41 @@ def test_kernels_that_start_early_do_not_read_by_the_read_only_path():
     assert seen >= 5
 
 
+@pytest.fixture
+def plain_ckpt8(monkeypatch):
+    """linear_ckpt8 on the CPU: packing and the weight gradient in plain torch; counts the packings."""
+    calls = []
+
+    def pack(x):
+        calls.append(x.shape)
+        return {"q": x.detach().to(torch.float8_e4m3fn), "scale": torch.ones(len(x), (x.shape[1] + 127) // 128)}
+
+    def dw(dy, q, scale, *, dW, flags, check):
+        dW.copy_(dy.float().t() @ q.float())
+
+    monkeypatch.setattr(flce, "ckpt8_pack", pack)
+    monkeypatch.setattr(flce, "ckpt8_dw", dw)
+    return calls
+
+
+def test_linear_ckpt8_packs_only_for_a_gradient_of_its_weight(plain_ckpt8):
+    x, W = torch.randn(3, 5, 40, requires_grad=True), torch.randn(7, 40, requires_grad=True)
+    want = x.detach() @ W.detach().t()
+    with torch.no_grad():
+        assert torch.equal(torch_ops.linear_ckpt8(x, W), want)
+    with torch.inference_mode():
+        torch_ops.linear_ckpt8(x, W)
+    frozen = torch_ops.linear_ckpt8(x, W.detach())
+    assert frozen.requires_grad and not plain_ckpt8
+    frozen.sum().backward()
+    assert torch.allclose(x.grad, W.detach().sum(0).expand_as(x))
+    y = torch_ops.linear_ckpt8(x.detach(), W)
+    assert torch.equal(y.detach(), want) and plain_ckpt8 == [(15, 40)]
+    y.sum().backward()
+    q = x.detach().reshape(15, 40).to(torch.float8_e4m3fn).float()
+    assert torch.allclose(W.grad, q.sum(0).expand(7, 40))
+
+
 def _storages(outs):
     return [t.untyped_storage()._cdata for t in outs]
 
