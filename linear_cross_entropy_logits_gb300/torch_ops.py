@@ -347,7 +347,8 @@ class LinearCkpt8(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         W, q, scale = ctx.saved_tensors
-        dx = torch.mm(dy, W) if ctx.needs_input_grad[0] else None
+        # (under autocast y and dy have its type; autograd takes dx and dW to x's and W's)
+        dx = torch.mm(dy, W.to(dy.dtype)) if ctx.needs_input_grad[0] else None
         return dx, ckpt8_dw_op(dy, q, scale, W.dtype == torch.float32)
 
 

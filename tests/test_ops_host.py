@@ -310,6 +310,26 @@ def test_linear_ckpt8_packs_only_for_a_gradient_of_its_weight(plain_ckpt8):
     assert torch.allclose(W.grad, q.sum(0).expand(7, 40))
 
 
+@pytest.mark.parametrize("x_dtype", [torch.float32, torch.bfloat16])
+def test_linear_ckpt8_under_autocast(plain_ckpt8, x_dtype):
+    """fp32 weights, a 16-bit product: gradients come back in the types of x and W."""
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(6, 40, generator=g).to(x_dtype).requires_grad_()
+    W = torch.randn(7, 40, generator=g).requires_grad_()
+    with torch.autocast("cpu", torch.bfloat16):
+        y = torch_ops.linear_ckpt8(x, W)
+    assert y.dtype is torch.bfloat16
+    c = torch.randn(6, 7, generator=g).bfloat16()
+    y.backward(c)
+    assert x.grad.dtype is x_dtype and W.grad.dtype is torch.float32
+    Wb = W.detach().bfloat16().double()
+    # sums of 7 products of bf16 values, rounded to bf16
+    close = lambda a, b, tol: ((a.double() - b).abs() <= tol).all()  # noqa: E731
+    assert close(x.grad, c.double() @ Wb, 2.0 ** -8 * (c.double().abs() @ Wb.abs()))
+    q = x.detach().to(torch.float8_e4m3fn).double()
+    assert close(W.grad, c.double().t() @ q, 2.0 ** -20 * (c.double().abs().t() @ q.abs()))
+
+
 def _storages(outs):
     return [t.untyped_storage()._cdata for t in outs]
 
