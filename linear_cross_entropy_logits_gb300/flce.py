@@ -625,7 +625,10 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, weight_offset=0.0, want_y
     lib = _lib or load()
     dev, (N, H), dt = _cuda_2d("x", x)
     dtype = x.dtype
-    o = dict(outputs) if outputs else {}
+    if want_h is None:
+        want_h = residual is not None
+    o = {} if outputs is None else _wanted(outputs, rstd=True, y=want_y, h=want_h, y8=want_y8, y8_scale=want_y8,
+                                           h8=want_h8, h8_scale=want_h8)
     given = o.get
     px, ldx = _matrix("x", x, N, H, dtype, dev)
     pr, ldr = (None, 0) if residual is None else _matrix("residual", residual, N, H, dtype, dev)
@@ -636,8 +639,6 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, weight_offset=0.0, want_y
     else:
         prstd = _dense("rstd", rstd, (N,), torch.float32, dev)
     (py, ldy) = _row_output(o, "y", x, N, H, dtype, dev) if want_y else (None, 0)
-    if want_h is None:
-        want_h = residual is not None
     (ph, ldh) = _row_output(o, "h", x, N, H, dtype, dev) if want_h else (None, 0)
     (py8, ldy8, psy) = _rows8(o, "y8", "y8_scale", N, H, dev) if want_y8 else (None, 0, None)
     (ph8, ldh8, psh) = _rows8(o, "h8", "h8_scale", N, H, dev) if want_h8 else (None, 0, None)
@@ -645,6 +646,11 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, weight_offset=0.0, want_y
                         ph, ldh, py, ldy, prstd, py8, ldy8, psy, ph8, ldh8, psh)
     _launch(lib.flce_rmsnorm_fwd, "flce_rmsnorm_fwd", a, dev)
     return o
+
+
+def _wanted(outputs, **wanted):
+    """The given outputs that the call writes; others (of an earlier call, say) are not passed on."""
+    return {k: t for k, t in outputs.items() if wanted.get(k)}
 
 
 def _row_output(o, key, like, N, H, dtype, dev):
@@ -684,7 +690,7 @@ def rmsnorm_bwd(dy, weight, rstd, h=None, *, h8=None, h8_scale=None, dh=None, we
     dtype = dy.dtype
     if (h is None) == (h8 is None) or (h8 is not None and h8_scale is None):
         raise ValueError("rmsnorm_bwd takes h, or h8 with h8_scale")
-    o = dict(outputs) if outputs else {}
+    o = {} if outputs is None else _wanted(outputs, dx=want_dx)
     (pdx, lddx) = _row_output(o, "dx", dy, N, H, dtype, dev) if want_dx else (None, 0)
     pw = pws = None
     wbytes, wdt = 0, 0
@@ -719,7 +725,7 @@ def ckpt8_pack(x, *, outputs=None, stream=None):
         return _on(stream, ckpt8_pack, locals())
     lib = _lib or load()
     dev, (N, H), dt = _cuda_2d("x", x)
-    o = dict(outputs) if outputs else {}
+    o = {} if outputs is None else _wanted(outputs, q=True, scale=True)
     px, ldx = _matrix("x", x, N, H, x.dtype, dev)
     pq, ldq, ps = _rows8(o, "q", "scale", N, H, dev)
     _launch(lib.flce_ckpt8_pack, "flce_ckpt8_pack", FlceCkpt8Args(N, H, dt, 0, px, ldx, pq, ldq, ps), dev)

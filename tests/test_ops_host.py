@@ -250,6 +250,23 @@ def test_a_given_stream_owns_what_the_call_makes(lib, streams, name):
     assert not [e for e in log if e[0] == "record"]
 
 
+def test_results_hold_nothing_that_the_call_did_not_write(lib, streams):
+    """Outputs of an earlier call given again, with fewer of them wanted."""
+    x, w = torch.randn(6, 8), torch.ones(8)
+    a = flce.rmsnorm_fwd(x, w, x.clone(), want_y8=True, want_h8=True)
+    assert set(a) == {"rstd", "y", "h", "y8", "y8_scale", "h8", "h8_scale"}
+    b = flce.rmsnorm_fwd(x, w, outputs=a)
+    assert set(b) == {"rstd", "y"} and b["y"] is a["y"] and b["rstd"] is a["rstd"]
+    assert set(flce.rmsnorm_fwd(x, w, want_y=False, want_h8=True, outputs=a)) == {"rstd", "h8", "h8_scale"}
+    c = flce.rmsnorm_bwd(x, w, a["rstd"], x)
+    assert set(c) == {"dx", "dweight", "workspace"}
+    assert set(flce.rmsnorm_bwd(x, w, a["rstd"], x, want_dweight=False, outputs=c)) == {"dx"}
+    d = flce.rmsnorm_bwd(x, w, a["rstd"], x, want_dx=False, outputs=c)
+    assert set(d) == {"dweight", "workspace"} and d["dweight"] is not c["dweight"]
+    p = flce.ckpt8_pack(x)
+    assert set(flce.ckpt8_pack(x, outputs=dict(p, y=x))) == {"q", "scale"}
+
+
 def test_a_stream_of_another_device_is_refused(streams):
     s = _Stream()
     s.device = torch.device("meta")
