@@ -398,7 +398,7 @@ typedef struct flce_ckpt8_args {
   const void* x;            /* [N,H]                                                     */
   int64_t ldx;
   void* q;                  /* [N,H] e4m3                                                */
-  int64_t ldq;              /* a multiple of 16 lets flce_ckpt8_dw take tensor cores     */
+  int64_t ldq;              /* a multiple of 16: flce_ckpt8_dw reads it in place         */
   float* scale;             /* [N, cdiv(H,128)]                                          */
 } flce_ckpt8_args;
 
@@ -413,8 +413,9 @@ FLCE_API int32_t flce_ckpt8_pack(const flce_ckpt8_args* args, void* stream);
  * off by up to 2^-40 of the largest value that the largest scale allows. fp32 dy is split
  * into three bf16 terms (exact); where a scale is no power of two, so is q * scale, to 2^-22,
  * at twice the work. FLCE_FLAG_FORCE_SIMT takes fp32 FMA kernels instead, without any rounding
- * of the operands. The sum is held in fp32 and added to dW with one rounding. If a wait runs
- * out (FLCE_ERR_TIMEOUT), the tiles of dW that were not finished are NaN. */
+ * of the operands. The sum is held in fp32 and added to dW with one rounding (an addition to
+ * an fp32 dW takes values below 2^-126 as zero). If a wait runs out (FLCE_ERR_TIMEOUT), the
+ * tiles of dW that were not finished are NaN. */
 typedef struct flce_ckpt8_dw_args {
   int64_t M;                /* rows (tokens), 0 .. 2^29                                  */
   int64_t N;                /* output features: columns of dy, rows of dW                */
@@ -438,9 +439,10 @@ typedef struct flce_ckpt8_dw_args {
 
 FLCE_API int32_t flce_ckpt8_dw(const flce_ckpt8_dw_args* args, void* stream);
 /* Workspace bytes that flce_ckpt8_dw needs for these arguments (0 on invalid sizes or dtype);
- * the fields from workspace on are not looked at. Partial sums of a part of the output tiles,
- * tens of MB at most; fp32 dy adds 6 bytes an element, and rows of dy or q that do not start at
- * multiples of 16 bytes a copy of that operand. Host-only. */
+ * the fields from workspace on are not looked at. Partial sums of output tiles: up to 16 parts
+ * of 256 KB for fewer tiles than there are pairs of SMs: 300 MB at most on 152 SMs, reached with
+ * very many rows (4096 x 4096 over 8192 rows: 15 MB). fp32 dy adds 6 bytes an element, and rows of dy or q that
+ * do not start at multiples of 16 bytes a copy of that operand. Host-only. */
 FLCE_API size_t flce_ckpt8_dw_workspace_size(const flce_ckpt8_dw_args* args);
 
 /* Size of the fixed device scratch used by flce_fwd_bwd_noalloc (128 MiB). */

@@ -149,6 +149,16 @@ def test_workspace_sizes(lib):
     assert size(_dw(**big, dtype=0)) - plain >= 3 * 4096 * 1024 * 2       # fp32 dy: three bf16 terms
 
 
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+@pytest.mark.parametrize("N,K", [(256, 256), (1024, 4352), (1024, 4096), (2048, 2048), (4096, 4608), (520, 2008)])
+def test_dw_workspace_stays_within_the_header(lib, dtype, N, K):
+    """Parts of at most 75 tiles (152 SMs), 16 of 256 KB each, beside the copies of fp32 dy."""
+    for M in (1, 1000, 8192, 32768, 65536, 1 << 20, 1 << 24, 1 << 29):
+        size = lib.flce_ckpt8_dw_workspace_size(_dw(M=M, N=N, K=K, lddy=N, ldq=(K + 15) & ~15, lddW=K, dtype=dtype))
+        copy = 6 * ((M + 63) // 64 * 64) * N if dtype == 0 else 0
+        assert 0 < size - copy <= 300 * 2 ** 20 + 2048
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
     x, w = torch.randn(4, 8), torch.randn(8)
     for f in (lambda: flce.rmsnorm_fwd(x, w), lambda: flce.ckpt8_pack(x),
