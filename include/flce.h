@@ -441,8 +441,8 @@ FLCE_API int32_t flce_ckpt8_dw(const flce_ckpt8_dw_args* args, void* stream);
 /* Workspace bytes that flce_ckpt8_dw needs for these arguments (0 on invalid sizes or dtype);
  * the fields from workspace on are not looked at. Partial sums of output tiles: up to 16 parts
  * of 256 KB for fewer tiles than there are pairs of SMs: 300 MB at most on 152 SMs, reached with
- * very many rows (4096 x 4096 over 8192 rows: 15 MB). fp32 dy adds 6 bytes an element, and rows of dy or q that
- * do not start at multiples of 16 bytes a copy of that operand. Host-only. */
+ * very many rows (4096 x 4096 over 8192 rows: 15 MB). fp32 dy adds 6 bytes an element, and rows
+ * of dy or q that do not start at multiples of 16 bytes a copy of that operand. Host-only. */
 FLCE_API size_t flce_ckpt8_dw_workspace_size(const flce_ckpt8_dw_args* args);
 
 /* Size of the fixed device scratch used by flce_fwd_bwd_noalloc (128 MiB). */

@@ -126,6 +126,46 @@ def test_gradient_strides(dt, dE_dt, H, extra, offset):
     close(dE, want, (n[:, None] + 3) * F32 * mag + 2 * ULP[dE_dt] * np.abs(want) + FLOOR[dE_dt])
 
 
+@pytest.mark.parametrize("dt,dE_dt,H,extra,offset", [("bf16", "f32", 72, 5, 1), ("f16", "f16", 72, 8, 8), ("f16", "f16", 1003, 2, 3),
+                                                     ("bf16", "bf16", 7, 1, 3), ("f32", "f32", 20000, 4, 0),
+                                                     ("bf16", "bf16", 40000, 3, 1)])
+@pytest.mark.parametrize("N", [3, 700])
+def test_gradient_overwrites_a_table_with_a_pitch(dt, dE_dt, H, extra, offset, N):
+    """Every row of dE is written, and the elements between the rows stay as they were."""
+    g = torch.Generator().manual_seed(H + N)
+    V = 61
+    t = _tokens("skewed", N, V, g)
+    d = torch.randn(N, H, generator=g).to(DT[dt])
+    flat = torch.randn(V * (H + extra) + offset, generator=g).to(DT[dE_dt]).cuda()
+    keep = flat.clone()
+    view = lambda f: f[offset:].view(V, H + extra)  # noqa: E731
+    dE = view(flat)[:, :H]
+    dE.fill_(float("nan"))
+    flce.embed_bwd(t.cuda(), d.cuda(), dE=dE, ignore_index=IGN, flags=flce.FLAG_DW_OVERWRITE)
+    want, mag, n = oo.embed_bwd(t.numpy(), np64(d), V, 1.0, IGN)
+    close(dE, want, (n[:, None] + 3) * F32 * mag + 2 * ULP[dE_dt] * np.abs(want) + FLOOR[dE_dt])
+    assert torch.equal(view(flat)[:, H:], view(keep)[:, H:]) and torch.equal(flat[:offset], keep[:offset])
+
+
+@pytest.mark.parametrize("N", [5, 1000, 70000])
+def test_ignore_index_inside_the_vocabulary(N):
+    """The usual padding id: its rows are zero, its gradient is nothing, and it is in range."""
+    g = torch.Generator().manual_seed(N)
+    V, H, pad = 50, 24, 7
+    t = torch.randint(0, V, (N,), generator=g)
+    t[::2] = pad
+    E, d = torch.randn(V, H, generator=g), torch.randn(N, H, generator=g)
+    d[t == pad] = float("nan")
+    o = flce.embed_fwd(t.cuda(), E.cuda(), ignore_index=pad)
+    assert o["status_code"] == flce.FLCE_OK
+    assert np.array_equal(np64(o["out"]), oo.embed_fwd(t.numpy(), np64(E), 1.0, pad))
+    b = flce.embed_bwd(t.cuda(), d.cuda(), V=V, ignore_index=pad)
+    assert b["status_code"] == flce.FLCE_OK
+    want, mag, n = oo.embed_bwd(t.numpy(), np64(d), V, 1.0, pad)
+    assert n[pad] == 0
+    close(b["dE"], want, (n[:, None] + 3) * F32 * mag)
+
+
 def test_gradient_is_the_derivative_of_the_forward():
     """Central differences of L(E) = sum(c * embed(tokens, E)) in fp32: L is linear in E, so a
     difference over a step of 1 is exact up to the rounding of the two sums."""

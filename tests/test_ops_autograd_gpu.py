@@ -133,6 +133,48 @@ def test_linear_ckpt8(dt):
     _near([mine[1].grad], [ref[1].grad], 0.036 + plain)
 
 
+@pytest.mark.parametrize("scale", [1.0, 1e-6, 2e4])
+def test_linear_ckpt8_fp16(scale):
+    """fp16 activations from its subnormals to its largest. y and dx are a library's fp16 products
+    (1e-2, where the result is in fp16's range); dW's only other rounding is its own to fp16."""
+    g = torch.Generator().manual_seed(5)
+    x = (scale * torch.randn(210, 144, generator=g).clamp(-3.2, 3.2)).half().cuda()
+    W = (0.1 * torch.randn(88, 144, generator=g)).half().cuda()
+    mine, ref = [_leaf(v) for v in (x, W)], [_leaf(v.double()) for v in (x, W)]
+    y, want = torch_ops.linear_ckpt8(*mine), ref[0] @ ref[1].t()
+    c = torch.randn(y.shape, generator=g).half().cuda() * (1.0 if scale == 1.0 else 0.01 if scale > 1 else 1000.0)
+    y.backward(c)
+    want.backward(c.double())
+    if scale >= 1:
+        fits = want.abs() < 65000
+        assert fits.float().mean() > 0.95
+        _near([torch.where(fits, y, 0), mine[0].grad], [torch.where(fits, want, 0), ref[0].grad], 1e-2)
+    _near([mine[1].grad], [ref[1].grad], 0.036 + 1e-2)
+
+
+@pytest.mark.parametrize("name", ["embedding", "linear_ckpt8", "add_rms_norm"])
+def test_each_form_compiled_equals_eager(name):
+    g = torch.Generator().manual_seed(6)
+    t = torch.randint(0, 30, (64,), generator=g).cuda()
+    x, W, w = torch.randn(64, 128, generator=g), torch.randn(30, 128, generator=g), torch.randn(128, generator=g)
+
+    def f(x, W, w):
+        if name == "embedding":
+            return (torch_ops.embedding(t, W, scale=2.0) * x * w).sum()
+        if name == "linear_ckpt8":
+            return (torch_ops.linear_ckpt8(x * w, W) * 0.5).sum()
+        return (torch_ops.add_rms_norm(x + W.sum(0), w) * 2).sum()     # no residual, no checkpoint
+
+    out = []
+    for fn in (f, torch.compile(f, backend="aot_eager", fullgraph=True)):
+        a = [_leaf(v.cuda()) for v in (x, W, w)]
+        loss = fn(*a)
+        loss.backward()
+        out.append([loss] + [v.grad for v in a])
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+
+
 def test_compiled_equals_eager():
     x, r = torch.randn(64, 128, device="cuda"), torch.randn(64, 128, device="cuda")
     w = torch.randn(128, device="cuda")
