@@ -13,6 +13,7 @@ import torch
 from linear_cross_entropy_logits_gb300 import build as B
 from linear_cross_entropy_logits_gb300 import flce, torch_ops
 from oracle import ops_oracle as oo
+from ops_util import DT, F32, FLOOR, ULP, close
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 BAD, UNS, WS = flce.FLCE_ERR_INVALID_ARG, flce.FLCE_ERR_UNSUPPORTED, flce.FLCE_ERR_WORKSPACE
@@ -467,3 +468,102 @@ def test_embed_oracle_gradient_against_differences():
             d = np.zeros_like(E)
             d[v, j] = 1.0
             assert abs((L(E + d) - L(E - d)) / 2 - dE[v, j]) < 1e-12
+
+
+# ---- planted mistakes: the GPU tests' comparisons pass a right result in the type's rounding and
+# reject each of these
+
+def _rounded(a, dt):
+    return torch.from_numpy(np.asarray(a)).to(DT[dt])
+
+
+def _check(good, bad, check):
+    check(good)
+    for what, b in bad.items():
+        try:
+            check(b)
+        except AssertionError:
+            continue
+        pytest.fail(f"not rejected: {what}")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_planted_mistakes_in_the_norm(dt):
+    rng = np.random.default_rng(5)
+    N, H, off, eps = 40, 300, 0.25, 1e-5
+    # (values of the type, as the tests' inputs are)
+    r = lambda *s: _rounded(rng.standard_normal(s), dt).double().numpy()  # noqa: E731
+    h, dy, dh, w = r(N, H), r(N, H), r(N, H), r(H)
+    y, rstd = oo.rmsnorm_fwd(h, w, eps, off)
+    RSTD = 80 * F32
+    _check(_rounded(y, dt), {
+        "no offset": _rounded(oo.rmsnorm_fwd(h, w, eps, 0.0)[0], dt),
+        "one column short": _rounded(h * (w + off) / np.sqrt(np.mean(h[:, :-1] ** 2, axis=1) + eps)[:, None], dt),
+        "mean over the padded row": _rounded(h * (w + off) / np.sqrt((h * h).sum(axis=1) / 304 + eps)[:, None], dt),
+    }, lambda got: close(got, y, (ULP[dt] + RSTD) * np.abs(y) + FLOOR[dt]))
+    dx, dw, mag, wmag = oo.rmsnorm_bwd(dy, h, rstd, w, off, dh)
+    xh = h * rstd[:, None]
+    g = dy * (w + off)
+    _check(_rounded(dx, dt), {
+        "no mean": _rounded(rstd[:, None] * g + dh, dt),
+        "no offset": _rounded(oo.rmsnorm_bwd(dy, h, rstd, w, 0.0, dh)[0], dt),
+        "no residual gradient": _rounded(dx - dh, dt),
+        "rstd once": _rounded(g * rstd[:, None] - h * np.mean(g * xh, axis=1, keepdims=True) + dh, dt),
+    }, lambda got: close(got, dx, ULP[dt] * np.abs(dx) + F32 * mag + FLOOR[dt]))
+    _check(torch.from_numpy(dw).float(), {
+        "of the dx written in dy's place": torch.from_numpy((dx * xh).sum(axis=0)).float(),
+        "a row left out": torch.from_numpy((dy[:-1] * xh[:-1]).sum(axis=0)).float(),
+        "of h": torch.from_numpy((dy * h).sum(axis=0)).float(),
+    }, lambda got: close(got, dw, F32 * ((N + 8) * wmag + np.abs(dw))))
+
+
+def test_planted_mistakes_in_the_packing():
+    x = np.random.default_rng(6).standard_normal((30, 300))
+    q, s = oo.pack(x)
+
+    def check(qs):
+        assert np.array_equal(qs[0], q) and np.array_equal(qs[1], s)
+
+    half = np.clip(x / oo.spread(s / 2, 300), -448, 448)
+    _check((q.copy(), s.copy()), {
+        "a scale too small": (oo.round_e4m3(half), s / 2),
+        "a scale too large": (oo.round_e4m3(x / oo.spread(2 * s, 300)), 2 * s),
+        "truncated": (np.sign(q) * np.minimum(np.abs(q), oo.round_e4m3(np.abs(x) / oo.spread(s, 300) * (1 - 2.0 ** -5))), s),
+    }, check)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_planted_mistakes_in_the_embedding_gradient(dt):
+    rng = np.random.default_rng(7)
+    N, H, V, scale = 200, 24, 20, 1.5
+    t = rng.integers(0, V, N)
+    t[::9] = -100
+    d = _rounded(rng.standard_normal((N, H)), dt).double().numpy()
+    want, mag, n = oo.embed_bwd(t, d, V, scale, -100)
+    one = np.flatnonzero(t == t[1])[1]            # a token's second row
+    less, zero = t.copy(), t.copy()
+    less[one] = -100
+    zero[t == -100] = 0
+    of = lambda tt, sc=scale: _rounded(oo.embed_bwd(tt, d, V, sc, -100)[0], dt)  # noqa: E731
+    bound = (n[:, None] + 3) * F32 * mag + 2 * ULP[dt] * np.abs(want) + FLOOR[dt]
+    _check(of(t), {"a token's second row left out": of(less), "ignored rows counted": of(zero), "no scale": of(t, 1.0),
+                   "another token's row": of(np.where(np.arange(N) == one, (t + 1) % V, t))},
+           lambda got: close(got, want, bound))
+
+
+@pytest.mark.parametrize("wdt", ["f32", "bf16"])
+def test_planted_mistakes_in_the_weight_gradient(wdt):
+    rng = np.random.default_rng(8)
+    M, N, K = 130, 40, 300
+    dy = _rounded(rng.standard_normal((M, N)), "bf16").double().numpy()
+    q, s = oo.pack(rng.standard_normal((M, K)) * np.exp(rng.standard_normal((M, 1))))
+    x = q * oo.spread(s, K)
+    want = dy.T @ x
+    mag = np.abs(dy).T @ np.abs(x)
+    bound = M * 2.0 ** -23 * mag + 2 * ULP[wdt] * np.abs(want) + FLOOR[wdt]
+    next_block = q * oo.spread(np.roll(s, 1, axis=1), K)
+    late = q * oo.spread(np.roll(s, 1, axis=0), K)
+    _check(_rounded(want, wdt), {"a row left out": _rounded(dy[:-1].T @ x[:-1], wdt), "the neighbouring block's scale": _rounded(dy.T @ next_block, wdt),
+                                 "the neighbouring row's scale": _rounded(dy.T @ late, wdt), "no scale": _rounded(dy.T @ q, wdt),
+                                 "a step of rows twice": _rounded(want + dy[64:128].T @ x[64:128], wdt)},
+           lambda got: close(got, want, bound))
