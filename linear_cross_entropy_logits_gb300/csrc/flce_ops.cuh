@@ -204,17 +204,11 @@ __device__ __forceinline__ float2 q_unpack2(uint32_t u) {
 // EPV e4m3 values as they lie in memory.
 template <int EPV>
 struct RawQ {
-  static_assert(EPV == 16 || EPV == 8 || EPV == 4 || EPV == 2 || EPV == 1, "vector width");
+  static_assert(EPV == 8 || EPV == 4 || EPV == 2 || EPV == 1, "vector width");
   static constexpr int W = EPV < 4 ? 1 : EPV / 4;
   uint32_t w[W];
   __device__ __forceinline__ void load(const uint8_t* p) {
-    if constexpr (EPV == 16) {
-      const uint4 u = *(const uint4*)p;
-      w[0] = u.x;
-      w[1] = u.y;
-      w[2] = u.z;
-      w[3] = u.w;
-    } else if constexpr (EPV == 8) {
+    if constexpr (EPV == 8) {
       const uint2 u = *(const uint2*)p;
       w[0] = u.x;
       w[1] = u.y;
