@@ -410,6 +410,31 @@ def test_calls_in_a_graph():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(300, 72, 272), (3000, 75, 133)])
+def test_dw_scales_change_between_replays(dt, M, N, K):
+    """What the scales ask for is decided on the device: a captured call replayed on others."""
+    g = torch.Generator().manual_seed(14)
+    p = flce.ckpt8_pack(torch.randn(M, K, generator=g).cuda())
+    dy = torch.randn(M, N, generator=g).to(DT[dt]).cuda()
+    s = p["scale"].clone()
+    dW = torch.empty(N, K, device="cuda")
+    call = lambda w: flce.ckpt8_dw(dy, p["q"], s, dW=w, flags=flce.FLAG_DW_OVERWRITE, check=False)  # noqa: E731
+    call(dW)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(dW)
+    for f in (1.0, 2.0 ** 40, 1.1, 2.0 ** -60, 0.3, 1.0):
+        s.copy_(p["scale"] * f)
+        graph.replay()
+        got = dW.clone()
+        call(dW)
+        assert torch.equal(got, dW)
+        if dt == "f32" or f in (1.0, 2.0 ** 40, 2.0 ** -60):
+            assert rel_fro(np64(got), np64(dy).T @ (np64(p["q"]) * oo.spread(np64(s), K))) <= 1e-5
+
+
 def test_dw_status_word_in_the_workspace():
     """Without a status word of the caller's, flce_get_status reads the workspace's."""
     p = flce.ckpt8_pack(torch.randn(200, 128, device="cuda"))
