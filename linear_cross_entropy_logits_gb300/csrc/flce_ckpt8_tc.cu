@@ -27,8 +27,11 @@
 // 156). What bounds it is the expansion sharing shared memory and issue slots with the rest.
 // The tensor cores truncate when they add to an accumulator; over M rows that adds up to an
 // error of about M * 1.1e-9 relative (9e-6 at 8192 rows). So the accumulator is read out after
-// 2048 rows (1024 of a term of fp32 dy) and added, rounded to nearest, to fp32 sums in the registers of the
-// output warps (128 x 256 sums over 256 threads); the other accumulator is filled meanwhile.
+// 2048 rows and added, rounded to nearest, to fp32 sums in the registers of the output warps
+// (128 x 256 sums over 256 threads); the other accumulator is filled meanwhile. 8192 x 4096 x 4096:
+// bf16 6.8e-7 (every 1024 rows 3.1e-7, 208 us; every 512 1.6e-7, 220 us; a plain fp32 product
+// 3.7e-7). fp16 products have three bits more to lose, 1.8e-6 with 2048 rows: it takes 1024, 8.4e-7
+// (211 us, 206 with 2048; 512 rows 3.9e-7, 226 us; plain 7.9e-7), as do the terms of fp32 dy.
 //
 // Work split: whole tiles go round-robin over the pairs; the tiles of the last, partly filled
 // wave are split along m into S parts so that they fill the pairs. Parts are left as fp32 in
@@ -74,8 +77,8 @@ constexpr int THREADS = 128 + 32 * CONV_WARPS + 256;
 constexpr int SMEM = OFF_BARS + 512 + 1024;
 static_assert(SMEM <= 232448, "shared memory per CTA");
 static_assert(STAGES > SLOTS, "the expanding warps watch a stage's barrier for their slot");
-constexpr int SEG16 = 32;                 // steps per accumulator for 16-bit dy (2048 rows)
-constexpr int SEG32 = 16;                 // for fp32 dy (1024 rows of a term): half that error
+constexpr int SEG_BF16 = 32;              // steps per accumulator for bf16 dy (2048 rows)
+constexpr int SEG = 16;                   // for the others (1024 rows of a term)
 constexpr int MAX_SPLIT = 16;
 constexpr int SCAN_BLOCKS = 128;          // of k_scan_scales
 constexpr int SCAN_LOADS = 8;             // its threads' loads in flight
@@ -979,7 +982,7 @@ cudaError_t launch_dw_tc8(const DwArgs& a, int dt, int wdt, void* workspace, int
   p.mstep = pl.mstep;
   p.whole = pl.whole;
   p.S = pl.S;
-  p.seg = dt == FLCE_F32 ? SEG32 : SEG16;
+  p.seg = dt == FLCE_BF16 ? SEG_BF16 : SEG;
   p.part = (float*)(ws + pl.off_part);
   p.scan = (const uint32_t*)(ws + pl.off_scan);
   p.status = status;
