@@ -286,6 +286,30 @@ def test_dw_fp16_gradient_beside_blocks_of_zeros(K, extra, offset, one):
     assert rel_fro(np64(got), want) <= 1e-5
 
 
+@pytest.mark.parametrize("M,N,K,extra", [(1, 8, 260, 0), (47, 170, 171, 0), (700, 72, 272, 1), (4100, 40, 520, 0)])
+@pytest.mark.parametrize("most", [1, 5])
+def test_dw_fp16_gradient_beside_zeros_of_any_scale(M, N, K, extra, most):
+    """Blocks of zeros whose scales pass the others' by 2^10 to 2^60, most of the blocks or some; and
+    nothing but such blocks."""
+    g = torch.Generator().manual_seed(M)
+    nblk = (K + 127) // 128
+    p = flce.ckpt8_pack(torch.randn(M, K, generator=g).cuda())
+    zero = torch.randint(0, 6, (M, nblk), generator=g) < most
+    zero[0, 0] = False
+    p["q"].view(torch.int8)[zero.repeat_interleave(128, dim=1)[:, :K].cuda()] = 0
+    up = torch.exp2(torch.randint(10, 61, (M, nblk), generator=g).float())
+    s = p["scale"] * torch.where(zero, up, 1.0).cuda()
+    dy = (torch.randn(M, N, generator=g) * 0.3).half()
+    xs = np64(p["q"]) * oo.spread(np64(s), K)
+    want = np64(dy).T @ xs
+    got = flce.ckpt8_dw(dy.cuda(), strided(p["q"], extra, 0), s)["dW"]
+    close(got, want, _dw_bound(np64(dy), xs, M, "f16", "f32", want, 0 * want, False)
+          + 2.0 ** -39 * np.abs(xs).max() * np.abs(np64(dy)).sum(axis=0)[:, None])
+    p["q"].view(torch.int8).zero_()
+    got = flce.ckpt8_dw(dy.cuda(), strided(p["q"], extra, 0), 2.0 ** 60 * s)["dW"]
+    assert torch.all(got == 0)
+
+
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("bad", [float("inf"), float("nan")])
 def test_dw_scales_that_are_not_finite(dt, bad):
